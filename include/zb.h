@@ -564,6 +564,155 @@ zb_status zb_post_validated_adamw(int32_t P, const double* const* stage_state,
                                   void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* Mixture of experts: router, rows by expert, the experts' split passes     */
+/* ------------------------------------------------------------------------ */
+/* A pipeline stage whose MLP block is E expert blocks: each of T tokens goes
+ * to its k experts of largest router logit, and the stage's F, B and W run on
+ * the tokens of every expert at once.  The tokens' copies are rows, ordered by
+ * (expert, token); expert e owns rows offsets[e] .. offsets[e+1] - 1 of every
+ * row buffer.  The counts stay on the device: no call waits for them.
+ *
+ *   route    -> dispatch -> zb_moe_forward -> combine
+ *   combine_backward -> zb_moe_backward_input -> combine (gates NULL: dX)
+ *                    -> zb_moe_backward_weight (deferrable) ; route_backward
+ *
+ * Row buffers hold `rows` rows (T k, or any bound on offsets[E]); those at and
+ * past offsets[E] are neither read (their values change nothing) nor written.
+ * `offsets` is E + 1 ascending int32 on the device, from 0 to at most rows
+ * (others give unspecified results, but no access leaves the buffers).  rows
+ * and tokens may be 0 (row buffers may then be NULL). */
+
+/* 1 <= topk <= experts <= 256, topk <= 32, 0 <= tokens, tokens topk <= 2^30. */
+typedef struct zb_router {
+    int64_t tokens;   /* T                                                     */
+    int32_t experts;  /* E                                                     */
+    int32_t topk;     /* k                                                     */
+    int32_t dtype;    /* zb_dtype of the logits (and of dlogits)               */
+    int32_t renorm;   /* 0: gates are the softmax over all E logits;
+                         1: the softmax over the chosen k                      */
+} zb_router;
+
+/* Choose the k largest logits of every row z[t, :] ([T, E]; ties go to the
+ * lowest index) and order the rows.
+ *   gates[T,k]     fp32, in descending order of the logits;
+ *   expert[T,k]    int32, the chosen experts, -1 where fewer than k are left;
+ *   offsets[E+1]   int32, first row of each expert; offsets[E] = rows in use;
+ *   row_of[T,k]    int32, the row of each choice (-1: none);
+ *   token_of[T k]  int32, the token of each row (-1 at and past offsets[E]).
+ * A logit of -inf is never chosen and has no weight: a row of them (a padding
+ * token) gets no rows and gates of 0.  A NaN ranks below every number and is
+ * chosen only when nothing else is left; a row with a NaN or +inf gets NaN
+ * gates.  Whole results do not depend on timing; rows of an expert are in
+ * ascending token order.  Workspace: zb_moe_route_workspace_bytes, 16-byte
+ * aligned. */
+size_t zb_moe_route_workspace_bytes(const zb_router* r);
+zb_status zb_moe_route(const zb_router* r, const void* logits, float* gates, int32_t* expert,
+                       int32_t* offsets, int32_t* row_of, int32_t* token_of, void* workspace,
+                       size_t ws_bytes, void* stream);
+
+/* Gradient of the gates to the logits, dlogits[T,E] in r->dtype (overwritten):
+ *   renorm 0: dz_i = [i chosen] g_i dg_i - p_i sum_j g_j dg_j, p = softmax(z);
+ *   renorm 1: dz_i = g_i (dg_i - sum_j g_j dg_j) where chosen, else 0.
+ * `logits` is read for renorm 0 only (else may be NULL).  Choices of -1 and
+ * logits of -inf get no gradient. */
+zb_status zb_moe_route_backward(const zb_router* r, const void* logits, const int32_t* expert,
+                                const float* gates, const float* dgates, void* dlogits, void* stream);
+
+/* Xp[row_of[t,j], :] = X[t, :] (bf16, `width` a multiple of 8).  The gradient
+ * of dispatch is combine with gates NULL.  Entries of row_of outside
+ * [0, tokens topk) are skipped, here and below. */
+zb_status zb_moe_dispatch(int64_t tokens, int32_t topk, int64_t width, const void* X,
+                          const int32_t* row_of, void* Xp, void* stream);
+
+/* Y[t, :] = sum_j gates[t,j] Yp[row_of[t,j], :], j ascending, summed in fp32
+ * (gates NULL: all 1; a token without rows gets zeros). */
+zb_status zb_moe_combine(int64_t tokens, int32_t topk, int64_t width, const void* Yp,
+                         const int32_t* row_of, const float* gates, void* Y, void* stream);
+
+/* dYp[row_of[t,j], :] = gates[t,j] dY[t, :] and dgates[t,j] = <dY[t,:],
+ * Yp[row_of[t,j],:]> (fp32; 0 where there is no row). */
+zb_status zb_moe_combine_backward(int64_t tokens, int32_t topk, int64_t width, const void* dY,
+                                  const void* Yp, const int32_t* row_of, const float* gates, void* dYp,
+                                  float* dgates, void* stream);
+
+/* E expert blocks of zb_block's mathematics on the rows of each.  Weights are
+ * W1[E,h,f], W2[E,f,h], b1[E,f], b2[E,h] in bf16, gradients the same shapes in
+ * fp32; X, Y, dY, dX are [rows,h] and H, A, dH [rows,f] in bf16.  h and f are
+ * multiples of 8, 1 <= experts <= 256, 0 <= rows <= 2^30.  ZB_ACT_NONE: the
+ * single linear map Y_e = X_e W1[e] with Y, dY [rows,f] (W2, H, A, dH unused). */
+typedef struct zb_moe {
+    int64_t rows, h, f;
+    int32_t experts;
+    int32_t act;       /* zb_act                                               */
+    int32_t has_bias;
+    int32_t flags;     /* must be 0                                            */
+} zb_moe;
+
+/* F, B and W of the experts, as zb_forward, zb_backward_input and
+ * zb_backward_weight with one weight per expert.  An expert without rows is
+ * not read in F and B; in W it gets zeros (accumulate = 0) or keeps what it
+ * has (accumulate = 1).  W needs zb_moe_workspace_bytes of device memory,
+ * 256-byte aligned, until its work on the stream has ended.  The sums over an
+ * expert's rows have a fixed order: the same inputs give the same bits. */
+zb_status zb_moe_forward(const zb_moe* m, const int32_t* offsets, const void* X, const void* W1,
+                         const void* W2, const void* b1, const void* b2, void* H_save, void* A_save,
+                         void* Y, void* stream);
+zb_status zb_moe_backward_input(const zb_moe* m, const int32_t* offsets, const void* dY, const void* W1,
+                                const void* W2, const void* H_save, void* dH_out, void* dX, void* stream);
+size_t zb_moe_workspace_bytes(const zb_moe* m);
+zb_status zb_moe_backward_weight(const zb_moe* m, const int32_t* offsets, const void* X,
+                                 const void* A_save, const void* dH, const void* dY, float* dW1,
+                                 float* dW2, float* db1, float* db2, int accumulate, void* workspace,
+                                 size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Products in 8-bit floating point with a scale for each block of 128        */
+/* ------------------------------------------------------------------------ */
+/* Values are e4m3 (4 exponent, 3 mantissa bits, largest 448) with one fp32
+ * scale for each 128 consecutive elements of a row of X (a 1 x 128 block) and
+ * for each 128 x 128 block of W: x = scale * q.  The quantisers take as scale
+ * the least power of two s with amax / s <= 448 (at least 2^-126; 1 for a
+ * block of zeros), so that x / s is exact and the only rounding is e4m3's own
+ * (to nearest, ties to even); the product takes any fp32 scales.  A block with
+ * a NaN or an infinity gets the scale NaN, so that what it touches is NaN.  A
+ * last block may be narrower than 128. */
+
+/* X[rows,cols] bf16 -> Q[rows,cols] e4m3 and S[rows, ceil(cols/128)].  cols is
+ * a multiple of 16. */
+zb_status zb_fp8_quantize_rows(int64_t rows, int64_t cols, const void* X, void* Q, float* S, void* stream);
+
+/* W[experts,rows,cols] bf16 in blocks of 128 x 128: Q[experts,rows,cols] with
+ * S[experts, ceil(rows/128), ceil(cols/128)], and its transpose
+ * QT[experts,cols,rows] with ST (the transposed scales), the operands of
+ * dX = dY W^T and of Y = X W.  Either pair may be NULL.  rows and cols are
+ * multiples of 16. */
+zb_status zb_fp8_quantize_weight(int32_t experts, int64_t rows, int64_t cols, const void* W, void* Q,
+                                 float* S, void* QT, float* ST, void* stream);
+
+typedef enum zb_fp8_epilogue {
+    ZB_FP8_STORE = 0,     /* out0 = D (+ bias)                                  */
+    ZB_FP8_GELU = 1,      /* out0 = H = D (+ bias), out1 = GeLU(H)              */
+    ZB_FP8_GELU_GRAD = 2  /* out0 = D * GeLU'(H)                                */
+} zb_fp8_epilogue;
+
+/* D[M,N] = X W_e^T by expert: row r of expert e has
+ *   D[r,n] = sum_b xs[r,b] ws[e,n/128,b] sum_{k in block b} xq[r,k] wq[e,n,k]
+ * with xq[M,K], xs[M,ceil(K/128)], wq[E,N,K], ws[E,ceil(N/128),ceil(K/128)].
+ * offsets as above, or NULL when experts = 1 (every row).  K a multiple of 16,
+ * N of 8; 0 <= M <= 2^30, 1 <= experts <= 256.  H and the outputs are bf16
+ * [M,N], bias bf16 [E,N] (NULL: none; not with ZB_FP8_GELU_GRAD). */
+typedef struct zb_fp8_gemm {
+    int64_t M, N, K;
+    int32_t experts;
+    int32_t epilogue;  /* zb_fp8_epilogue                                      */
+    int32_t act;       /* ZB_ACT_GELU_ERF or ZB_ACT_GELU_TANH (GeLU epilogues) */
+    int32_t reserved;  /* must be 0                                            */
+} zb_fp8_gemm;
+zb_status zb_fp8_matmul(const zb_fp8_gemm* g, const int32_t* offsets, const void* Xq, const float* xs,
+                        const void* Wq, const float* ws, const void* bias, const void* H, void* out0,
+                        void* out1, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Status                                                                   */
 /* ------------------------------------------------------------------------ */
 

@@ -39,6 +39,7 @@ ZB_DT_BF16 = 1
 ZB_ACT_NONE = 0
 ZB_ACT_GELU_ERF = 1
 ZB_ACT_GELU_TANH = 2
+ZB_FP8_STORE, ZB_FP8_GELU, ZB_FP8_GELU_GRAD = range(3)
 ZB_BLOCK_NO_SPLIT_K = 1  # zb_block.flags: single passes never split K
 
 ZB_OP_F, ZB_OP_B, ZB_OP_W, ZB_OP_BW, ZB_OP_OPT = range(5)
@@ -108,6 +109,21 @@ class zb_stage_decision(C.Structure):
                 ("skip_global", C.c_int32), ("rolled_back", C.c_int32), ("reserved", C.c_int32)]
 
 
+class zb_router(C.Structure):
+    _fields_ = [("tokens", C.c_int64), ("experts", C.c_int32), ("topk", C.c_int32), ("dtype", C.c_int32),
+                ("renorm", C.c_int32)]
+
+
+class zb_moe(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("h", C.c_int64), ("f", C.c_int64), ("experts", C.c_int32),
+                ("act", C.c_int32), ("has_bias", C.c_int32), ("flags", C.c_int32)]
+
+
+class zb_fp8_gemm(C.Structure):
+    _fields_ = [("M", C.c_int64), ("N", C.c_int64), ("K", C.c_int64), ("experts", C.c_int32),
+                ("epilogue", C.c_int32), ("act", C.c_int32), ("reserved", C.c_int32)]
+
+
 class ZBError(RuntimeError):
     def __init__(self, status: int, where: str, msg: str):
         super().__init__(f"{where}: {STATUS_NAMES.get(status, status)}: {msg}")
@@ -151,6 +167,17 @@ def _load():
         "zb_sync_status": [vp],
         "zb_post_validated_adamw": [C.c_int32, C.POINTER(vp), C.POINTER(zb_opt_tensor), C.c_int32,
                                     C.POINTER(zb_adamw_params), vp, vp],
+        "zb_moe_route": [C.POINTER(zb_router), vp, vp, vp, vp, vp, vp, vp, sz, vp],
+        "zb_moe_route_backward": [C.POINTER(zb_router), vp, vp, vp, vp, vp, vp],
+        "zb_moe_dispatch": [C.c_int64, C.c_int32, C.c_int64, vp, vp, vp, vp],
+        "zb_moe_combine": [C.c_int64, C.c_int32, C.c_int64, vp, vp, vp, vp, vp],
+        "zb_moe_combine_backward": [C.c_int64, C.c_int32, C.c_int64, vp, vp, vp, vp, vp, vp, vp],
+        "zb_moe_forward": [C.POINTER(zb_moe)] + [vp] * 10,
+        "zb_moe_backward_input": [C.POINTER(zb_moe)] + [vp] * 8,
+        "zb_moe_backward_weight": [C.POINTER(zb_moe)] + [vp] * 9 + [C.c_int, vp, sz, vp],
+        "zb_fp8_quantize_rows": [C.c_int64, C.c_int64, vp, vp, vp, vp],
+        "zb_fp8_quantize_weight": [C.c_int32, C.c_int64, C.c_int64, vp, vp, vp, vp, vp, vp],
+        "zb_fp8_matmul": [C.POINTER(zb_fp8_gemm)] + [vp] * 10,
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -160,6 +187,9 @@ def _load():
     lib.zb_last_error.restype = C.c_char_p
     lib.zb_grad_stats_scratch_bytes.argtypes = []
     lib.zb_grad_stats_scratch_bytes.restype = C.c_size_t
+    for name, desc in (("zb_moe_route_workspace_bytes", zb_router), ("zb_moe_workspace_bytes", zb_moe)):
+        getattr(lib, name).argtypes = [C.POINTER(desc)]
+        getattr(lib, name).restype = C.c_size_t
     lib.zb_version.argtypes = []
     lib.zb_version.restype = C.c_char_p
     return lib
@@ -451,6 +481,91 @@ def zb_run_stage_schedule_static(pl, stages, X0, dY_last, dX0_out, Y_last_out, o
                                             _ptr_array(dX0_out), _ptr_array(Y_last_out), arr,
                                             len(arr), st_ptr, _stream(stream)),
            "zb_run_stage_schedule_static")
+
+
+# ---------------------------------------------------------------- experts
+def make_router(tokens: int, experts: int, topk: int, dtype: int = ZB_DT_F32, renorm: bool = False) -> zb_router:
+    return zb_router(tokens, experts, topk, dtype, 1 if renorm else 0)
+
+
+def zb_moe_route_workspace_bytes(router) -> int:
+    return LIB.zb_moe_route_workspace_bytes(C.byref(router))
+
+
+def zb_moe_route(router, logits, gates, expert, offsets, row_of, token_of, workspace, ws_bytes, stream=None):
+    """Top-k gates and experts of every token, and the rows ordered by expert."""
+    _check(LIB.zb_moe_route(C.byref(router), _ptr(logits), _ptr(gates), _ptr(expert), _ptr(offsets),
+                            _ptr(row_of), _ptr(token_of), _ptr(workspace), ws_bytes, _stream(stream)),
+           "zb_moe_route")
+
+
+def zb_moe_route_backward(router, logits, expert, gates, dgates, dlogits, stream=None):
+    _check(LIB.zb_moe_route_backward(C.byref(router), _ptr(logits), _ptr(expert), _ptr(gates), _ptr(dgates),
+                                     _ptr(dlogits), _stream(stream)), "zb_moe_route_backward")
+
+
+def zb_moe_dispatch(tokens: int, topk: int, width: int, X, row_of, Xp, stream=None):
+    _check(LIB.zb_moe_dispatch(tokens, topk, width, _ptr(X), _ptr(row_of), _ptr(Xp), _stream(stream)),
+           "zb_moe_dispatch")
+
+
+def zb_moe_combine(tokens: int, topk: int, width: int, Yp, row_of, gates, Y, stream=None):
+    """Weighted sums over each token's rows (gates None: plain sums, dispatch's gradient)."""
+    _check(LIB.zb_moe_combine(tokens, topk, width, _ptr(Yp), _ptr(row_of), _ptr(gates), _ptr(Y),
+                              _stream(stream)), "zb_moe_combine")
+
+
+def zb_moe_combine_backward(tokens: int, topk: int, width: int, dY, Yp, row_of, gates, dYp, dgates, stream=None):
+    _check(LIB.zb_moe_combine_backward(tokens, topk, width, _ptr(dY), _ptr(Yp), _ptr(row_of), _ptr(gates),
+                                       _ptr(dYp), _ptr(dgates), _stream(stream)), "zb_moe_combine_backward")
+
+
+def make_moe(rows: int, h: int, f: int, experts: int, act: int = ZB_ACT_GELU_ERF, has_bias: bool = False) -> zb_moe:
+    return zb_moe(rows, h, f, experts, act, 1 if has_bias else 0, 0)
+
+
+def zb_moe_forward(moe, offsets, X, W1, W2, b1, b2, H_save, A_save, Y, stream=None):
+    _check(LIB.zb_moe_forward(C.byref(moe), _ptr(offsets), _ptr(X), _ptr(W1), _ptr(W2), _ptr(b1), _ptr(b2),
+                              _ptr(H_save), _ptr(A_save), _ptr(Y), _stream(stream)), "zb_moe_forward")
+
+
+def zb_moe_backward_input(moe, offsets, dY, W1, W2, H_save, dH_out, dX, stream=None):
+    _check(LIB.zb_moe_backward_input(C.byref(moe), _ptr(offsets), _ptr(dY), _ptr(W1), _ptr(W2), _ptr(H_save),
+                                     _ptr(dH_out), _ptr(dX), _stream(stream)), "zb_moe_backward_input")
+
+
+def zb_moe_workspace_bytes(moe) -> int:
+    return LIB.zb_moe_workspace_bytes(C.byref(moe))
+
+
+def zb_moe_backward_weight(moe, offsets, X, A_save, dH, dY, dW1, dW2, db1, db2, accumulate, workspace, ws_bytes,
+                           stream=None):
+    _check(LIB.zb_moe_backward_weight(C.byref(moe), _ptr(offsets), _ptr(X), _ptr(A_save), _ptr(dH), _ptr(dY),
+                                      _ptr(dW1), _ptr(dW2), _ptr(db1), _ptr(db2), 1 if accumulate else 0,
+                                      _ptr(workspace), ws_bytes, _stream(stream)), "zb_moe_backward_weight")
+
+
+# ---------------------------------------------------------------- 8 bits
+def zb_fp8_quantize_rows(rows: int, cols: int, X, Q, S, stream=None):
+    """e4m3 values with a power-of-two scale for each 1 x 128 block."""
+    _check(LIB.zb_fp8_quantize_rows(rows, cols, _ptr(X), _ptr(Q), _ptr(S), _stream(stream)),
+           "zb_fp8_quantize_rows")
+
+
+def zb_fp8_quantize_weight(experts: int, rows: int, cols: int, W, Q, S, QT, ST, stream=None):
+    """e4m3 weight and its transpose with a power-of-two scale for each 128 x 128 block."""
+    _check(LIB.zb_fp8_quantize_weight(experts, rows, cols, _ptr(W), _ptr(Q), _ptr(S), _ptr(QT), _ptr(ST),
+                                      _stream(stream)), "zb_fp8_quantize_weight")
+
+
+def make_fp8_matmul(M: int, N: int, K: int, experts: int = 1, epilogue: int = ZB_FP8_STORE,
+                    act: int = ZB_ACT_GELU_ERF) -> zb_fp8_gemm:
+    return zb_fp8_gemm(M, N, K, experts, epilogue, act, 0)
+
+
+def zb_fp8_matmul(g, offsets, Xq, xs, Wq, ws, H, out0, out1, bias=None, stream=None):
+    _check(LIB.zb_fp8_matmul(C.byref(g), _ptr(offsets), _ptr(Xq), _ptr(xs), _ptr(Wq), _ptr(ws), _ptr(bias),
+                             _ptr(H), _ptr(out0), _ptr(out1), _stream(stream)), "zb_fp8_matmul")
 
 
 def zb_sync_status(stream=None):
