@@ -3,6 +3,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <atomic>
 #include <string>
 
 #include "gemm_core.cuh"
@@ -10,7 +12,7 @@
 namespace {
 
 constexpr int MAX_EXPERTS = 256;
-constexpr int TM = 64, TN = 64, TK = 16;
+constexpr int MAX_TOK = 32;  // tokens of one epilogue chunk
 
 // Rows [lo, hi) of expert e, kept inside [0, rows] whatever the offsets say.
 __device__ __forceinline__ void expert_rows(const int* offsets, int e, int rows, int& lo, int& hi) {
@@ -18,89 +20,783 @@ __device__ __forceinline__ void expert_rows(const int* offsets, int e, int rows,
     hi = max(min(offsets[e + 1], rows), lo);
 }
 
-struct SimpleArgs {
-    const __nv_bfloat16* A;   // [rows, K]
-    const __nv_bfloat16* W;   // element (k, n) of expert e at e * K * N + k * sk + n * sn
-    long long sk, sn;
-    const __nv_bfloat16* bias;  // [E, N]
-    const __nv_bfloat16* aux;   // [rows, N]
-    __nv_bfloat16 *out0, *out1;
-    const int* offsets;
-    int rows, N, K, epi, act;
+// ---------------------------------------------------------------- F and B
+// D[row, n] = sum_k A[row, k] W_e(k, n) for the rows of every expert e, as the
+// transposed product D^T = W_e^T A^T: the weights' columns are the MMA's M side
+// (128 for one CTA, 256 for a pair: always full but for the matrix edge) and
+// an expert's rows its N side, whose extent is any multiple of 16 (32 for a
+// pair) chosen per tile.  So a ragged expert costs its own rows rounded up to
+// 16 or 32, not to 128 or 256, and one row (a decoding step) costs little more
+// than streaming the weights.  The roles, the ring and the two accumulators
+// are those of the dense kernel (gemm_tc.cu): warp 0 copies, warp 1 issues
+// MMAs, warps 2-9 drain.  Tiles are walked in a fixed order; every role walks
+// the experts' offsets (in shared memory) by itself.
+//
+// Epilogue: a TMEM lane is a column n of D and a TMEM column a row of D, so a
+// chunk of 32 lanes x 32 columns is read as 8 x 8 fragments (16x256b loads),
+// rounded to bf16 pairs of rows and transposed on its way to the staging box
+// by stmatrix; H (for GeLU') comes the same way back, by TMA and ldmatrix.  A
+// box of 32 rows leaves by a TMA store; the last, partial box of an expert by
+// plain stores of its live rows, since the rows after it are another expert's.
+template <int CG>
+struct RowsCfg {
+    static constexpr int TILE_F = 128 * CG;   // columns of D per tile
+    static constexpr int TILE_T = 128 * CG;   // rows of D per tile, at most
+    static constexpr int N_STEP = 16 * CG;    // granularity of the MMA's N
+    static constexpr uint32_t STAGE = 32 * 1024;  // 16 KiB of weights, 16 KiB of rows
+    static constexpr uint32_t TMEM = 2 * TILE_T;
+};
+template <int EPI>
+struct RowsEpi {
+    static constexpr int STAGES = EPI == zb::EPI_GELU_BWD ? 5 : 6;
+    static constexpr int BOXES = EPI == zb::EPI_GELU_BWD ? 4 : 2;  // staging boxes per warp
+};
+constexpr uint32_t ROW_BOX = 32 * 64;  // 32 rows x 32 columns of bf16
+constexpr int EPI_WARPS = 8;
+
+struct RowsCtl {
+    uint64_t full[6], empty[6], tfull[2], tempty[2], drain;
+    uint64_t hbar[EPI_WARPS][4];  // H boxes
+    uint32_t tmem_base;
+    int abort_flag;
+    int off[MAX_EXPERTS + 1];  // legal, ascending
 };
 
-__device__ __forceinline__ float gelu_of(float x, int act) {
-    return act == ZB_ACT_GELU_TANH ? gelu_t<true>(x) : gelu_t<false>(x);
+template <int EPI>
+constexpr size_t rows_smem() {
+    return 1024 + RowsEpi<EPI>::STAGES * RowsCfg<1>::STAGE + EPI_WARPS * RowsEpi<EPI>::BOXES * ROW_BOX + sizeof(RowsCtl);
 }
-__device__ __forceinline__ float gelu_grad_of(float x, int act) {
-    return act == ZB_ACT_GELU_TANH ? gelu_grad_t<true>(x) : gelu_grad_t<false>(x);
+static_assert(rows_smem<zb::EPI_GELU_BWD>() <= 232448 && rows_smem<zb::EPI_GELU_DUAL>() <= 232448, "shared memory");
+
+struct RowsArgs {
+    const int* offsets;
+    const __nv_bfloat16* bias;  // [E, N] or nullptr
+    __nv_bfloat16 *out0, *out1;
+    int rows, experts, N, K, act;
+    unsigned int* err;
+};
+
+// A role's walk over the tiles: tile t of the launch is tile `local` of expert
+// e, which has nt tiles of `tr` rows (the last one fewer) x tiles_f of columns.
+template <int TILE_T>
+struct Walk {
+    const int* off;
+    int experts, tiles_f;
+    int e, first, nt, tr;
+    __device__ Walk(const int* off_, int experts_, int tiles_f_)
+        : off(off_), experts(experts_), tiles_f(tiles_f_), e(-1), first(0), nt(0), tr(0) {}
+    // Moves to tile t (ascending calls); false past the last one.
+    __device__ __forceinline__ bool to(int t, int& row0, int& nrows, int& fb) {
+        while (t >= first + nt * tiles_f) {
+            first += nt * tiles_f;
+            if (++e >= experts) return false;
+            const int n = off[e + 1] - off[e];
+            nt = (n + TILE_T - 1) / TILE_T;
+            tr = nt ? ((n + nt - 1) / nt + 31) / 32 * 32 : 0;
+        }
+        int tb;
+        tile_coords(t - first, nt, tiles_f, 16, tb, fb);
+        row0 = off[e] + tb * tr;
+        nrows = min(tr, off[e + 1] - row0);
+        return true;
+    }
+};
+
+// off[0..experts] in shared memory from the caller's offsets, made legal:
+// inside [0, rows] and ascending (a running maximum, 32 at a time).
+__device__ __forceinline__ void load_offsets(int* off, const int* offsets, int experts, int rows) {
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        int carry = 0;
+        for (int i0 = 0; i0 <= experts; i0 += 32) {
+            const int i = i0 + lane;
+            int v = max(carry, i <= experts ? min(max(offsets[i], 0), rows) : 0);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v = max(v, u);
+            }
+            if (i <= experts) off[i] = v;
+            carry = __shfl_sync(0xffffffffu, v, 31);
+        }
+    }
+    __syncthreads();
 }
 
-__global__ void __launch_bounds__(256) zb_moe_rows_simple_kernel(const SimpleArgs a) {
-    __shared__ float As[TK][TM + 4], Bs[TK][TN + 4];
-    int lo, hi;
-    expert_rows(a.offsets, blockIdx.y, a.rows, lo, hi);
-    const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
-    const int n0 = blockIdx.x * TN;
-    const __nv_bfloat16* W = a.W + static_cast<long long>(blockIdx.y) * a.K * a.N;
-    for (int m0 = lo + blockIdx.z * TM; m0 < hi; m0 += gridDim.z * TM) {
-        float acc[4][4] = {};
-        for (int k0 = 0; k0 < a.K; k0 += TK) {
-            for (int i = tid; i < TK * TM; i += 256) {
-                const int m = m0 + i / TK, k = k0 + i % TK;
-                As[i % TK][i / TK] = m < hi && k < a.K ? __bfloat162float(a.A[static_cast<long long>(m) * a.K + k]) : 0.0f;
-                const int n = n0 + i % TN, kb = k0 + i / TN;
-                Bs[i / TN][i % TN] = n < a.N && kb < a.K ? __bfloat162float(W[kb * a.sk + n * a.sn]) : 0.0f;
-            }
-            __syncthreads();
-            for (int k = 0; k < TK; ++k)
-                for (int i = 0; i < 4; ++i)
-                    for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(As[k][ty * 4 + i], Bs[k][tx * 4 + j], acc[i][j]);
-            __syncthreads();
+template <int EPI, int A_MN, int CG>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    zb_moe_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA128,
+                       const __grid_constant__ CUtensorMap tmA32, const __grid_constant__ CUtensorMap tmO0,
+                       const __grid_constant__ CUtensorMap tmO1, const RowsArgs args) {
+    using C = RowsCfg<CG>;
+    constexpr bool PAIR = CG == 2;
+    constexpr int STAGES = RowsEpi<EPI>::STAGES;
+    constexpr int BOXES = RowsEpi<EPI>::BOXES;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t* staging = smem + STAGES * C::STAGE;
+    RowsCtl* ctl = reinterpret_cast<RowsCtl*>(staging + EPI_WARPS * BOXES * ROW_BOX);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = PAIR ? zbp::cluster_ctarank() : 0u;
+    const bool leader = rank == 0;
+    const int cluster = blockIdx.x / CG, clusters = gridDim.x / CG;
+    const int tiles_f = (args.N + C::TILE_F - 1) / C::TILE_F;
+    const int num_kb = (args.K + BK - 1) / BK;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            zbp::mbar_init(zbp::smem_u32(&ctl->full[s]), 1);
+            zbp::mbar_init(zbp::smem_u32(&ctl->empty[s]), 1);
         }
-        for (int i = 0; i < 4; ++i)
-            for (int j = 0; j < 4; ++j) {
-                const int m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-                if (m >= hi || n >= a.N) continue;
-                const long long at = static_cast<long long>(m) * a.N + n;
-                float x = acc[i][j];
-                if (a.bias) x += __bfloat162float(a.bias[static_cast<long long>(blockIdx.y) * a.N + n]);
-                if (a.epi == zb::EPI_GELU_BWD) x *= gelu_grad_of(__bfloat162float(a.aux[at]), a.act);
-                a.out0[at] = __float2bfloat16_rn(x);
-                if (a.epi == zb::EPI_GELU_DUAL) a.out1[at] = __float2bfloat16_rn(gelu_of(x, a.act));
+        for (int b = 0; b < 2; ++b) {
+            zbp::mbar_init(zbp::smem_u32(&ctl->tfull[b]), 1);
+            zbp::mbar_init(zbp::smem_u32(&ctl->tempty[b]), EPI_WARPS * CG);
+        }
+        zbp::mbar_init(zbp::smem_u32(&ctl->drain), 1);
+        if (EPI == zb::EPI_GELU_BWD)
+            for (int w = 0; w < EPI_WARPS; ++w)
+                for (int b = 0; b < 4; ++b) zbp::mbar_init(zbp::smem_u32(&ctl->hbar[w][b]), 1);
+        ctl->abort_flag = 0;
+        zbp::fence_mbar_init();
+        zbp::tma_prefetch_desc(&tmW);
+        zbp::tma_prefetch_desc(&tmA128);
+        zbp::tma_prefetch_desc(&tmA32);
+        zbp::tma_prefetch_desc(&tmO0);
+        if (EPI != zb::EPI_STORE_BF16) zbp::tma_prefetch_desc(&tmO1);
+    }
+    if (warp == 1) {
+        if (PAIR) {
+            zbp::tmem_alloc_pair(zbp::smem_u32(&ctl->tmem_base), C::TMEM);
+            zbp::tmem_relinquish_pair();
+        } else {
+            zbp::tmem_alloc(zbp::smem_u32(&ctl->tmem_base), C::TMEM);
+            zbp::tmem_relinquish();
+        }
+    }
+    zbp::tc_fence_before();
+    __syncthreads();
+    if (PAIR) zbp::cluster_sync();
+    zbp::tc_fence_after();
+    const uint32_t tmem_base = ctl->tmem_base;
+    volatile int* abort_flag = &ctl->abort_flag;
+    zbp::grid_dependency_wait();
+    zbp::allow_dependent_launch();
+    load_offsets(ctl->off, args.offsets, args.experts, args.rows);
+
+    Walk<C::TILE_T> walk(ctl->off, args.experts, tiles_f);
+    int row0 = 0, nrows = 0, fb = 0;
+    if (warp == 0) {
+        if (lane == 0) {
+            // ------------------------------------------------ TMA producer
+            uint32_t it = 0;
+            bool ok = true;
+            for (int tile = cluster; ok && walk.to(tile, row0, nrows, fb); tile += clusters) {
+                const int f0 = fb * C::TILE_F + static_cast<int>(rank) * 128;
+                const int mma_n = (nrows + C::N_STEP - 1) / C::N_STEP * C::N_STEP;
+                const int half = mma_n / CG;  // rows in this CTA
+                const int r0 = row0 + static_cast<int>(rank) * half;
+                const int boxes = (half + 31) / 32;
+                const uint32_t bytes = CG * (A_BYTES + static_cast<uint32_t>(boxes) * 32u * BK * 2u);
+                for (int kb = 0; kb < num_kb; ++kb, ++it) {
+                    const uint32_t s = it % STAGES, r = it / STAGES;
+                    if (!wait_bar<PAIR>(zbp::smem_u32(&ctl->empty[s]), (r & 1u) ^ 1u, abort_flag, args.err,
+                                        ERR_WAIT_PRODUCER, WAIT_LIMIT_NS, true)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t full_local = zbp::smem_u32(&ctl->full[s]);
+                    const uint32_t full = PAIR ? zbp::mapa_shared(full_local, 0) : full_local;
+                    const uint32_t sa = zbp::smem_u32(smem + s * C::STAGE);
+                    const uint32_t sb = sa + A_BYTES;
+                    const int k0 = kb * BK;
+                    if (leader) zbp::mbar_arrive_expect_tx(full_local, bytes);
+                    auto load_w = [&](uint32_t dst, int x, int y) {
+                        if (PAIR)
+                            zbp::tma_load_3d_pair(dst, &tmW, full, x, y, walk.e);
+                        else
+                            zbp::tma_load_3d(dst, &tmW, full, x, y, walk.e);
+                    };
+                    auto load_a = [&](uint32_t dst, const CUtensorMap* tm, int y) {
+                        if (PAIR)
+                            zbp::tma_load_2d_pair(dst, tm, full, k0, y);
+                        else
+                            zbp::tma_load_2d(dst, tm, full, k0, y);
+                    };
+                    if (A_MN) {
+                        load_w(sa, f0, k0);
+                        load_w(sa + MN_ATOM_BYTES, f0 + 64, k0);
+                    } else {
+                        load_w(sa, k0, f0);
+                    }
+                    if (boxes == 4) {
+                        load_a(sb, &tmA128, r0);
+                    } else {
+                        for (int b = 0; b < boxes; ++b) load_a(sb + static_cast<uint32_t>(b) * 32u * BK * 2u, &tmA32, r0 + 32 * b);
+                    }
+                }
             }
+            if (!ok && leader) {
+                // wait for the copies that were issued but may not have landed
+                const uint32_t first = it > STAGES ? it - STAGES : 0;
+                for (uint32_t i = first; i < it; ++i)
+                    wait_bar<PAIR>(zbp::smem_u32(&ctl->full[i % STAGES]), (i / STAGES) & 1u, abort_flag, args.err,
+                                   ERR_WAIT_PRODUCER, DRAIN_LIMIT_NS, false);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {
+            // ------------------------------------------------ MMA issuer
+            uint32_t it = 0, local = 0;
+            bool ok = true;
+            for (int tile = cluster; ok && walk.to(tile, row0, nrows, fb); tile += clusters, ++local) {
+                const uint32_t buf = local & 1u, tr = local >> 1;
+                if (!wait_bar<PAIR>(zbp::smem_u32(&ctl->tempty[buf]), (tr & 1u) ^ 1u, abort_flag, args.err,
+                                    ERR_WAIT_MMA, WAIT_LIMIT_NS, true))
+                    break;
+                zbp::tc_fence_after();
+                const uint32_t d_tmem = tmem_base + buf * C::TILE_T;
+                const uint32_t mma_n = static_cast<uint32_t>((nrows + C::N_STEP - 1) / C::N_STEP * C::N_STEP);
+                const uint32_t idesc = zbp::idesc_bf16_f32(128 * CG, mma_n, A_MN, 0);
+                for (int kb = 0; kb < num_kb; ++kb, ++it) {
+                    const uint32_t s = it % STAGES, r = it / STAGES;
+                    if (!wait_bar<PAIR>(zbp::smem_u32(&ctl->full[s]), r & 1u, abort_flag, args.err, ERR_WAIT_MMA,
+                                        WAIT_LIMIT_NS, true)) {
+                        ok = false;
+                        break;
+                    }
+                    zbp::tc_fence_after();
+                    const uint32_t sa = zbp::smem_u32(smem + s * C::STAGE);
+                    const uint32_t sb = sa + A_BYTES;
+#pragma unroll
+                    for (int kk = 0; kk < BK / 16; ++kk) {
+                        const uint64_t ad = A_MN ? zbp::smem_desc_sw128(sa + kk * 2048, MN_ATOM_BYTES, 1024)
+                                                 : zbp::smem_desc_sw128(sa + kk * 32, 16, 1024);
+                        const uint64_t bd = zbp::smem_desc_sw128(sb + kk * 32, 16, 1024);
+                        const uint32_t acc = (kb | kk) != 0 ? 1u : 0u;
+                        if (PAIR)
+                            zbp::tc_mma_f16_pair(d_tmem, ad, bd, idesc, acc);
+                        else
+                            zbp::tc_mma_f16(d_tmem, ad, bd, idesc, acc);
+                    }
+                    if (PAIR)
+                        zbp::tc_commit_pair_multicast(zbp::smem_u32(&ctl->empty[s]), 0x3);
+                    else
+                        zbp::tc_commit(zbp::smem_u32(&ctl->empty[s]));
+                }
+                if (!ok) break;
+                if (PAIR)
+                    zbp::tc_commit_pair_multicast(zbp::smem_u32(&ctl->tfull[buf]), 0x3);
+                else
+                    zbp::tc_commit(zbp::smem_u32(&ctl->tfull[buf]));
+            }
+            // every MMA issued here completes before TMEM is released
+            if (PAIR)
+                zbp::tc_commit_pair(zbp::smem_u32(&ctl->drain));
+            else
+                zbp::tc_commit(zbp::smem_u32(&ctl->drain));
+            wait_bar<PAIR>(zbp::smem_u32(&ctl->drain), 0, abort_flag, args.err, ERR_WAIT_MMA, DRAIN_LIMIT_NS, false);
+        }
+    } else {
+        // ---------------------------------------------------- epilogue
+        const int ew = warp - 2, q = warp & 3, hf = ew >> 2;
+        const uint32_t stg0 = zbp::smem_u32(staging + ew * BOXES * ROW_BOX);
+        // this lane's address in a box for the matrix moves: matrix lane/8 is
+        // an 8-column block, memory row lane%8 a row of D (64-byte swizzle)
+        const int mr = lane & 7, mb = lane >> 3;
+        uint32_t local = 0;
+        uint32_t g = 0;       // boxes filled so far (GeLU': chunks)
+        uint32_t issued = 0;  // H boxes asked for
+        bool ok = true;
+        for (int tile = cluster; ok && walk.to(tile, row0, nrows, fb); tile += clusters, ++local) {
+            const uint32_t buf = local & 1u, tr = local >> 1;
+            const int n0 = fb * C::TILE_F + static_cast<int>(rank) * 128 + q * 32;  // first column of D
+            const int chunks = (nrows + MAX_TOK - 1) / MAX_TOK;
+            const bool cols_live = n0 < args.N;
+            const int mine = cols_live ? (chunks - hf + 1) / 2 : 0;  // chunks hf, hf + 2, ...
+            auto ask_h = [&](int i) {  // chunk i of mine: H into box (g0 + i) % 4
+                if (lane == 0) {
+                    const uint32_t b = issued & 3u;
+                    const uint32_t bar = zbp::smem_u32(&ctl->hbar[ew][b]);
+                    zbp::mbar_arrive_expect_tx(bar, ROW_BOX);
+                    zbp::tma_load_2d(stg0 + b * ROW_BOX, &tmO1, bar, n0, row0 + (hf + 2 * i) * MAX_TOK);
+                }
+                ++issued;
+            };
+            if (EPI == zb::EPI_GELU_BWD && mine > 0) {
+                // at most the last two boxes' stores still read them
+                if (lane == 0) zbp::bulk_wait_read<2>();
+                ask_h(0);
+                if (mine > 1) ask_h(1);
+            }
+            float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (EPI != zb::EPI_GELU_BWD && args.bias && cols_live) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int n = n0 + i * 8 + (lane >> 2);
+                    if (n < args.N) bias[i] = __bfloat162float(args.bias[static_cast<long long>(walk.e) * args.N + n]);
+                }
+            }
+            if (!wait_bar<PAIR>(zbp::smem_u32(&ctl->tfull[buf]), tr & 1u, abort_flag, args.err, ERR_WAIT_EPI,
+                                WAIT_LIMIT_NS, true))
+                break;
+            zbp::tc_fence_after();
+            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * C::TILE_T;
+#pragma unroll 1
+            for (int i = 0; i < mine; ++i) {
+                const int c = hf + 2 * i;
+                uint32_t v[2][16];
+                zbp::tmem_ld_16x256b_x4(taddr + c * MAX_TOK, v[0]);
+                zbp::tmem_ld_16x256b_x4(taddr + (16u << 16) + c * MAX_TOK, v[1]);
+                const int row = row0 + c * MAX_TOK;
+                const int live = nrows - c * MAX_TOK;  // rows of this chunk
+                if (EPI == zb::EPI_GELU_BWD && i + 2 < mine) {
+                    if (lane == 0) zbp::bulk_wait_read<1>();
+                    ask_h(i + 2);
+                }
+                // one box of bf16 pairs: w[j][fb]: rows 8j + 2(t%4), +1 of column block fb
+                auto store = [&](const CUtensorMap* tm, __nv_bfloat16* out, uint32_t stg, const uint32_t (&w)[4][4]) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int rr = 8 * j + mr;
+                        zbp::stmatrix_x4_trans(stg + static_cast<uint32_t>(rr * 64 + ((mb ^ ((rr >> 1) & 3)) << 4)),
+                                               w[j][0], w[j][1], w[j][2], w[j][3]);
+                    }
+                    if (live >= MAX_TOK) {
+                        zbp::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            zbp::tma_store_2d(tm, stg, n0, row);
+                            zbp::bulk_commit();
+                        }
+                    } else {
+                        __syncwarp();
+                        if (lane < live) {
+                            __nv_bfloat16* o = out + static_cast<long long>(row + lane) * args.N + n0;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (n0 + 8 * k < args.N) {
+                                    const float4 x = zbp::ld_shared_v4(
+                                        stg + static_cast<uint32_t>(lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)));
+                                    *reinterpret_cast<float4*>(o + 8 * k) = x;
+                                }
+                        }
+                        zbp::fence_proxy_async_smem();  // the box may be a copy's target next
+                        __syncwarp();
+                        if (lane == 0) zbp::bulk_commit();  // an empty group: groups count boxes
+                    }
+                };
+                uint32_t hw[4][4];
+                uint32_t hstg = 0;
+                if (EPI == zb::EPI_GELU_BWD) {
+                    const uint32_t b = g & 3u;
+                    if (!wait_bar<false>(zbp::smem_u32(&ctl->hbar[ew][b]), (g >> 2) & 1u, abort_flag, args.err,
+                                         ERR_WAIT_EPI, WAIT_LIMIT_NS, true)) {
+                        ok = false;
+                        break;
+                    }
+                    hstg = stg0 + b * ROW_BOX;
+                    ++g;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int rr = 8 * j + mr;
+                        zbp::ldmatrix_x4_trans(hstg + static_cast<uint32_t>(rr * 64 + ((mb ^ ((rr >> 1) & 3)) << 4)),
+                                               hw[j][0], hw[j][1], hw[j][2], hw[j][3]);
+                    }
+                }
+                zbp::tmem_ld_wait();
+                // x[j * 8 + 2 fb + p]: row 8j + 2(t%4) + p, column block fb
+                float x[32];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int f = 0; f < 4; ++f)
+#pragma unroll
+                        for (int p = 0; p < 2; ++p)
+                            x[j * 8 + f * 2 + p] = __uint_as_float(v[f >> 1][4 * j + 2 * (f & 1) + p]) +
+                                                   (EPI == zb::EPI_GELU_BWD ? 0.0f : bias[f]);
+                if (EPI == zb::EPI_GELU_BWD) {
+                    uint32_t hf32[16];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int f = 0; f < 4; ++f) hf32[j * 4 + f] = hw[j][f];
+                    if (args.act == ZB_ACT_GELU_TANH)
+                        gelu_grad_mul<true, 32>(x, hf32);
+                    else
+                        gelu_grad_mul<false, 32>(x, hf32);
+                }
+                uint32_t w[4][4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int f = 0; f < 4; ++f) w[j][f] = pack_bf16x2(x[j * 8 + f * 2], x[j * 8 + f * 2 + 1]);
+                if (EPI == zb::EPI_GELU_BWD) {
+                    __syncwarp();  // every lane has read H from this box
+                    store(&tmO0, args.out0, hstg, w);
+                } else {
+                    uint32_t stg = stg0 + (g & 1u) * ROW_BOX;
+                    ++g;
+                    staging_acquire(lane);
+                    store(&tmO0, args.out0, stg, w);
+                    if (EPI == zb::EPI_GELU_DUAL) {
+                        uint32_t a[16];
+                        if (args.act == ZB_ACT_GELU_TANH)
+                            gelu_pack<true, 32>(x, a);
+                        else
+                            gelu_pack<false, 32>(x, a);
+                        uint32_t w2[4][4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int f = 0; f < 4; ++f) w2[j][f] = a[j * 4 + f];
+                        stg = stg0 + (g & 1u) * ROW_BOX;
+                        ++g;
+                        staging_acquire(lane);
+                        store(&tmO1, args.out1, stg, w2);
+                    }
+                }
+            }
+            if (!ok) break;
+            zbp::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                const uint32_t te = zbp::smem_u32(&ctl->tempty[buf]);
+                if (PAIR)
+                    zbp::mbar_arrive_cluster(zbp::mapa_shared(te, 0));
+                else
+                    zbp::mbar_arrive(te);
+            }
+        }
+        if (EPI == zb::EPI_GELU_BWD)  // H boxes asked for and not used (after an abort)
+            for (; g != issued; ++g)
+                wait_bar<false>(zbp::smem_u32(&ctl->hbar[ew][g & 3u]), (g >> 2) & 1u, abort_flag, args.err, ERR_WAIT_EPI,
+                                DRAIN_LIMIT_NS, false);
+        // the staging boxes must not be released while a bulk store reads them
+        if (lane == 0) zbp::bulk_wait<0>();
+        __syncwarp();
+    }
+
+    __syncthreads();
+    if (PAIR) zbp::cluster_sync();  // no remote arrivals or copies remain
+    if (warp == 1) {
+        zbp::tc_fence_after();
+        if (PAIR)
+            zbp::tmem_dealloc_pair(tmem_base, C::TMEM);
+        else
+            zbp::tmem_dealloc(tmem_base, C::TMEM);
     }
 }
 
-// dW[e][m][n] (+)= sum over the rows r of e of A[r][m] B[r][n]
-__global__ void __launch_bounds__(256)
-    zb_moe_wgrad_simple_kernel(const __nv_bfloat16* A, const __nv_bfloat16* B, float* dW, const int* offsets, int rows,
-                               int M, int N, int accumulate) {
-    __shared__ float As[TK][TM], Bs[TK][TN];
-    int lo, hi;
-    expert_rows(offsets, blockIdx.z, rows, lo, hi);
-    const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
-    const int m0 = blockIdx.y * TM, n0 = blockIdx.x * TN;
-    float acc[4][4] = {};
-    for (int r0 = lo; r0 < hi; r0 += TK) {
-        for (int i = tid; i < TK * TM; i += 256) {
-            const int r = r0 + i / TM, m = m0 + i % TM, n = n0 + i % TN;
-            As[i / TM][i % TM] = r < hi && m < M ? __bfloat162float(A[static_cast<long long>(r) * M + m]) : 0.0f;
-            Bs[i / TN][i % TN] = r < hi && n < N ? __bfloat162float(B[static_cast<long long>(r) * N + n]) : 0.0f;
-        }
-        __syncthreads();
-        for (int k = 0; k < TK; ++k)
-            for (int i = 0; i < 4; ++i)
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(As[k][ty * 4 + i], Bs[k][tx * 4 + j], acc[i][j]);
-        __syncthreads();
+// ---------------------------------------------------------------- W
+// dW[e][m][n] (+)= sum over the rows r of e of A[r][m] B[r][n], both of the
+// pass's products in one launch.  The contraction runs over an expert's rows,
+// so its last block of 64 must not see the next expert's: each expert has
+// tensor maps of its own rows (their start and number set on the device by
+// zb_moe_maps_kernel), and the copies past the last row fill in zeros.  Both
+// operands are read as they lie (MN-major).  The fp32 tile goes out through
+// 32 x 32 staging boxes, added in place by TMA reduce-adds when accumulating
+// (one add per element: no order to vary).
+struct MapsArgs {
+    const int* offsets;
+    int rows, experts, width[4];
+    const __nv_bfloat16* base[4];
+    CUtensorMap* out;  // [experts][4]
+};
+__global__ void __launch_bounds__(128)
+    zb_moe_maps_kernel(const __grid_constant__ CUtensorMap t0, const __grid_constant__ CUtensorMap t1,
+                       const __grid_constant__ CUtensorMap t2, const __grid_constant__ CUtensorMap t3,
+                       const MapsArgs a) {
+    const int i = blockIdx.x * blockDim.x + threadIdx.x;
+    zbp::grid_dependency_wait();
+    zbp::allow_dependent_launch();
+    if (i >= 4 * a.experts) return;
+    const int e = i >> 2, k = i & 3;
+    const CUtensorMap* t = k == 0 ? &t0 : k == 1 ? &t1 : k == 2 ? &t2 : &t3;
+    if (a.base[k] == nullptr) return;
+    // the rows of e as load_offsets() makes them legal
+    int lo = 0, hi = 0;
+    for (int x = 0; x <= e + 1; ++x) {
+        const int o = max(hi, min(max(a.offsets[x], 0), a.rows));
+        lo = hi;
+        hi = o;
     }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-            if (m >= M || n >= N) continue;
-            float* d = dW + (static_cast<long long>(blockIdx.z) * M + m) * N + n;
-            *d = accumulate ? *d + acc[i][j] : acc[i][j];
+    uint4* dst = reinterpret_cast<uint4*>(a.out + i);
+    const uint4* src = reinterpret_cast<const uint4*>(t);
+#pragma unroll
+    for (int w = 0; w < 8; ++w) dst[w] = src[w];
+    // a map has at least one row; an expert without rows does not use its maps
+    zbp::tensormap_set(dst, a.base[k] + static_cast<long long>(lo) * a.width[k],
+                       static_cast<uint32_t>(max(hi - lo, 1)));
+}
+
+struct WArgs {
+    const int* offsets;
+    const CUtensorMap* maps;  // [experts][4]: A and B of product 0, of product 1
+    int rows, experts, products;
+    int M[2], N[2];
+    int accumulate;
+    unsigned int* err;
+};
+template <int CG>
+struct WCtl {
+    uint64_t full[6], empty[6], tfull[2], tempty[2], drain;
+    uint32_t tmem_base;
+    int abort_flag;
+    int off[MAX_EXPERTS + 1];
+};
+template <int CG>
+constexpr size_t w_smem() {
+    return 1024 + Cfg<CG>::STAGES * Cfg<CG>::STAGE_BYTES + STAGING_BYTES + sizeof(WCtl<CG>);
+}
+static_assert(w_smem<1>() <= 232448 && w_smem<2>() <= 232448, "shared memory");
+
+template <int CG>
+__global__ void __launch_bounds__(192, 1)
+    zb_moe_wgrad_kernel(const __grid_constant__ CUtensorMap tmO0, const __grid_constant__ CUtensorMap tmO1,
+                        const WArgs args) {
+    using C = Cfg<CG>;
+    constexpr int STAGES = C::STAGES;
+    constexpr bool PAIR = CG == 2;
+    constexpr int WARPS = 4;
+    constexpr uint32_t BOX = 32 * 128;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t* staging = smem + STAGES * C::STAGE_BYTES;
+    WCtl<CG>* ctl = reinterpret_cast<WCtl<CG>*>(staging + STAGING_BYTES);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = PAIR ? zbp::cluster_ctarank() : 0u;
+    const bool leader = rank == 0;
+    const int cluster = blockIdx.x / CG, clusters = gridDim.x / CG;
+    const int tm0 = (args.M[0] + C::TILE_M - 1) / C::TILE_M, tn0 = (args.N[0] + BN - 1) / BN;
+    const int tm1 = args.products > 1 ? (args.M[1] + C::TILE_M - 1) / C::TILE_M : 0;
+    const int tn1 = args.products > 1 ? (args.N[1] + BN - 1) / BN : 0;
+    const int per = tm0 * tn0 + tm1 * tn1;  // tiles of one expert
+    const int num_tiles = per * args.experts;
+    // expert, product and block of a tile
+    auto locate = [&](int tile, int& e, int& mb, int& nb) -> int {
+        e = tile / per;
+        int t = tile - e * per;
+        if (t < tm0 * tn0) {
+            tile_coords(t, tm0, tn0, C::GROUP_M, mb, nb);
+            return 0;
         }
+        tile_coords(t - tm0 * tn0, tm1, tn1, C::GROUP_M, mb, nb);
+        return 1;
+    };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            zbp::mbar_init(zbp::smem_u32(&ctl->full[s]), 1);
+            zbp::mbar_init(zbp::smem_u32(&ctl->empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            zbp::mbar_init(zbp::smem_u32(&ctl->tfull[b]), 1);
+            zbp::mbar_init(zbp::smem_u32(&ctl->tempty[b]), WARPS * CG);
+        }
+        zbp::mbar_init(zbp::smem_u32(&ctl->drain), 1);
+        ctl->abort_flag = 0;
+        zbp::fence_mbar_init();
+        zbp::tma_prefetch_desc(&tmO0);
+        if (args.products > 1) zbp::tma_prefetch_desc(&tmO1);
+    }
+    if (warp == 1) {
+        if (PAIR) {
+            zbp::tmem_alloc_pair(zbp::smem_u32(&ctl->tmem_base), TMEM_COLS);
+            zbp::tmem_relinquish_pair();
+        } else {
+            zbp::tmem_alloc(zbp::smem_u32(&ctl->tmem_base), TMEM_COLS);
+            zbp::tmem_relinquish();
+        }
+    }
+    zbp::tc_fence_before();
+    __syncthreads();
+    if (PAIR) zbp::cluster_sync();
+    zbp::tc_fence_after();
+    const uint32_t tmem_base = ctl->tmem_base;
+    volatile int* abort_flag = &ctl->abort_flag;
+    zbp::grid_dependency_wait();
+    zbp::allow_dependent_launch();
+    load_offsets(ctl->off, args.offsets, args.experts, args.rows);
+    auto blocks_of = [&](int e) { return (ctl->off[e + 1] - ctl->off[e] + BK - 1) / BK; };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ------------------------------------------------ TMA producer
+            uint32_t it = 0;
+            bool ok = true;
+            for (int tile = cluster; tile < num_tiles && ok; tile += clusters) {
+                int e, mb, nb;
+                const int p = locate(tile, e, mb, nb);
+                const int num_kb = blocks_of(e);
+                if (num_kb == 0) continue;
+                const CUtensorMap* tma = args.maps + 4 * e + 2 * p;
+                const CUtensorMap* tmb = tma + 1;
+                zbp::fence_tensormap_acquire(tma);
+                zbp::fence_tensormap_acquire(tmb);
+                const int m0 = mb * C::TILE_M + static_cast<int>(rank) * BM;
+                const int nb0 = nb * BN + static_cast<int>(rank) * C::B_ROWS;
+                for (int kb = 0; kb < num_kb; ++kb, ++it) {
+                    const uint32_t s = it % STAGES, r = it / STAGES;
+                    if (!wait_bar<PAIR>(zbp::smem_u32(&ctl->empty[s]), (r & 1u) ^ 1u, abort_flag, args.err,
+                                        ERR_WAIT_PRODUCER, WAIT_LIMIT_NS, true)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t full_local = zbp::smem_u32(&ctl->full[s]);
+                    const uint32_t full = PAIR ? zbp::mapa_shared(full_local, 0) : full_local;
+                    const uint32_t sa = zbp::smem_u32(smem + s * C::STAGE_BYTES);
+                    const uint32_t sb = sa + A_BYTES;
+                    if (leader) zbp::mbar_arrive_expect_tx(full_local, C::STAGE_BYTES * CG);
+                    auto load = [&](uint32_t dst, const CUtensorMap* tm, int x) {
+                        if (PAIR)
+                            zbp::tma_load_2d_pair(dst, tm, full, x, kb * BK);
+                        else
+                            zbp::tma_load_2d(dst, tm, full, x, kb * BK);
+                    };
+                    load(sa, tma, m0);
+                    load(sa + MN_ATOM_BYTES, tma, m0 + 64);
+#pragma unroll
+                    for (int i = 0; i < C::B_ROWS / 64; ++i) load(sb + i * MN_ATOM_BYTES, tmb, nb0 + 64 * i);
+                }
+            }
+            if (!ok && leader) {
+                const uint32_t first = it > STAGES ? it - STAGES : 0;
+                for (uint32_t i = first; i < it; ++i)
+                    wait_bar<PAIR>(zbp::smem_u32(&ctl->full[i % STAGES]), (i / STAGES) & 1u, abort_flag, args.err,
+                                   ERR_WAIT_PRODUCER, DRAIN_LIMIT_NS, false);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {
+            // ------------------------------------------------ MMA issuer
+            constexpr uint32_t idesc = zbp::idesc_bf16_f32(BM * CG, BN, 1, 1);
+            uint32_t it = 0, local = 0;
+            bool ok = true;
+            for (int tile = cluster; tile < num_tiles && ok; tile += clusters) {
+                int e, mb, nb;
+                locate(tile, e, mb, nb);
+                const int num_kb = blocks_of(e);
+                if (num_kb == 0) continue;
+                const uint32_t buf = local & 1u, tr = local >> 1;
+                ++local;
+                if (!wait_bar<PAIR>(zbp::smem_u32(&ctl->tempty[buf]), (tr & 1u) ^ 1u, abort_flag, args.err,
+                                    ERR_WAIT_MMA, WAIT_LIMIT_NS, true))
+                    break;
+                zbp::tc_fence_after();
+                const uint32_t d_tmem = tmem_base + buf * ACC_COLS;
+                for (int kb = 0; kb < num_kb; ++kb, ++it) {
+                    const uint32_t s = it % STAGES, r = it / STAGES;
+                    if (!wait_bar<PAIR>(zbp::smem_u32(&ctl->full[s]), r & 1u, abort_flag, args.err, ERR_WAIT_MMA,
+                                        WAIT_LIMIT_NS, true)) {
+                        ok = false;
+                        break;
+                    }
+                    zbp::tc_fence_after();
+                    const uint32_t sa = zbp::smem_u32(smem + s * C::STAGE_BYTES);
+                    const uint32_t sb = sa + A_BYTES;
+#pragma unroll
+                    for (int kk = 0; kk < BK / 16; ++kk) {
+                        const uint64_t ad = zbp::smem_desc_sw128(sa + kk * 2048, MN_ATOM_BYTES, 1024);
+                        const uint64_t bd = zbp::smem_desc_sw128(sb + kk * 2048, MN_ATOM_BYTES, 1024);
+                        const uint32_t acc = (kb | kk) != 0 ? 1u : 0u;
+                        if (PAIR)
+                            zbp::tc_mma_f16_pair(d_tmem, ad, bd, idesc, acc);
+                        else
+                            zbp::tc_mma_f16(d_tmem, ad, bd, idesc, acc);
+                    }
+                    if (PAIR)
+                        zbp::tc_commit_pair_multicast(zbp::smem_u32(&ctl->empty[s]), 0x3);
+                    else
+                        zbp::tc_commit(zbp::smem_u32(&ctl->empty[s]));
+                }
+                if (!ok) break;
+                if (PAIR)
+                    zbp::tc_commit_pair_multicast(zbp::smem_u32(&ctl->tfull[buf]), 0x3);
+                else
+                    zbp::tc_commit(zbp::smem_u32(&ctl->tfull[buf]));
+            }
+            if (PAIR)
+                zbp::tc_commit_pair(zbp::smem_u32(&ctl->drain));
+            else
+                zbp::tc_commit(zbp::smem_u32(&ctl->drain));
+            wait_bar<PAIR>(zbp::smem_u32(&ctl->drain), 0, abort_flag, args.err, ERR_WAIT_MMA, DRAIN_LIMIT_NS, false);
+        }
+    } else {
+        // ---------------------------------------------------- epilogue
+        const int ew = warp - 2, q = warp & 3;
+        const uint32_t stg0 = zbp::smem_u32(staging + ew * 2 * BOX);
+        uint32_t flip = 0, local = 0;
+        for (int tile = cluster; tile < num_tiles; tile += clusters) {
+            int e, mb, nb;
+            const int p = locate(tile, e, mb, nb);
+            const bool none = blocks_of(e) == 0;
+            if (none && args.accumulate) continue;
+            const int row0 = mb * C::TILE_M + static_cast<int>(rank) * BM + q * 32;
+            const int n0 = nb * BN;
+            const int Mp = args.M[p], Np = args.N[p];
+            const CUtensorMap* tmO = p ? &tmO1 : &tmO0;
+            const uint32_t buf = local & 1u, tr = local >> 1;
+            if (!none) {
+                ++local;
+                if (!wait_bar<PAIR>(zbp::smem_u32(&ctl->tfull[buf]), tr & 1u, abort_flag, args.err, ERR_WAIT_EPI,
+                                    WAIT_LIMIT_NS, true))
+                    break;
+                zbp::tc_fence_after();
+            }
+            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * ACC_COLS;
+#pragma unroll 1
+            for (int c = 0; c < BN / 32; ++c) {
+                const int col0 = n0 + c * 32;
+                uint32_t v[32];
+                if (none) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = 0u;  // no rows: the gradient is zero
+                } else {
+                    zbp::tmem_ld_32x32b_x32(taddr + c * 32, v);
+                    zbp::tmem_ld_wait();
+                }
+                if (row0 >= Mp || col0 >= Np) continue;
+                const uint32_t stg = stg0 + flip * BOX;
+                flip ^= 1u;
+                staging_acquire(lane);
+                stage_row(stg, lane, v);
+                zbp::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (args.accumulate)
+                        zbp::tma_reduce_add_3d(tmO, stg, col0, row0, e);
+                    else
+                        zbp::tma_store_3d(tmO, stg, col0, row0, e);
+                    zbp::bulk_commit();
+                }
+            }
+            if (!none) {
+                zbp::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    const uint32_t te = zbp::smem_u32(&ctl->tempty[buf]);
+                    if (PAIR)
+                        zbp::mbar_arrive_cluster(zbp::mapa_shared(te, 0));
+                    else
+                        zbp::mbar_arrive(te);
+                }
+            }
+        }
+        if (lane == 0) zbp::bulk_wait<0>();
+        __syncwarp();
+    }
+
+    __syncthreads();
+    if (PAIR) zbp::cluster_sync();
+    if (warp == 1) {
+        zbp::tc_fence_after();
+        if (PAIR)
+            zbp::tmem_dealloc_pair(tmem_base, TMEM_COLS);
+        else
+            zbp::tmem_dealloc(tmem_base, TMEM_COLS);
+    }
 }
 
 // db[e][n] (+)= sum over the rows of e of X[r][n]: a block takes 64 columns of
@@ -146,27 +842,218 @@ zb_status launched(const char* who) {
     return ZB_OK;
 }
 
+// 3-D map of a stack of `count` matrices [outer, inner], dense.
+bool make_map3(CUtensorMap* m, const void* base, bool f32, uint64_t inner, uint64_t outer, uint64_t count,
+               uint32_t box_inner, uint32_t box_outer, std::string* why) {
+    EncodeTiledFn fn = encode_fn(why);
+    if (!fn) return false;
+    const uint64_t es = f32 ? 4 : 2;
+    cuuint64_t dims[3] = {inner, outer, count};
+    cuuint64_t strides[2] = {inner * es, inner * outer * es};
+    cuuint32_t box[3] = {box_inner, box_outer, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                          const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        if (why) *why = "cuTensorMapEncodeTiled failed with CUresult " + std::to_string(static_cast<int>(r));
+        return false;
+    }
+    return true;
+}
+
+// Shared-memory limit of a kernel, set once per device, and the CTAs of a
+// full grid of its clusters.
+template <typename K>
+zb_status full_grid(K kern, std::atomic<int>* cache, size_t smem, int threads, int cg, int* ctas) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev < 0 || dev >= 64) return zb::fail(ZB_ERR_CUDA, "cudaGetDevice failed");
+    if (!cache[dev].load(std::memory_order_relaxed)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e != cudaSuccess)
+            return zb::fail(ZB_ERR_CUDA, std::string("cudaFuncSetAttribute: ") + cudaGetErrorString(e));
+        int n = sm_count();
+        if (cg == 2) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(512);
+            cfg.blockDim = dim3(threads);
+            cfg.dynamicSmemBytes = smem;
+            cudaLaunchAttribute attr;
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = 2;
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            int clusters = 0;
+            e = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
+            if (e != cudaSuccess || clusters <= 0)
+                return zb::fail(ZB_ERR_UNSUPPORTED, std::string("no co-resident CTA pairs: ") + cudaGetErrorString(e));
+            n = 2 * clusters;
+        }
+        if (n <= 0) return zb::fail(ZB_ERR_CUDA, "cannot query the SM count");
+        cache[dev].store(n, std::memory_order_relaxed);
+    }
+    *ctas = cache[dev].load(std::memory_order_relaxed);
+    return ZB_OK;
+}
+
+struct LaunchCfg {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    LaunchCfg(int grid, int threads, size_t smem, int cg, void* stream) {
+        cfg.gridDim = dim3(static_cast<unsigned>(grid));
+        cfg.blockDim = dim3(static_cast<unsigned>(threads));
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = static_cast<cudaStream_t>(stream);
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = cg;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = cg == 2 ? 2 : 1;
+    }
+};
+
+template <int EPI, int A_MN, int CG>
+zb_status launch_rows(const CUtensorMap (&mp)[5], const RowsArgs& a, long long tiles, void* stream) {
+    auto kern = zb_moe_rows_kernel<EPI, A_MN, CG>;
+    static std::atomic<int> cache[64];
+    int ctas = 0;
+    zb_status s = full_grid(kern, cache, rows_smem<EPI>(), NUM_THREADS, CG, &ctas);
+    if (s != ZB_OK) return s;
+    const int grid = static_cast<int>(std::min<long long>(tiles * CG, ctas));
+    LaunchCfg lc(grid, NUM_THREADS, rows_smem<EPI>(), CG, stream);
+    const cudaError_t e = cudaLaunchKernelEx(&lc.cfg, kern, mp[0], mp[1], mp[2], mp[3], mp[4], a);
+    if (e != cudaSuccess) return zb::fail(ZB_ERR_CUDA, std::string("grouped product launch: ") + cudaGetErrorString(e));
+    return launched("grouped product");
+}
+
+// D[row, n] = sum_k A[row, k] W[e](k, n): W[e] is [K, N] or, transposed, [N, K].
 zb_status rows_product(const zb_moe& m, const int32_t* offsets, const void* A, const void* W, bool transposed,
                        int64_t N, int64_t K, const void* bias, const void* aux, int epi, void* out0, void* out1,
                        void* stream) {
-    SimpleArgs a;
-    a.A = static_cast<const __nv_bfloat16*>(A);
-    a.W = static_cast<const __nv_bfloat16*>(W);
-    a.sk = transposed ? 1 : N;
-    a.sn = transposed ? K : 1;
+    // Pairs take tiles of 256 columns x up to 256 rows, single CTAs 128 x 128.
+    // The number of row tiles depends on counts that only the device knows;
+    // this is their number when the rows are spread evenly over the experts.
+    const int64_t used = std::min<int64_t>(m.experts, m.rows);
+    const int64_t each = (m.rows + used - 1) / used;
+    const long long pair_tiles = used * ((each + 255) / 256) * ((N + 255) / 256);
+    const bool pair = pair_tiles >= sm_count() / 2;
+    // no launch has more tiles than this
+    const int tt = pair ? 256 : 128;
+    const long long most = (m.rows / tt + used) * ((N + tt - 1) / tt);
+
+    std::string why;
+    CUtensorMap mp[5];
+    const uint64_t rows = static_cast<uint64_t>(m.rows);
+    bool ok = transposed ? make_map3(&mp[0], W, false, K, N, m.experts, BK, 128, &why)
+                         : make_map3(&mp[0], W, false, N, K, m.experts, 64, BK, &why);
+    ok = ok && make_map(&mp[1], A, false, K, rows, K, BK, 128, &why);
+    ok = ok && make_map(&mp[2], A, false, K, rows, K, BK, 32, &why);
+    ok = ok && make_map(&mp[3], out0, false, N, rows, N, 32, 32, &why, CU_TENSOR_MAP_SWIZZLE_64B);
+    const void* second = epi == zb::EPI_GELU_DUAL ? out1 : epi == zb::EPI_GELU_BWD ? aux : out0;
+    ok = ok && make_map(&mp[4], second, false, N, rows, N, 32, 32, &why, CU_TENSOR_MAP_SWIZZLE_64B);
+    if (!ok) return zb::fail(ZB_ERR_CUDA, why);
+    unsigned int* err = zb::device_error_word();
+    if (!err) return ZB_ERR_CUDA;
+    RowsArgs a;
+    a.offsets = offsets;
     a.bias = static_cast<const __nv_bfloat16*>(bias);
-    a.aux = static_cast<const __nv_bfloat16*>(aux);
     a.out0 = static_cast<__nv_bfloat16*>(out0);
     a.out1 = static_cast<__nv_bfloat16*>(out1);
-    a.offsets = offsets;
     a.rows = static_cast<int>(m.rows);
+    a.experts = m.experts;
     a.N = static_cast<int>(N);
     a.K = static_cast<int>(K);
-    a.epi = epi;
     a.act = m.act;
-    const dim3 grid(static_cast<unsigned>((N + TN - 1) / TN), m.experts, 8);
-    zb_moe_rows_simple_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
-    return launched("grouped product");
+    a.err = err;
+    if (epi == zb::EPI_GELU_DUAL)
+        return pair ? launch_rows<zb::EPI_GELU_DUAL, 1, 2>(mp, a, most, stream)
+                    : launch_rows<zb::EPI_GELU_DUAL, 1, 1>(mp, a, most, stream);
+    if (epi == zb::EPI_GELU_BWD)
+        return pair ? launch_rows<zb::EPI_GELU_BWD, 0, 2>(mp, a, most, stream)
+                    : launch_rows<zb::EPI_GELU_BWD, 0, 1>(mp, a, most, stream);
+    if (transposed)
+        return pair ? launch_rows<zb::EPI_STORE_BF16, 0, 2>(mp, a, most, stream)
+                    : launch_rows<zb::EPI_STORE_BF16, 0, 1>(mp, a, most, stream);
+    return pair ? launch_rows<zb::EPI_STORE_BF16, 1, 2>(mp, a, most, stream)
+                : launch_rows<zb::EPI_STORE_BF16, 1, 1>(mp, a, most, stream);
+}
+
+struct WProduct {
+    const void *A, *B;  // [rows, M], [rows, N]
+    float* dW;          // [E, M, N]
+    int64_t M, N;
+};
+
+template <int CG>
+zb_status launch_wgrad(const CUtensorMap (&mo)[2], const WArgs& a, long long tiles, void* stream) {
+    auto kern = zb_moe_wgrad_kernel<CG>;
+    static std::atomic<int> cache[64];
+    int ctas = 0;
+    zb_status s = full_grid(kern, cache, w_smem<CG>(), 192, CG, &ctas);
+    if (s != ZB_OK) return s;
+    LaunchCfg lc(static_cast<int>(std::min<long long>(tiles * CG, ctas)), 192, w_smem<CG>(), CG, stream);
+    const cudaError_t e = cudaLaunchKernelEx(&lc.cfg, kern, mo[0], mo[1], a);
+    if (e != cudaSuccess)
+        return zb::fail(ZB_ERR_CUDA, std::string("grouped weight gradient launch: ") + cudaGetErrorString(e));
+    return launched("grouped weight gradient");
+}
+
+zb_status wgrad(const zb_moe& m, const int32_t* offsets, const WProduct* p, int products, int accumulate,
+                void* workspace, void* stream) {
+    std::string why;
+    CUtensorMap mi[4], mo[2];
+    MapsArgs ma;
+    WArgs a;
+    const uint64_t rows = static_cast<uint64_t>(std::max<int64_t>(m.rows, 1));
+    bool ok = true;
+    long long tiles2 = 0, tiles1 = 0;
+    for (int i = 0; i < 2; ++i) {
+        const WProduct& w = p[i < products ? i : 0];
+        // without rows there is nothing to read and no map of it
+        ma.base[2 * i] = i < products && m.rows ? static_cast<const __nv_bfloat16*>(w.A) : nullptr;
+        ma.base[2 * i + 1] = i < products && m.rows ? static_cast<const __nv_bfloat16*>(w.B) : nullptr;
+        ma.width[2 * i] = a.M[i] = static_cast<int>(w.M);
+        ma.width[2 * i + 1] = a.N[i] = static_cast<int>(w.N);
+        ok = ok && make_map3(&mo[i], w.dW, true, w.N, w.M, m.experts, 32, 32, &why);
+        if (m.rows) {
+            ok = ok && make_map(&mi[2 * i], w.A, false, w.M, rows, w.M, 64, BK, &why);
+            ok = ok && make_map(&mi[2 * i + 1], w.B, false, w.N, rows, w.N, 64, BK, &why);
+        } else {
+            mi[2 * i] = mi[2 * i + 1] = mo[i];
+        }
+        if (i < products) {
+            tiles2 += ((w.M + 255) / 256) * ((w.N + 255) / 256);
+            tiles1 += ((w.M + 127) / 128) * ((w.N + 255) / 256);
+        }
+    }
+    if (!ok) return zb::fail(ZB_ERR_CUDA, why);
+    unsigned int* err = zb::device_error_word();
+    if (!err) return ZB_ERR_CUDA;
+    ma.offsets = offsets;
+    ma.rows = static_cast<int>(m.rows);
+    ma.experts = m.experts;
+    ma.out = static_cast<CUtensorMap*>(workspace);
+    {
+        LaunchCfg lc((4 * m.experts + 127) / 128, 128, 0, 1, stream);
+        const cudaError_t e = cudaLaunchKernelEx(&lc.cfg, zb_moe_maps_kernel, mi[0], mi[1], mi[2], mi[3], ma);
+        if (e != cudaSuccess)
+            return zb::fail(ZB_ERR_CUDA, std::string("grouped weight gradient launch: ") + cudaGetErrorString(e));
+    }
+    a.offsets = offsets;
+    a.maps = ma.out;
+    a.rows = ma.rows;
+    a.experts = m.experts;
+    a.products = products;
+    a.accumulate = accumulate;
+    a.err = err;
+    tiles1 *= m.experts;
+    tiles2 *= m.experts;
+    return tiles2 >= sm_count() / 2 ? launch_wgrad<2>(mo, a, tiles2, stream) : launch_wgrad<1>(mo, a, tiles1, stream);
 }
 
 }  // namespace
@@ -251,20 +1138,18 @@ extern "C" zb_status zb_moe_backward_weight(const zb_moe* m, const int32_t* offs
         return zb::fail(ZB_ERR_ALIGN, "zb_moe_backward_weight: workspace must be 256-byte aligned");
     const int rows = static_cast<int>(m->rows), h = static_cast<int>(m->h), f = static_cast<int>(m->f);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    auto product = [&](const void* A, const void* B, float* dW, int M, int N) {
-        const dim3 grid((N + TN - 1) / TN, (M + TM - 1) / TM, m->experts);
-        zb_moe_wgrad_simple_kernel<<<grid, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(A),
-                                                         static_cast<const __nv_bfloat16*>(B), dW, offsets, rows, M, N,
-                                                         accumulate ? 1 : 0);
-        return launched("grouped weight gradient");
-    };
     auto colsum = [&](const void* A, float* db, int N) {
         zb_moe_colsum_kernel<<<dim3((N + 63) / 64, m->experts), 256, 0, st>>>(static_cast<const __nv_bfloat16*>(A), db,
                                                                               offsets, rows, N, accumulate ? 1 : 0);
         return launched("grouped column sums");
     };
-    if (mlp) s = product(A_save, dY, dW2, f, h);
-    if (s == ZB_OK) s = product(X, mlp ? dH : dY, dW1, h, f);
+    if (mlp) {
+        const WProduct p[2] = {{A_save, dY, dW2, f, h}, {X, dH, dW1, h, f}};
+        s = wgrad(*m, offsets, p, 2, accumulate ? 1 : 0, workspace, stream);
+    } else {
+        const WProduct p[1] = {{X, dY, dW1, h, f}};
+        s = wgrad(*m, offsets, p, 1, accumulate ? 1 : 0, workspace, stream);
+    }
     if (s == ZB_OK && m->has_bias) s = colsum(mlp ? dH : dY, db1, f);
     if (s == ZB_OK && m->has_bias && mlp) s = colsum(dY, db2, h);
     if (s == ZB_OK) zb::clear_error();

@@ -174,6 +174,9 @@ CASES = [
     ([300, 513, 64], 256, 512, "erf", True, 0),
     ([700, 20, 0, 0, 1100], 264, 1032, "tanh", False, 3),
     ([5, 17, 8, 0, 2, 40] * 10, 128, 384, "erf", False, 0),
+    # enough tiles for CTA pairs on either side
+    ([290, 1, 257, 0, 40, 513, 96, 33] * 2, 136, 1288, "erf", True, 7),
+    ([290, 1, 257, 0, 40, 513, 96, 33] * 2, 1288, 136, "tanh", False, 0),
     ([200, 90], 320, 136, "none", True, 1),
     ([3, 0, 70], 40, 72, "none", False, 0),
 ]
