@@ -7,11 +7,10 @@
 
 #include <string>
 
-#include "gemm_core.cuh"
+#include "grouped.cuh"
 
 namespace {
 
-constexpr int MAX_EXPERTS = 256;
 constexpr int BLK = 128;
 
 // The least power of two s with amax / s <= 448 = 1.75 * 2^8, at least 2^-126;
@@ -38,9 +37,6 @@ __device__ __forceinline__ uint32_t magnitude(__nv_bfloat16 x) { return (__bfloa
 
 __device__ __forceinline__ uint8_t to_e4m3(float x) {
     return static_cast<uint8_t>(__nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3));
-}
-__device__ __forceinline__ float from_e4m3(uint8_t q) {
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw(q, __NV_E4M3)));
 }
 
 // One warp per 1 x 128 block.
@@ -94,75 +90,363 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-struct MatmulArgs {
-    const uint8_t *A, *B;
-    const float *sa, *sb;
+// ---------------------------------------------------------------- product
+// D[r, n] = sum_b xs[r, b] ws[n/128, b] P_b[r, n], P_b the product over the
+// b-th block of 128 of K.  The scales change from block to block, so a tensor
+// core accumulator holds one P_b only (4 MMAs of K = 32 into one of two
+// accumulators), and the epilogue warps add xs ws P_b to fp32 sums in registers
+// while the next P_b is computed into the other.  A tile's M side is rows, so
+// that a thread (one TMEM lane) has one row: its factor xs ws is one scalar for
+// its 128 columns, one packed FMA per two elements.  The tensor core needs 512
+// cycles for a block of a 128 x 256 tile, the FMAs of 8 warps 128 a scheduler,
+// the TMEM reads 256.
+//
+// Warps 0-3 give registers to warps 4-11, whose threads hold 128 sums and 32
+// loaded values: more than the 168 of an equal share.
+constexpr int FP8_THREADS = 384;
+constexpr int FP8_EPI_WARPS = 8;
+constexpr int FP8_REGS_LOW = 96, FP8_REGS_HIGH = 200;
+static_assert(128 * FP8_REGS_LOW + 256 * FP8_REGS_HIGH <= FP8_THREADS * 168, "register split");
+
+template <int CG>
+struct Fp8Cfg {
+    static constexpr int TILE_T = 128 * CG;                       // rows of D per tile
+    static constexpr int B_ROWS = 256 / CG;                       // columns of D held per CTA
+    static constexpr uint32_t A_BYTES8 = 128 * 128;               // 128 rows x 128 k
+    static constexpr uint32_t STAGE = A_BYTES8 + B_ROWS * 128;
+    static constexpr int STAGES = CG == 1 ? 4 : 6;
+};
+constexpr uint32_t FP8_BOX = 32 * 64;  // 32 rows x 32 columns of bf16
+
+struct Fp8Ctl {
+    uint64_t full[6], empty[6], tfull[2], tempty[2], drain;
+    uint32_t tmem_base;
+    int abort_flag;
+    int off[MAX_EXPERTS + 1];
+};
+template <int CG>
+constexpr size_t fp8_smem() {
+    return 1024 + Fp8Cfg<CG>::STAGES * Fp8Cfg<CG>::STAGE + FP8_EPI_WARPS * 2 * FP8_BOX + sizeof(Fp8Ctl);
+}
+static_assert(fp8_smem<1>() <= 232448 && fp8_smem<2>() <= 232448, "shared memory");
+
+struct Fp8Args {
+    const int* offsets;  // nullptr: one expert with every row
+    const float *xs, *ws;
     const __nv_bfloat16 *bias, *aux;
     __nv_bfloat16 *out0, *out1;
-    const int* offsets;
-    int rows, N, K, epi, act;
+    int rows, experts, N, K, act;
+    unsigned int* err;
 };
 
-__global__ void __launch_bounds__(256) zb_fp8_simple_kernel(const MatmulArgs a) {
-    constexpr int TM = 64, TN = 64, TK = 16;
-    __shared__ float As[TK][TM + 4], Bs[TK][TN + 4];
-    const int e = blockIdx.y;
-    int lo = 0, hi = a.rows;
-    if (a.offsets) {
-        lo = min(max(a.offsets[e], 0), a.rows);
-        hi = max(min(a.offsets[e + 1], a.rows), lo);
+template <int EPI, int CG>
+__global__ void __launch_bounds__(FP8_THREADS, 1)
+    zb_fp8_matmul_kernel(const __grid_constant__ CUtensorMap tmA128, const __grid_constant__ CUtensorMap tmA32,
+                         const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmO0,
+                         const __grid_constant__ CUtensorMap tmO1, const Fp8Args args) {
+    using C = Fp8Cfg<CG>;
+    constexpr bool PAIR = CG == 2;
+    constexpr int STAGES = C::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t* staging = smem + STAGES * C::STAGE;
+    Fp8Ctl* ctl = reinterpret_cast<Fp8Ctl*>(staging + FP8_EPI_WARPS * 2 * FP8_BOX);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = PAIR ? zbp::cluster_ctarank() : 0u;
+    const bool leader = rank == 0;
+    const int cluster = blockIdx.x / CG, clusters = gridDim.x / CG;
+    const int tiles_n = (args.N + 255) / 256;
+    const int num_kb = (args.K + BLK - 1) / BLK;
+    const int n_blocks = (args.N + BLK - 1) / BLK;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            zbp::mbar_init(zbp::smem_u32(&ctl->full[s]), 1);
+            zbp::mbar_init(zbp::smem_u32(&ctl->empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            zbp::mbar_init(zbp::smem_u32(&ctl->tfull[b]), 1);
+            zbp::mbar_init(zbp::smem_u32(&ctl->tempty[b]), FP8_EPI_WARPS * CG);
+        }
+        zbp::mbar_init(zbp::smem_u32(&ctl->drain), 1);
+        ctl->abort_flag = 0;
+        zbp::fence_mbar_init();
+        zbp::tma_prefetch_desc(&tmA128);
+        zbp::tma_prefetch_desc(&tmA32);
+        zbp::tma_prefetch_desc(&tmB);
+        zbp::tma_prefetch_desc(&tmO0);
+        if (EPI == ZB_FP8_GELU) zbp::tma_prefetch_desc(&tmO1);
     }
-    const int KB = (a.K + BLK - 1) / BLK, NB = (a.N + BLK - 1) / BLK;
-    const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
-    const int n0 = blockIdx.x * TN;
-    const uint8_t* B = a.B + static_cast<long long>(e) * a.N * a.K;
-    const float* sb = a.sb + static_cast<long long>(e) * NB * KB;
-    for (int m0 = lo + blockIdx.z * TM; m0 < hi; m0 += gridDim.z * TM) {
-        float acc[4][4] = {}, part[4][4] = {};
-        for (int k0 = 0; k0 < a.K; k0 += TK) {
-            for (int i = tid; i < TK * TM; i += 256) {
-                const int k = k0 + i % TK, m = m0 + i / TK, n = n0 + i / TK;
-                As[i % TK][i / TK] = m < hi && k < a.K ? from_e4m3(a.A[static_cast<long long>(m) * a.K + k]) : 0.0f;
-                Bs[i % TK][i / TK] = n < a.N && k < a.K ? from_e4m3(B[static_cast<long long>(n) * a.K + k]) : 0.0f;
+    if (warp == 1) {
+        if (PAIR) {
+            zbp::tmem_alloc_pair(zbp::smem_u32(&ctl->tmem_base), TMEM_COLS);
+            zbp::tmem_relinquish_pair();
+        } else {
+            zbp::tmem_alloc(zbp::smem_u32(&ctl->tmem_base), TMEM_COLS);
+            zbp::tmem_relinquish();
+        }
+    }
+    zbp::tc_fence_before();
+    __syncthreads();
+    if (PAIR) zbp::cluster_sync();
+    zbp::tc_fence_after();
+    const uint32_t tmem_base = ctl->tmem_base;
+    volatile int* abort_flag = &ctl->abort_flag;
+    zbp::grid_dependency_wait();
+    zbp::allow_dependent_launch();
+    if (args.offsets) {
+        load_offsets(ctl->off, args.offsets, args.experts, args.rows);
+    } else {
+        if (threadIdx.x == 0) {
+            ctl->off[0] = 0;
+            ctl->off[1] = args.rows;
+        }
+        __syncthreads();
+    }
+
+    Walk<C::TILE_T, false> walk(ctl->off, args.experts, tiles_n);
+    int row0 = 0, nrows = 0, nb = 0;
+    if (warp < 4) {
+        zbp::regs_dec<FP8_REGS_LOW>();
+        if (warp == 0 && lane == 0) {
+            // ------------------------------------------------ TMA producer
+            uint32_t it = 0;
+            bool ok = true;
+            for (int tile = cluster; ok && walk.to(tile, row0, nrows, nb); tile += clusters) {
+                // 32-row boxes of rows in this CTA, and in both
+                auto boxes_of = [&](int r) { return max(0, min(4, (nrows - r * 128 + 31) / 32)); };
+                const int boxes = boxes_of(static_cast<int>(rank));
+                const int r0 = row0 + static_cast<int>(rank) * 128;
+                const int all = boxes_of(0) + (PAIR ? boxes_of(1) : 0);
+                const uint32_t bytes = static_cast<uint32_t>(all) * 32u * 128u + 256u * 128u;
+                const int n0 = nb * 256 + static_cast<int>(rank) * C::B_ROWS;
+                for (int kb = 0; kb < num_kb; ++kb, ++it) {
+                    const uint32_t s = it % STAGES, r = it / STAGES;
+                    if (!wait_bar<PAIR>(zbp::smem_u32(&ctl->empty[s]), (r & 1u) ^ 1u, abort_flag, args.err,
+                                        ERR_WAIT_PRODUCER, WAIT_LIMIT_NS, true)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t full_local = zbp::smem_u32(&ctl->full[s]);
+                    const uint32_t full = PAIR ? zbp::mapa_shared(full_local, 0) : full_local;
+                    const uint32_t sa = zbp::smem_u32(smem + s * C::STAGE);
+                    const uint32_t sb = sa + C::A_BYTES8;
+                    const int k0 = kb * BLK;
+                    if (leader) zbp::mbar_arrive_expect_tx(full_local, bytes);
+                    auto load_a = [&](uint32_t dst, const CUtensorMap* tm, int y) {
+                        if (PAIR)
+                            zbp::tma_load_2d_pair(dst, tm, full, k0, y);
+                        else
+                            zbp::tma_load_2d(dst, tm, full, k0, y);
+                    };
+                    if (boxes == 4)
+                        load_a(sa, &tmA128, r0);
+                    else
+                        for (int b = 0; b < boxes; ++b) load_a(sa + static_cast<uint32_t>(b) * 32u * 128u, &tmA32, r0 + 32 * b);
+                    if (PAIR)
+                        zbp::tma_load_3d_pair(sb, &tmB, full, k0, n0, walk.e);
+                    else
+                        zbp::tma_load_3d(sb, &tmB, full, k0, n0, walk.e);
+                }
             }
-            __syncthreads();
-            for (int k = 0; k < TK; ++k)
-                for (int i = 0; i < 4; ++i)
-                    for (int j = 0; j < 4; ++j) part[i][j] = fmaf(As[k][ty * 4 + i], Bs[k][tx * 4 + j], part[i][j]);
-            __syncthreads();
-            if ((k0 + TK) % BLK == 0 || k0 + TK >= a.K) {
-                const int kb = k0 / BLK;
-                for (int i = 0; i < 4; ++i) {
-                    const int m = m0 + ty * 4 + i;
-                    const float s = m < hi ? a.sa[static_cast<long long>(m) * KB + kb] : 0.0f;
-                    for (int j = 0; j < 4; ++j) {
-                        const int n = n0 + tx * 4 + j;
-                        if (n < a.N) acc[i][j] = fmaf(s * sb[static_cast<long long>(n / BLK) * KB + kb], part[i][j], acc[i][j]);
-                        part[i][j] = 0.0f;
+            if (!ok && leader) {
+                // wait for the copies that were issued but may not have landed
+                const uint32_t first = it > STAGES ? it - STAGES : 0;
+                for (uint32_t i = first; i < it; ++i)
+                    wait_bar<PAIR>(zbp::smem_u32(&ctl->full[i % STAGES]), (i / STAGES) & 1u, abort_flag, args.err,
+                                   ERR_WAIT_PRODUCER, DRAIN_LIMIT_NS, false);
+            }
+        } else if (warp == 1 && lane == 0 && leader) {
+            // ------------------------------------------------ MMA issuer
+            constexpr uint32_t idesc = zbp::idesc_e4m3_f32(128 * CG, 256);
+            uint32_t it = 0;  // stage and accumulator: one block of K each
+            bool ok = true;
+            for (int tile = cluster; ok && walk.to(tile, row0, nrows, nb); tile += clusters) {
+                for (int kb = 0; kb < num_kb; ++kb, ++it) {
+                    const uint32_t s = it % STAGES, r = it / STAGES;
+                    const uint32_t buf = it & 1u, tr = it >> 1;
+                    if (!wait_bar<PAIR>(zbp::smem_u32(&ctl->full[s]), r & 1u, abort_flag, args.err, ERR_WAIT_MMA,
+                                        WAIT_LIMIT_NS, true) ||
+                        !wait_bar<PAIR>(zbp::smem_u32(&ctl->tempty[buf]), (tr & 1u) ^ 1u, abort_flag, args.err,
+                                        ERR_WAIT_MMA, WAIT_LIMIT_NS, true)) {
+                        ok = false;
+                        break;
+                    }
+                    zbp::tc_fence_after();
+                    const uint32_t sa = zbp::smem_u32(smem + s * C::STAGE);
+                    const uint32_t sb = sa + C::A_BYTES8;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const uint64_t ad = zbp::smem_desc_sw128(sa + kk * 32, 16, 1024);
+                        const uint64_t bd = zbp::smem_desc_sw128(sb + kk * 32, 16, 1024);
+                        if (PAIR)
+                            zbp::tc_mma_f8_pair(tmem_base + buf * ACC_COLS, ad, bd, idesc, kk != 0);
+                        else
+                            zbp::tc_mma_f8(tmem_base + buf * ACC_COLS, ad, bd, idesc, kk != 0);
+                    }
+                    if (PAIR) {
+                        zbp::tc_commit_pair_multicast(zbp::smem_u32(&ctl->empty[s]), 0x3);
+                        zbp::tc_commit_pair_multicast(zbp::smem_u32(&ctl->tfull[buf]), 0x3);
+                    } else {
+                        zbp::tc_commit(zbp::smem_u32(&ctl->empty[s]));
+                        zbp::tc_commit(zbp::smem_u32(&ctl->tfull[buf]));
                     }
                 }
             }
+            // every MMA issued here completes before TMEM is released
+            if (PAIR)
+                zbp::tc_commit_pair(zbp::smem_u32(&ctl->drain));
+            else
+                zbp::tc_commit(zbp::smem_u32(&ctl->drain));
+            wait_bar<PAIR>(zbp::smem_u32(&ctl->drain), 0, abort_flag, args.err, ERR_WAIT_MMA, DRAIN_LIMIT_NS, false);
         }
-        for (int i = 0; i < 4; ++i)
-            for (int j = 0; j < 4; ++j) {
-                const int m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-                if (m >= hi || n >= a.N) continue;
-                const long long at = static_cast<long long>(m) * a.N + n;
-                float x = acc[i][j];
-                const bool tanh_form = a.act == ZB_ACT_GELU_TANH;
-                if (a.bias) x += __bfloat162float(a.bias[static_cast<long long>(e) * a.N + n]);
-                if (a.epi == ZB_FP8_GELU_GRAD) {
-                    const float h = __bfloat162float(a.aux[at]);
-                    x *= tanh_form ? gelu_grad_t<true>(h) : gelu_grad_t<false>(h);
+    } else {
+        // ---------------------------------------------------- epilogue
+        zbp::regs_inc<FP8_REGS_HIGH>();
+        const int ew = warp - 4, q = warp & 3;
+        const int c_lo = (ew >> 2) * 128;  // this warp's half of the tile's columns: one block of 128
+        const uint32_t stg0 = zbp::smem_u32(staging + ew * 2 * FP8_BOX);
+        uint32_t it = 0, flip = 0;
+        bool ok = true;
+        for (int tile = cluster; ok && walk.to(tile, row0, nrows, nb); tile += clusters) {
+            const int first = row0 + static_cast<int>(rank) * 128 + q * 32;  // the warp's first row
+            const int live = row0 + nrows - first;                           // its live rows
+            const int n0 = nb * 256 + c_lo;
+            const bool scaled = lane < live && n0 < args.N;
+            const float* xs = args.xs + static_cast<long long>(scaled ? first + lane : 0) * num_kb;
+            const float* ws = args.ws + (static_cast<long long>(walk.e) * n_blocks + (scaled ? n0 / BLK : 0)) * num_kb;
+            f32x2 sum[64];
+#pragma unroll
+            for (int i = 0; i < 64; ++i) sum[i] = 0ull;
+            float xn = scaled ? __ldg(xs) : 0.0f, wn = scaled ? __ldg(ws) : 0.0f;
+            for (int kb = 0; kb < num_kb; ++kb, ++it) {
+                const float f = xn * wn;
+                if (scaled && kb + 1 < num_kb) {
+                    xn = __ldg(xs + kb + 1);
+                    wn = __ldg(ws + kb + 1);
                 }
-                a.out0[at] = __float2bfloat16_rn(x);
-                if (a.epi == ZB_FP8_GELU) a.out1[at] = __float2bfloat16_rn(tanh_form ? gelu_t<true>(x) : gelu_t<false>(x));
+                const uint32_t buf = it & 1u, tr = it >> 1;
+                if (!wait_bar<PAIR>(zbp::smem_u32(&ctl->tfull[buf]), tr & 1u, abort_flag, args.err, ERR_WAIT_EPI,
+                                    WAIT_LIMIT_NS, true)) {
+                    ok = false;
+                    break;
+                }
+                zbp::tc_fence_after();
+                const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * ACC_COLS + c_lo;
+                const f32x2 ff = pk2(f, f);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t v[32];
+                    zbp::tmem_ld_32x32b_x32(taddr + c * 32, v);
+                    zbp::tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        sum[c * 16 + i] =
+                            fma2(pk2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), ff, sum[c * 16 + i]);
+                }
+                zbp::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    const uint32_t te = zbp::smem_u32(&ctl->tempty[buf]);
+                    if (PAIR)
+                        zbp::mbar_arrive_cluster(zbp::mapa_shared(te, 0));
+                    else
+                        zbp::mbar_arrive(te);
+                }
             }
+            if (!ok) break;
+            if (live <= 0) continue;
+            const long long at = static_cast<long long>(first + lane) * args.N;
+            // a box of 32 rows by TMA, fewer by each row's thread
+            auto store = [&](const CUtensorMap* tm, __nv_bfloat16* out, int col0, const uint32_t (&w)[16]) {
+                if (live >= 32) {
+                    const uint32_t stg = stg0 + flip * FP8_BOX;
+                    flip ^= 1u;
+                    staging_acquire(lane);
+                    stage_row64(stg, lane, w);
+                    zbp::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        zbp::tma_store_2d(tm, stg, col0, first);
+                        zbp::bulk_commit();
+                    }
+                } else if (lane < live) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (col0 + 8 * k < args.N)
+                            *reinterpret_cast<uint4*>(out + at + col0 + 8 * k) =
+                                make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+                }
+            };
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int col0 = n0 + c * 32;
+                if (col0 >= args.N) break;
+                float x[32];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) up2(sum[c * 16 + i], x[2 * i], x[2 * i + 1]);
+                if (EPI != ZB_FP8_GELU_GRAD && args.bias) {
+                    const __nv_bfloat16* bp = args.bias + static_cast<long long>(walk.e) * args.N + col0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (col0 + 8 * k >= args.N) break;
+                        const uint4 b = *reinterpret_cast<const uint4*>(bp + 8 * k);
+                        const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 f2 = unpack_bf16x2(bw[i]);
+                            x[8 * k + 2 * i] += f2.x;
+                            x[8 * k + 2 * i + 1] += f2.y;
+                        }
+                    }
+                }
+                if (EPI == ZB_FP8_GELU_GRAD) {
+                    uint32_t h[16];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                        if (lane < live && col0 + 8 * k < args.N)
+                            v = __ldg(reinterpret_cast<const uint4*>(args.aux + at + col0 + 8 * k));
+                        h[4 * k] = v.x;
+                        h[4 * k + 1] = v.y;
+                        h[4 * k + 2] = v.z;
+                        h[4 * k + 3] = v.w;
+                    }
+                    if (args.act == ZB_ACT_GELU_TANH)
+                        gelu_grad_mul<true, 32>(x, h);
+                    else
+                        gelu_grad_mul<false, 32>(x, h);
+                }
+                uint32_t w[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+                store(&tmO0, args.out0, col0, w);
+                if (EPI == ZB_FP8_GELU) {
+                    if (args.act == ZB_ACT_GELU_TANH)
+                        gelu_pack<true, 32>(x, w);
+                    else
+                        gelu_pack<false, 32>(x, w);
+                    store(&tmO1, args.out1, col0, w);
+                }
+            }
+        }
+        if (lane == 0) zbp::bulk_wait<0>();
+        __syncwarp();
+    }
+
+    __syncthreads();
+    if (PAIR) zbp::cluster_sync();  // no remote arrivals or copies remain
+    if (warp == 1) {
+        zbp::tc_fence_after();
+        if (PAIR)
+            zbp::tmem_dealloc_pair(tmem_base, TMEM_COLS);
+        else
+            zbp::tmem_dealloc(tmem_base, TMEM_COLS);
     }
 }
 
 // ---------------------------------------------------------------- host side
-bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 bool off4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 
 zb_status launched(const char* who) {
@@ -170,6 +454,37 @@ zb_status launched(const char* who) {
     if (e != cudaSuccess) return zb::fail(ZB_ERR_CUDA, std::string(who) + " launch: " + cudaGetErrorString(e));
     zb::clear_error();
     return ZB_OK;
+}
+
+template <int EPI, int CG>
+zb_status launch_fp8(const CUtensorMap (&mp)[5], const Fp8Args& a, long long tiles, void* stream) {
+    auto kern = zb_fp8_matmul_kernel<EPI, CG>;
+    static std::atomic<int> cache[64];
+    int ctas = 0;
+    zb_status s = full_grid(kern, cache, fp8_smem<CG>(), FP8_THREADS, CG, &ctas);
+    if (s != ZB_OK) return s;
+    LaunchCfg lc(static_cast<int>(std::min<long long>(tiles * CG, ctas)), FP8_THREADS, fp8_smem<CG>(), CG, stream);
+    const cudaError_t e = cudaLaunchKernelEx(&lc.cfg, kern, mp[0], mp[1], mp[2], mp[3], mp[4], a);
+    if (e != cudaSuccess) return zb::fail(ZB_ERR_CUDA, std::string("zb_fp8_matmul launch: ") + cudaGetErrorString(e));
+    return launched("zb_fp8_matmul");
+}
+
+// 2-D map of e4m3 rows, 128 bytes wide boxes, 128-byte swizzle.
+bool make_map8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint32_t box_outer, std::string* why) {
+    EncodeTiledFn fn = encode_fn(why);
+    if (!fn) return false;
+    cuuint64_t dims[2] = {inner, outer};
+    cuuint64_t strides[1] = {inner};
+    cuuint32_t box[2] = {BLK, box_outer};
+    cuuint32_t estr[2] = {1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        if (why) *why = "cuTensorMapEncodeTiled failed with CUresult " + std::to_string(static_cast<int>(r));
+        return false;
+    }
+    return true;
 }
 
 }  // namespace
@@ -236,22 +551,46 @@ extern "C" zb_status zb_fp8_matmul(const zb_fp8_gemm* g, const int32_t* offsets,
     if (off16(offsets) || off16(Xq) || off4(xs) || off16(Wq) || off4(ws) || off16(bias) || off16(H) || off16(out0) ||
         off16(out1))
         return zb::fail(ZB_ERR_ALIGN, "zb_fp8_matmul: pointers must be 16-byte aligned (scales: 4)");
-    MatmulArgs a;
-    a.A = static_cast<const uint8_t*>(Xq);
-    a.B = static_cast<const uint8_t*>(Wq);
-    a.sa = xs;
-    a.sb = ws;
+    // tiles of 256 rows on pairs when they fill the SMs, else 128 (counts as if
+    // the rows were spread evenly)
+    const int64_t used = std::min<int64_t>(g->experts, g->M);
+    const int64_t each = (g->M + used - 1) / used;
+    const long long cols = (g->N + 255) / 256;
+    const bool pair = used * ((each + 255) / 256) * cols >= sm_count() / 2;
+    const int tt = pair ? 256 : 128;
+    const long long most = (g->M / tt + used) * cols;  // no launch has more tiles
+    std::string why;
+    CUtensorMap mp[5];
+    const uint64_t rows = static_cast<uint64_t>(g->M);
+    bool ok = make_map8(&mp[0], Xq, g->K, rows, 128, &why) && make_map8(&mp[1], Xq, g->K, rows, 32, &why) &&
+              make_map3(&mp[2], Wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g->K, g->N, g->experts, BLK, pair ? 128 : 256, &why) &&
+              make_map(&mp[3], out0, false, g->N, rows, g->N, 32, 32, &why, CU_TENSOR_MAP_SWIZZLE_64B) &&
+              make_map(&mp[4], g->epilogue == ZB_FP8_GELU ? out1 : out0, false, g->N, rows, g->N, 32, 32, &why,
+                       CU_TENSOR_MAP_SWIZZLE_64B);
+    if (!ok) return zb::fail(ZB_ERR_CUDA, why);
+    unsigned int* err = zb::device_error_word();
+    if (!err) return ZB_ERR_CUDA;
+    Fp8Args a;
+    a.offsets = offsets;
+    a.xs = xs;
+    a.ws = ws;
     a.bias = static_cast<const __nv_bfloat16*>(bias);
     a.aux = static_cast<const __nv_bfloat16*>(H);
     a.out0 = static_cast<__nv_bfloat16*>(out0);
     a.out1 = static_cast<__nv_bfloat16*>(out1);
-    a.offsets = offsets;
     a.rows = static_cast<int>(g->M);
+    a.experts = g->experts;
     a.N = static_cast<int>(g->N);
     a.K = static_cast<int>(g->K);
-    a.epi = g->epilogue;
     a.act = g->act;
-    const dim3 grid(static_cast<unsigned>((g->N + 63) / 64), static_cast<unsigned>(g->experts), 8);
-    zb_fp8_simple_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
-    return launched("zb_fp8_matmul");
+    a.err = err;
+    switch (g->epilogue) {
+        case ZB_FP8_STORE:
+            return pair ? launch_fp8<ZB_FP8_STORE, 2>(mp, a, most, stream) : launch_fp8<ZB_FP8_STORE, 1>(mp, a, most, stream);
+        case ZB_FP8_GELU:
+            return pair ? launch_fp8<ZB_FP8_GELU, 2>(mp, a, most, stream) : launch_fp8<ZB_FP8_GELU, 1>(mp, a, most, stream);
+        default:
+            return pair ? launch_fp8<ZB_FP8_GELU_GRAD, 2>(mp, a, most, stream)
+                        : launch_fp8<ZB_FP8_GELU_GRAD, 1>(mp, a, most, stream);
+    }
 }

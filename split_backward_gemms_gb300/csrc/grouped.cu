@@ -7,11 +7,10 @@
 #include <atomic>
 #include <string>
 
-#include "gemm_core.cuh"
+#include "grouped.cuh"
 
 namespace {
 
-constexpr int MAX_EXPERTS = 256;
 constexpr int MAX_TOK = 32;  // tokens of one epilogue chunk
 
 // Rows [lo, hi) of expert e, kept inside [0, rows] whatever the offsets say.
@@ -76,53 +75,6 @@ struct RowsArgs {
     unsigned int* err;
 };
 
-// A role's walk over the tiles: tile t of the launch is tile `local` of expert
-// e, which has nt tiles of `tr` rows (the last one fewer) x tiles_f of columns.
-template <int TILE_T>
-struct Walk {
-    const int* off;
-    int experts, tiles_f;
-    int e, first, nt, tr;
-    __device__ Walk(const int* off_, int experts_, int tiles_f_)
-        : off(off_), experts(experts_), tiles_f(tiles_f_), e(-1), first(0), nt(0), tr(0) {}
-    // Moves to tile t (ascending calls); false past the last one.
-    __device__ __forceinline__ bool to(int t, int& row0, int& nrows, int& fb) {
-        while (t >= first + nt * tiles_f) {
-            first += nt * tiles_f;
-            if (++e >= experts) return false;
-            const int n = off[e + 1] - off[e];
-            nt = (n + TILE_T - 1) / TILE_T;
-            tr = nt ? ((n + nt - 1) / nt + 31) / 32 * 32 : 0;
-        }
-        int tb;
-        tile_coords(t - first, nt, tiles_f, 16, tb, fb);
-        row0 = off[e] + tb * tr;
-        nrows = min(tr, off[e + 1] - row0);
-        return true;
-    }
-};
-
-// off[0..experts] in shared memory from the caller's offsets, made legal:
-// inside [0, rows] and ascending (a running maximum, 32 at a time).
-__device__ __forceinline__ void load_offsets(int* off, const int* offsets, int experts, int rows) {
-    if (threadIdx.x < 32) {
-        const int lane = threadIdx.x;
-        int carry = 0;
-        for (int i0 = 0; i0 <= experts; i0 += 32) {
-            const int i = i0 + lane;
-            int v = max(carry, i <= experts ? min(max(offsets[i], 0), rows) : 0);
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int u = __shfl_up_sync(0xffffffffu, v, o);
-                if (lane >= o) v = max(v, u);
-            }
-            if (i <= experts) off[i] = v;
-            carry = __shfl_sync(0xffffffffu, v, 31);
-        }
-    }
-    __syncthreads();
-}
-
 template <int EPI, int A_MN, int CG>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     zb_moe_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA128,
@@ -184,7 +136,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     zbp::allow_dependent_launch();
     load_offsets(ctl->off, args.offsets, args.experts, args.rows);
 
-    Walk<C::TILE_T> walk(ctl->off, args.experts, tiles_f);
+    Walk<C::TILE_T, true> walk(ctl->off, args.experts, tiles_f);
     int row0 = 0, nrows = 0, fb = 0;
     if (warp == 0) {
         if (lane == 0) {
@@ -494,9 +446,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 // so its last block of 64 must not see the next expert's: each expert has
 // tensor maps of its own rows (their start and number set on the device by
 // zb_moe_maps_kernel), and the copies past the last row fill in zeros.  Both
-// operands are read as they lie (MN-major).  The fp32 tile goes out through
-// 32 x 32 staging boxes, added in place by TMA reduce-adds when accumulating
-// (one add per element: no order to vary).
+// operands are read as they lie (MN-major).
+//
+// The tensor core cuts off low bits as it accumulates, so the error of one
+// long accumulator grows with its length (1.4e-6 of the result after ~1024
+// rows, where plain fp32 sums are 3e-7 off).  So an accumulator takes W_SEG
+// blocks of rows only; the 8 epilogue warps (32 lanes x 128 columns each) add
+// the partial sums in registers, rounding to nearest, while the MMAs of the
+// next segment fill the other accumulator.  The fp32 tile goes out through 32 x
+// 32 staging boxes, added in place by TMA reduce-adds when accumulating (one
+// add per element: no order to vary).
+constexpr int W_SEG = 4;  // blocks of 64 rows
 struct MapsArgs {
     const int* offsets;
     int rows, experts, width[4];
@@ -552,14 +512,14 @@ constexpr size_t w_smem() {
 static_assert(w_smem<1>() <= 232448 && w_smem<2>() <= 232448, "shared memory");
 
 template <int CG>
-__global__ void __launch_bounds__(192, 1)
+__global__ void __launch_bounds__(NUM_THREADS, 1)
     zb_moe_wgrad_kernel(const __grid_constant__ CUtensorMap tmO0, const __grid_constant__ CUtensorMap tmO1,
                         const WArgs args) {
     using C = Cfg<CG>;
     constexpr int STAGES = C::STAGES;
     constexpr bool PAIR = CG == 2;
-    constexpr int WARPS = 4;
-    constexpr uint32_t BOX = 32 * 128;
+    constexpr int WARPS = 8;
+    constexpr uint32_t BOX = 32 * 128;  // one staging box a warp
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t* staging = smem + STAGES * C::STAGE_BYTES;
@@ -679,43 +639,48 @@ __global__ void __launch_bounds__(192, 1)
                 locate(tile, e, mb, nb);
                 const int num_kb = blocks_of(e);
                 if (num_kb == 0) continue;
-                const uint32_t buf = local & 1u, tr = local >> 1;
-                ++local;
-                if (!wait_bar<PAIR>(zbp::smem_u32(&ctl->tempty[buf]), (tr & 1u) ^ 1u, abort_flag, args.err,
-                                    ERR_WAIT_MMA, WAIT_LIMIT_NS, true))
-                    break;
-                zbp::tc_fence_after();
-                const uint32_t d_tmem = tmem_base + buf * ACC_COLS;
-                for (int kb = 0; kb < num_kb; ++kb, ++it) {
-                    const uint32_t s = it % STAGES, r = it / STAGES;
-                    if (!wait_bar<PAIR>(zbp::smem_u32(&ctl->full[s]), r & 1u, abort_flag, args.err, ERR_WAIT_MMA,
-                                        WAIT_LIMIT_NS, true)) {
+                for (int kb0 = 0; kb0 < num_kb && ok; kb0 += W_SEG) {
+                    const uint32_t buf = local & 1u, tr = local >> 1;
+                    ++local;
+                    if (!wait_bar<PAIR>(zbp::smem_u32(&ctl->tempty[buf]), (tr & 1u) ^ 1u, abort_flag, args.err,
+                                        ERR_WAIT_MMA, WAIT_LIMIT_NS, true)) {
                         ok = false;
                         break;
                     }
                     zbp::tc_fence_after();
-                    const uint32_t sa = zbp::smem_u32(smem + s * C::STAGE_BYTES);
-                    const uint32_t sb = sa + A_BYTES;
+                    const uint32_t d_tmem = tmem_base + buf * ACC_COLS;
+                    const int kb1 = min(kb0 + W_SEG, num_kb);
+                    for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                        const uint32_t s = it % STAGES, r = it / STAGES;
+                        if (!wait_bar<PAIR>(zbp::smem_u32(&ctl->full[s]), r & 1u, abort_flag, args.err, ERR_WAIT_MMA,
+                                            WAIT_LIMIT_NS, true)) {
+                            ok = false;
+                            break;
+                        }
+                        zbp::tc_fence_after();
+                        const uint32_t sa = zbp::smem_u32(smem + s * C::STAGE_BYTES);
+                        const uint32_t sb = sa + A_BYTES;
 #pragma unroll
-                    for (int kk = 0; kk < BK / 16; ++kk) {
-                        const uint64_t ad = zbp::smem_desc_sw128(sa + kk * 2048, MN_ATOM_BYTES, 1024);
-                        const uint64_t bd = zbp::smem_desc_sw128(sb + kk * 2048, MN_ATOM_BYTES, 1024);
-                        const uint32_t acc = (kb | kk) != 0 ? 1u : 0u;
+                        for (int kk = 0; kk < BK / 16; ++kk) {
+                            const uint64_t ad = zbp::smem_desc_sw128(sa + kk * 2048, MN_ATOM_BYTES, 1024);
+                            const uint64_t bd = zbp::smem_desc_sw128(sb + kk * 2048, MN_ATOM_BYTES, 1024);
+                            const uint32_t acc = (kb != kb0 || kk != 0) ? 1u : 0u;
+                            if (PAIR)
+                                zbp::tc_mma_f16_pair(d_tmem, ad, bd, idesc, acc);
+                            else
+                                zbp::tc_mma_f16(d_tmem, ad, bd, idesc, acc);
+                        }
                         if (PAIR)
-                            zbp::tc_mma_f16_pair(d_tmem, ad, bd, idesc, acc);
+                            zbp::tc_commit_pair_multicast(zbp::smem_u32(&ctl->empty[s]), 0x3);
                         else
-                            zbp::tc_mma_f16(d_tmem, ad, bd, idesc, acc);
+                            zbp::tc_commit(zbp::smem_u32(&ctl->empty[s]));
                     }
+                    if (!ok) break;
                     if (PAIR)
-                        zbp::tc_commit_pair_multicast(zbp::smem_u32(&ctl->empty[s]), 0x3);
+                        zbp::tc_commit_pair_multicast(zbp::smem_u32(&ctl->tfull[buf]), 0x3);
                     else
-                        zbp::tc_commit(zbp::smem_u32(&ctl->empty[s]));
+                        zbp::tc_commit(zbp::smem_u32(&ctl->tfull[buf]));
                 }
-                if (!ok) break;
-                if (PAIR)
-                    zbp::tc_commit_pair_multicast(zbp::smem_u32(&ctl->tfull[buf]), 0x3);
-                else
-                    zbp::tc_commit(zbp::smem_u32(&ctl->tfull[buf]));
             }
             if (PAIR)
                 zbp::tc_commit_pair(zbp::smem_u32(&ctl->drain));
@@ -726,41 +691,60 @@ __global__ void __launch_bounds__(192, 1)
     } else {
         // ---------------------------------------------------- epilogue
         const int ew = warp - 2, q = warp & 3;
-        const uint32_t stg0 = zbp::smem_u32(staging + ew * 2 * BOX);
-        uint32_t flip = 0, local = 0;
-        for (int tile = cluster; tile < num_tiles; tile += clusters) {
+        const int c_lo = (ew >> 2) * (BN / 2);  // this warp's half of the tile's columns
+        const uint32_t stg = zbp::smem_u32(staging + ew * BOX);
+        uint32_t local = 0;
+        bool ok = true;
+        for (int tile = cluster; tile < num_tiles && ok; tile += clusters) {
             int e, mb, nb;
             const int p = locate(tile, e, mb, nb);
-            const bool none = blocks_of(e) == 0;
-            if (none && args.accumulate) continue;
+            const int num_kb = blocks_of(e);
+            if (num_kb == 0 && args.accumulate) continue;
             const int row0 = mb * C::TILE_M + static_cast<int>(rank) * BM + q * 32;
-            const int n0 = nb * BN;
-            const int Mp = args.M[p], Np = args.N[p];
+            const int n0 = nb * BN + c_lo;
+            const int Mp = p ? args.M[1] : args.M[0], Np = p ? args.N[1] : args.N[0];
             const CUtensorMap* tmO = p ? &tmO1 : &tmO0;
-            const uint32_t buf = local & 1u, tr = local >> 1;
-            if (!none) {
+            float sum[BN / 2];
+#pragma unroll
+            for (int i = 0; i < BN / 2; ++i) sum[i] = 0.0f;  // no rows: the gradient is zero
+            for (int kb0 = 0; kb0 < num_kb; kb0 += W_SEG) {
+                const uint32_t buf = local & 1u, tr = local >> 1;
                 ++local;
                 if (!wait_bar<PAIR>(zbp::smem_u32(&ctl->tfull[buf]), tr & 1u, abort_flag, args.err, ERR_WAIT_EPI,
-                                    WAIT_LIMIT_NS, true))
+                                    WAIT_LIMIT_NS, true)) {
+                    ok = false;
                     break;
-                zbp::tc_fence_after();
-            }
-            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * ACC_COLS;
-#pragma unroll 1
-            for (int c = 0; c < BN / 32; ++c) {
-                const int col0 = n0 + c * 32;
-                uint32_t v[32];
-                if (none) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = 0u;  // no rows: the gradient is zero
-                } else {
-                    zbp::tmem_ld_32x32b_x32(taddr + c * 32, v);
-                    zbp::tmem_ld_wait();
                 }
+                zbp::tc_fence_after();
+                const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * ACC_COLS + c_lo;
+#pragma unroll
+                for (int c = 0; c < BN / 32; ++c) {
+                    uint32_t v[16];
+                    zbp::tmem_ld_32x32b_x16(taddr + c * 16, v);
+                    zbp::tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) sum[c * 16 + i] += __uint_as_float(v[i]);
+                }
+                zbp::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    const uint32_t te = zbp::smem_u32(&ctl->tempty[buf]);
+                    if (PAIR)
+                        zbp::mbar_arrive_cluster(zbp::mapa_shared(te, 0));
+                    else
+                        zbp::mbar_arrive(te);
+                }
+            }
+            if (!ok) break;
+#pragma unroll
+            for (int c = 0; c < BN / 64; ++c) {
+                const int col0 = n0 + c * 32;
                 if (row0 >= Mp || col0 >= Np) continue;
-                const uint32_t stg = stg0 + flip * BOX;
-                flip ^= 1u;
-                staging_acquire(lane);
+                uint32_t v[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(sum[c * 32 + i]);
+                if (lane == 0) zbp::bulk_wait_read<0>();  // the box's last store has read it
+                __syncwarp();
                 stage_row(stg, lane, v);
                 zbp::fence_proxy_async_smem();
                 __syncwarp();
@@ -770,17 +754,6 @@ __global__ void __launch_bounds__(192, 1)
                     else
                         zbp::tma_store_3d(tmO, stg, col0, row0, e);
                     zbp::bulk_commit();
-                }
-            }
-            if (!none) {
-                zbp::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    const uint32_t te = zbp::smem_u32(&ctl->tempty[buf]);
-                    if (PAIR)
-                        zbp::mbar_arrive_cluster(zbp::mapa_shared(te, 0));
-                    else
-                        zbp::mbar_arrive(te);
                 }
             }
         }
@@ -821,8 +794,6 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---------------------------------------------------------------- host side
-bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
-
 zb_status check_moe(const zb_moe* m) {
     if (!m) return zb::fail(ZB_ERR_INVALID_ARG, "moe is NULL");
     if (m->flags) return zb::fail(ZB_ERR_INVALID_ARG, "moe.flags must be 0");
@@ -841,81 +812,6 @@ zb_status launched(const char* who) {
     if (e != cudaSuccess) return zb::fail(ZB_ERR_CUDA, std::string(who) + " launch: " + cudaGetErrorString(e));
     return ZB_OK;
 }
-
-// 3-D map of a stack of `count` matrices [outer, inner], dense.
-bool make_map3(CUtensorMap* m, const void* base, bool f32, uint64_t inner, uint64_t outer, uint64_t count,
-               uint32_t box_inner, uint32_t box_outer, std::string* why) {
-    EncodeTiledFn fn = encode_fn(why);
-    if (!fn) return false;
-    const uint64_t es = f32 ? 4 : 2;
-    cuuint64_t dims[3] = {inner, outer, count};
-    cuuint64_t strides[2] = {inner * es, inner * outer * es};
-    cuuint32_t box[3] = {box_inner, box_outer, 1};
-    cuuint32_t estr[3] = {1, 1, 1};
-    const CUresult r = fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-                          const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) {
-        if (why) *why = "cuTensorMapEncodeTiled failed with CUresult " + std::to_string(static_cast<int>(r));
-        return false;
-    }
-    return true;
-}
-
-// Shared-memory limit of a kernel, set once per device, and the CTAs of a
-// full grid of its clusters.
-template <typename K>
-zb_status full_grid(K kern, std::atomic<int>* cache, size_t smem, int threads, int cg, int* ctas) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess || dev < 0 || dev >= 64) return zb::fail(ZB_ERR_CUDA, "cudaGetDevice failed");
-    if (!cache[dev].load(std::memory_order_relaxed)) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-        if (e != cudaSuccess)
-            return zb::fail(ZB_ERR_CUDA, std::string("cudaFuncSetAttribute: ") + cudaGetErrorString(e));
-        int n = sm_count();
-        if (cg == 2) {
-            cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3(512);
-            cfg.blockDim = dim3(threads);
-            cfg.dynamicSmemBytes = smem;
-            cudaLaunchAttribute attr;
-            attr.id = cudaLaunchAttributeClusterDimension;
-            attr.val.clusterDim.x = 2;
-            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-            cfg.attrs = &attr;
-            cfg.numAttrs = 1;
-            int clusters = 0;
-            e = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
-            if (e != cudaSuccess || clusters <= 0)
-                return zb::fail(ZB_ERR_UNSUPPORTED, std::string("no co-resident CTA pairs: ") + cudaGetErrorString(e));
-            n = 2 * clusters;
-        }
-        if (n <= 0) return zb::fail(ZB_ERR_CUDA, "cannot query the SM count");
-        cache[dev].store(n, std::memory_order_relaxed);
-    }
-    *ctas = cache[dev].load(std::memory_order_relaxed);
-    return ZB_OK;
-}
-
-struct LaunchCfg {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[2];
-    LaunchCfg(int grid, int threads, size_t smem, int cg, void* stream) {
-        cfg.gridDim = dim3(static_cast<unsigned>(grid));
-        cfg.blockDim = dim3(static_cast<unsigned>(threads));
-        cfg.dynamicSmemBytes = smem;
-        cfg.stream = static_cast<cudaStream_t>(stream);
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        attr[1].id = cudaLaunchAttributeClusterDimension;
-        attr[1].val.clusterDim.x = cg;
-        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = cg == 2 ? 2 : 1;
-    }
-};
 
 template <int EPI, int A_MN, int CG>
 zb_status launch_rows(const CUtensorMap (&mp)[5], const RowsArgs& a, long long tiles, void* stream) {
@@ -946,11 +842,12 @@ zb_status rows_product(const zb_moe& m, const int32_t* offsets, const void* A, c
     const int tt = pair ? 256 : 128;
     const long long most = (m.rows / tt + used) * ((N + tt - 1) / tt);
 
+    constexpr CUtensorMapDataType BF16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     std::string why;
     CUtensorMap mp[5];
     const uint64_t rows = static_cast<uint64_t>(m.rows);
-    bool ok = transposed ? make_map3(&mp[0], W, false, K, N, m.experts, BK, 128, &why)
-                         : make_map3(&mp[0], W, false, N, K, m.experts, 64, BK, &why);
+    bool ok = transposed ? make_map3(&mp[0], W, BF16, 2, K, N, m.experts, BK, 128, &why)
+                         : make_map3(&mp[0], W, BF16, 2, N, K, m.experts, 64, BK, &why);
     ok = ok && make_map(&mp[1], A, false, K, rows, K, BK, 128, &why);
     ok = ok && make_map(&mp[2], A, false, K, rows, K, BK, 32, &why);
     ok = ok && make_map(&mp[3], out0, false, N, rows, N, 32, 32, &why, CU_TENSOR_MAP_SWIZZLE_64B);
@@ -994,9 +891,9 @@ zb_status launch_wgrad(const CUtensorMap (&mo)[2], const WArgs& a, long long til
     auto kern = zb_moe_wgrad_kernel<CG>;
     static std::atomic<int> cache[64];
     int ctas = 0;
-    zb_status s = full_grid(kern, cache, w_smem<CG>(), 192, CG, &ctas);
+    zb_status s = full_grid(kern, cache, w_smem<CG>(), NUM_THREADS, CG, &ctas);
     if (s != ZB_OK) return s;
-    LaunchCfg lc(static_cast<int>(std::min<long long>(tiles * CG, ctas)), 192, w_smem<CG>(), CG, stream);
+    LaunchCfg lc(static_cast<int>(std::min<long long>(tiles * CG, ctas)), NUM_THREADS, w_smem<CG>(), CG, stream);
     const cudaError_t e = cudaLaunchKernelEx(&lc.cfg, kern, mo[0], mo[1], a);
     if (e != cudaSuccess)
         return zb::fail(ZB_ERR_CUDA, std::string("grouped weight gradient launch: ") + cudaGetErrorString(e));
@@ -1019,7 +916,7 @@ zb_status wgrad(const zb_moe& m, const int32_t* offsets, const WProduct* p, int 
         ma.base[2 * i + 1] = i < products && m.rows ? static_cast<const __nv_bfloat16*>(w.B) : nullptr;
         ma.width[2 * i] = a.M[i] = static_cast<int>(w.M);
         ma.width[2 * i + 1] = a.N[i] = static_cast<int>(w.N);
-        ok = ok && make_map3(&mo[i], w.dW, true, w.N, w.M, m.experts, 32, 32, &why);
+        ok = ok && make_map3(&mo[i], w.dW, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, w.N, w.M, m.experts, 32, 32, &why);
         if (m.rows) {
             ok = ok && make_map(&mi[2 * i], w.A, false, w.M, rows, w.M, 64, BK, &why);
             ok = ok && make_map(&mi[2 * i + 1], w.B, false, w.N, rows, w.N, 64, BK, &why);

@@ -103,6 +103,10 @@ CASES = [
     ([16, 1, 0, 31, 33, 300], 200, 272, "gelu", "tanh", False, 0),
     ([130, 0, 0, 64, 257, 5], 392, 656, "grad", "erf", False, 9),
     ([600, 40, 513], 512, 512, "store", "erf", True, 0),
+    # enough tiles for CTA pairs
+    ([290, 1, 257, 0, 40, 513, 96, 33] * 2, 1288, 144, "grad", "erf", False, 7),
+    ([290, 1, 257, 0, 40, 513, 96, 33] * 2, 1288, 272, "gelu", "erf", True, 0),
+    (2500, 2056, 400, "store", "erf", True, 0),
 ]
 
 
