@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
                 const int n0 = nb * 256 + static_cast<int>(rank) * C::B_ROWS;
                 for (int kb = 0; kb < num_kb; ++kb, ++it) {
                     const uint32_t s = it % STAGES, r = it / STAGES;
-                    if (!wait_bar<PAIR>(zbp::smem_u32(&ctl->empty[s]), (r & 1u) ^ 1u, abort_flag, args.err,
+                    if (!wait_bar<false>(zbp::smem_u32(&ctl->empty[s]), (r & 1u) ^ 1u, abort_flag, args.err,
                                         ERR_WAIT_PRODUCER, WAIT_LIMIT_NS, true)) {
                         ok = false;
                         break;
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
                 // wait for the copies that were issued but may not have landed
                 const uint32_t first = it > STAGES ? it - STAGES : 0;
                 for (uint32_t i = first; i < it; ++i)
-                    wait_bar<PAIR>(zbp::smem_u32(&ctl->full[i % STAGES]), (i / STAGES) & 1u, abort_flag, args.err,
+                    wait_bar<false>(zbp::smem_u32(&ctl->full[i % STAGES]), (i / STAGES) & 1u, abort_flag, args.err,
                                    ERR_WAIT_PRODUCER, DRAIN_LIMIT_NS, false);
             }
         } else if (warp == 1 && lane == 0 && leader) {
@@ -266,9 +266,9 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
                 for (int kb = 0; kb < num_kb; ++kb, ++it) {
                     const uint32_t s = it % STAGES, r = it / STAGES;
                     const uint32_t buf = it & 1u, tr = it >> 1;
-                    if (!wait_bar<PAIR>(zbp::smem_u32(&ctl->full[s]), r & 1u, abort_flag, args.err, ERR_WAIT_MMA,
+                    if (!wait_bar<false>(zbp::smem_u32(&ctl->full[s]), r & 1u, abort_flag, args.err, ERR_WAIT_MMA,
                                         WAIT_LIMIT_NS, true) ||
-                        !wait_bar<PAIR>(zbp::smem_u32(&ctl->tempty[buf]), (tr & 1u) ^ 1u, abort_flag, args.err,
+                        !wait_bar<false>(zbp::smem_u32(&ctl->tempty[buf]), (tr & 1u) ^ 1u, abort_flag, args.err,
                                         ERR_WAIT_MMA, WAIT_LIMIT_NS, true)) {
                         ok = false;
                         break;
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
                 zbp::tc_commit_pair(zbp::smem_u32(&ctl->drain));
             else
                 zbp::tc_commit(zbp::smem_u32(&ctl->drain));
-            wait_bar<PAIR>(zbp::smem_u32(&ctl->drain), 0, abort_flag, args.err, ERR_WAIT_MMA, DRAIN_LIMIT_NS, false);
+            wait_bar<false>(zbp::smem_u32(&ctl->drain), 0, abort_flag, args.err, ERR_WAIT_MMA, DRAIN_LIMIT_NS, false);
         }
     } else {
         // ---------------------------------------------------- epilogue
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
                     wn = __ldg(ws + kb + 1);
                 }
                 const uint32_t buf = it & 1u, tr = it >> 1;
-                if (!wait_bar<PAIR>(zbp::smem_u32(&ctl->tfull[buf]), tr & 1u, abort_flag, args.err, ERR_WAIT_EPI,
+                if (!wait_bar<false>(zbp::smem_u32(&ctl->tfull[buf]), tr & 1u, abort_flag, args.err, ERR_WAIT_EPI,
                                     WAIT_LIMIT_NS, true)) {
                     ok = false;
                     break;
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
                 if (lane == 0) {
                     const uint32_t te = zbp::smem_u32(&ctl->tempty[buf]);
                     if (PAIR)
-                        zbp::mbar_arrive_cluster(zbp::mapa_shared(te, 0));
+                        zbp::mbar_arrive_remote(zbp::mapa_shared(te, 0));
                     else
                         zbp::mbar_arrive(te);
                 }

@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 const uint32_t bytes = CG * (A_BYTES + static_cast<uint32_t>(boxes) * 32u * BK * 2u);
                 for (int kb = 0; kb < num_kb; ++kb, ++it) {
                     const uint32_t s = it % STAGES, r = it / STAGES;
-                    if (!wait_bar<PAIR>(zbp::smem_u32(&ctl->empty[s]), (r & 1u) ^ 1u, abort_flag, args.err,
+                    if (!wait_bar<false>(zbp::smem_u32(&ctl->empty[s]), (r & 1u) ^ 1u, abort_flag, args.err,
                                         ERR_WAIT_PRODUCER, WAIT_LIMIT_NS, true)) {
                         ok = false;
                         break;
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 // wait for the copies that were issued but may not have landed
                 const uint32_t first = it > STAGES ? it - STAGES : 0;
                 for (uint32_t i = first; i < it; ++i)
-                    wait_bar<PAIR>(zbp::smem_u32(&ctl->full[i % STAGES]), (i / STAGES) & 1u, abort_flag, args.err,
+                    wait_bar<false>(zbp::smem_u32(&ctl->full[i % STAGES]), (i / STAGES) & 1u, abort_flag, args.err,
                                    ERR_WAIT_PRODUCER, DRAIN_LIMIT_NS, false);
             }
         }
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             bool ok = true;
             for (int tile = cluster; ok && walk.to(tile, row0, nrows, fb); tile += clusters, ++local) {
                 const uint32_t buf = local & 1u, tr = local >> 1;
-                if (!wait_bar<PAIR>(zbp::smem_u32(&ctl->tempty[buf]), (tr & 1u) ^ 1u, abort_flag, args.err,
+                if (!wait_bar<false>(zbp::smem_u32(&ctl->tempty[buf]), (tr & 1u) ^ 1u, abort_flag, args.err,
                                     ERR_WAIT_MMA, WAIT_LIMIT_NS, true))
                     break;
                 zbp::tc_fence_after();
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 const uint32_t idesc = zbp::idesc_bf16_f32(128 * CG, mma_n, A_MN, 0);
                 for (int kb = 0; kb < num_kb; ++kb, ++it) {
                     const uint32_t s = it % STAGES, r = it / STAGES;
-                    if (!wait_bar<PAIR>(zbp::smem_u32(&ctl->full[s]), r & 1u, abort_flag, args.err, ERR_WAIT_MMA,
+                    if (!wait_bar<false>(zbp::smem_u32(&ctl->full[s]), r & 1u, abort_flag, args.err, ERR_WAIT_MMA,
                                         WAIT_LIMIT_NS, true)) {
                         ok = false;
                         break;
@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 zbp::tc_commit_pair(zbp::smem_u32(&ctl->drain));
             else
                 zbp::tc_commit(zbp::smem_u32(&ctl->drain));
-            wait_bar<PAIR>(zbp::smem_u32(&ctl->drain), 0, abort_flag, args.err, ERR_WAIT_MMA, DRAIN_LIMIT_NS, false);
+            wait_bar<false>(zbp::smem_u32(&ctl->drain), 0, abort_flag, args.err, ERR_WAIT_MMA, DRAIN_LIMIT_NS, false);
         }
     } else {
         // ---------------------------------------------------- epilogue
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     if (n < args.N) bias[i] = __bfloat162float(args.bias[static_cast<long long>(walk.e) * args.N + n]);
                 }
             }
-            if (!wait_bar<PAIR>(zbp::smem_u32(&ctl->tfull[buf]), tr & 1u, abort_flag, args.err, ERR_WAIT_EPI,
+            if (!wait_bar<false>(zbp::smem_u32(&ctl->tfull[buf]), tr & 1u, abort_flag, args.err, ERR_WAIT_EPI,
                                 WAIT_LIMIT_NS, true))
                 break;
             zbp::tc_fence_after();
@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             if (lane == 0) {
                 const uint32_t te = zbp::smem_u32(&ctl->tempty[buf]);
                 if (PAIR)
-                    zbp::mbar_arrive_cluster(zbp::mapa_shared(te, 0));
+                    zbp::mbar_arrive_remote(zbp::mapa_shared(te, 0));
                 else
                     zbp::mbar_arrive(te);
             }
@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 const int nb0 = nb * BN + static_cast<int>(rank) * C::B_ROWS;
                 for (int kb = 0; kb < num_kb; ++kb, ++it) {
                     const uint32_t s = it % STAGES, r = it / STAGES;
-                    if (!wait_bar<PAIR>(zbp::smem_u32(&ctl->empty[s]), (r & 1u) ^ 1u, abort_flag, args.err,
+                    if (!wait_bar<false>(zbp::smem_u32(&ctl->empty[s]), (r & 1u) ^ 1u, abort_flag, args.err,
                                         ERR_WAIT_PRODUCER, WAIT_LIMIT_NS, true)) {
                         ok = false;
                         break;
@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             if (!ok && leader) {
                 const uint32_t first = it > STAGES ? it - STAGES : 0;
                 for (uint32_t i = first; i < it; ++i)
-                    wait_bar<PAIR>(zbp::smem_u32(&ctl->full[i % STAGES]), (i / STAGES) & 1u, abort_flag, args.err,
+                    wait_bar<false>(zbp::smem_u32(&ctl->full[i % STAGES]), (i / STAGES) & 1u, abort_flag, args.err,
                                    ERR_WAIT_PRODUCER, DRAIN_LIMIT_NS, false);
             }
         }
@@ -642,7 +642,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 for (int kb0 = 0; kb0 < num_kb && ok; kb0 += W_SEG) {
                     const uint32_t buf = local & 1u, tr = local >> 1;
                     ++local;
-                    if (!wait_bar<PAIR>(zbp::smem_u32(&ctl->tempty[buf]), (tr & 1u) ^ 1u, abort_flag, args.err,
+                    if (!wait_bar<false>(zbp::smem_u32(&ctl->tempty[buf]), (tr & 1u) ^ 1u, abort_flag, args.err,
                                         ERR_WAIT_MMA, WAIT_LIMIT_NS, true)) {
                         ok = false;
                         break;
@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     const int kb1 = min(kb0 + W_SEG, num_kb);
                     for (int kb = kb0; kb < kb1; ++kb, ++it) {
                         const uint32_t s = it % STAGES, r = it / STAGES;
-                        if (!wait_bar<PAIR>(zbp::smem_u32(&ctl->full[s]), r & 1u, abort_flag, args.err, ERR_WAIT_MMA,
+                        if (!wait_bar<false>(zbp::smem_u32(&ctl->full[s]), r & 1u, abort_flag, args.err, ERR_WAIT_MMA,
                                             WAIT_LIMIT_NS, true)) {
                             ok = false;
                             break;
@@ -686,7 +686,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 zbp::tc_commit_pair(zbp::smem_u32(&ctl->drain));
             else
                 zbp::tc_commit(zbp::smem_u32(&ctl->drain));
-            wait_bar<PAIR>(zbp::smem_u32(&ctl->drain), 0, abort_flag, args.err, ERR_WAIT_MMA, DRAIN_LIMIT_NS, false);
+            wait_bar<false>(zbp::smem_u32(&ctl->drain), 0, abort_flag, args.err, ERR_WAIT_MMA, DRAIN_LIMIT_NS, false);
         }
     } else {
         // ---------------------------------------------------- epilogue
@@ -710,7 +710,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             for (int kb0 = 0; kb0 < num_kb; kb0 += W_SEG) {
                 const uint32_t buf = local & 1u, tr = local >> 1;
                 ++local;
-                if (!wait_bar<PAIR>(zbp::smem_u32(&ctl->tfull[buf]), tr & 1u, abort_flag, args.err, ERR_WAIT_EPI,
+                if (!wait_bar<false>(zbp::smem_u32(&ctl->tfull[buf]), tr & 1u, abort_flag, args.err, ERR_WAIT_EPI,
                                     WAIT_LIMIT_NS, true)) {
                     ok = false;
                     break;
@@ -730,7 +730,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 if (lane == 0) {
                     const uint32_t te = zbp::smem_u32(&ctl->tempty[buf]);
                     if (PAIR)
-                        zbp::mbar_arrive_cluster(zbp::mapa_shared(te, 0));
+                        zbp::mbar_arrive_remote(zbp::mapa_shared(te, 0));
                     else
                         zbp::mbar_arrive(te);
                 }

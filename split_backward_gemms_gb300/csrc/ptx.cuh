@@ -448,6 +448,14 @@ __device__ __forceinline__ void tensormap_set(void* tmap, const void* base, uint
                  ::"l"(reinterpret_cast<uint64_t>(tmap)), "r"(dim1) : "memory");
 }
 
+// Arrive on an mbarrier of another CTA of the cluster where the phase hands
+// over tensor memory only (its loads have completed: tcgen05.wait, then
+// tcgen05.fence::before_thread_sync): no generic memory is released at cluster
+// scope, which would cost a memory barrier for each arrival.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // ---------------------------------------------------------------- transposes
 // 16 TMEM lanes x 32 columns: thread t gets, for each group j of 8 columns,
 // r[4j], r[4j+1] = lane t/4, columns 8j + 2(t%4), +1 and r[4j+2], r[4j+3] =
