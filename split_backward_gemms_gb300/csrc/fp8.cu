@@ -5,6 +5,7 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <cstddef>
 #include <string>
 
 #include "grouped.cuh"
@@ -39,21 +40,50 @@ __device__ __forceinline__ uint8_t to_e4m3(float x) {
     return static_cast<uint8_t>(__nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3));
 }
 
-// One warp per 1 x 128 block.
+// Two values rounded to e4m3 (to nearest, ties to even), the first in the low byte.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+
+// HBM-bound: 3 bytes a value.  16 lanes share a 1 x 128 block (16 bytes each,
+// read once and kept), a warp two neighbouring blocks of Q_ILP row groups, all
+// loads in flight before the first is used.
+constexpr int Q_ILP = 4;
 __global__ void __launch_bounds__(256)
-    zb_fp8_quantize_rows_kernel(const __nv_bfloat16* X, uint8_t* Q, float* S, long long rows, int cols, int blocks) {
-    const long long item = static_cast<long long>(blockIdx.x) * 8 + threadIdx.x / 32;
-    if (item >= rows * blocks) return;
-    const int lane = threadIdx.x % 32;
-    const long long r = item / blocks;
-    const int b = static_cast<int>(item - r * blocks);
-    uint32_t top = 0;
-    for (int c = b * BLK + lane; c < min((b + 1) * BLK, cols); c += 32) top = max(top, magnitude(X[r * cols + c]));
-    float s, inv;
-    block_scale(__uint_as_float(__reduce_max_sync(0xffffffffu, top)), s, inv);
-    for (int c = b * BLK + lane; c < min((b + 1) * BLK, cols); c += 32)
-        Q[r * cols + c] = to_e4m3(__bfloat162float(X[r * cols + c]) * inv);
-    if (lane == 0) S[r * blocks + b] = s;
+    zb_fp8_quantize_rows_kernel(const uint4* __restrict__ X, uint2* __restrict__ Q, float* __restrict__ S,
+                                long long total, int cols8, int blocks) {
+    zbp::allow_dependent_launch();
+    const int lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15;
+    const long long item0 = (static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * 2 * Q_ILP + half;
+    uint4 v[Q_ILP];
+    long long at[Q_ILP], item[Q_ILP];
+#pragma unroll
+    for (int u = 0; u < Q_ILP; ++u) {
+        item[u] = item0 + 2 * u;
+        const long long r = item[u] / blocks;
+        const int c = static_cast<int>(item[u] - r * blocks) * 16 + l;
+        at[u] = item[u] < total && c < cols8 ? r * cols8 + c : -1;
+        v[u] = at[u] >= 0 ? __ldg(X + at[u]) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int u = 0; u < Q_ILP; ++u) {
+        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+        uint32_t top = 0;  // the largest |x| as its bits: NaN above infinity above numbers
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        float s, inv;
+        block_scale(__uint_as_float(top << 16), s, inv);
+        uint32_t q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = unpack_bf16x2(w[i]);
+            q[i] = e4m3x2(f.x * inv, f.y * inv);
+        }
+        if (at[u] >= 0) Q[at[u]] = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
+        if (l == 0 && item[u] < total) S[item[u]] = s;
+    }
 }
 
 // One block of threads per 128 x 128 block.
@@ -93,9 +123,12 @@ __global__ void __launch_bounds__(256)
 // ---------------------------------------------------------------- product
 // D[r, n] = sum_b xs[r, b] ws[n/128, b] P_b[r, n], P_b the product over the
 // b-th block of 128 of K.  The scales change from block to block, so a tensor
-// core accumulator holds one P_b only (4 MMAs of K = 32 into one of two
-// accumulators), and the epilogue warps add xs ws P_b to fp32 sums in registers
-// while the next P_b is computed into the other.  A tile's M side is rows, so
+// core accumulator holds one P_b only (4 MMAs of K = 32), and the epilogue
+// warps add xs ws P_b to fp32 sums in registers while the next is computed.
+// TMEM holds two blocks' results.  They are handed over as four accumulators of
+// 128 columns rather than two of 256: the way round (commit, wake, read,
+// arrive, wake: over 1000 cycles on a pair) then has to fit in three quarters
+// of two blocks' MMA time instead of half.  A tile's M side is rows, so
 // that a thread (one TMEM lane) has one row: its factor xs ws is one scalar for
 // its 128 columns, one packed FMA per two elements.  The tensor core needs 512
 // cycles for a block of a 128 x 256 tile, the FMAs of 8 warps 128 a scheduler,
@@ -105,7 +138,7 @@ __global__ void __launch_bounds__(256)
 // loaded values: more than the 168 of an equal share.
 constexpr int FP8_THREADS = 384;
 constexpr int FP8_EPI_WARPS = 8;
-constexpr int FP8_REGS_LOW = 96, FP8_REGS_HIGH = 200;
+constexpr int FP8_REGS_LOW = 40, FP8_REGS_HIGH = 232;
 static_assert(128 * FP8_REGS_LOW + 256 * FP8_REGS_HIGH <= FP8_THREADS * 168, "register split");
 
 template <int CG>
@@ -114,26 +147,36 @@ struct Fp8Cfg {
     static constexpr int B_ROWS = 256 / CG;                       // columns of D held per CTA
     static constexpr uint32_t A_BYTES8 = 128 * 128;               // 128 rows x 128 k
     static constexpr uint32_t STAGE = A_BYTES8 + B_ROWS * 128;
-    static constexpr int STAGES = CG == 1 ? 4 : 6;
+};
+// GeLU' keeps a warp's 32 x 128 values of H in four staging boxes (copied while
+// the product runs) and stores from them; the others store through two.
+template <int EPI, int CG>
+struct Fp8Epi {
+    static constexpr int BOXES = EPI == ZB_FP8_GELU_GRAD ? 4 : 2;
+    static constexpr int STAGES = CG == 1 ? 3 : EPI == ZB_FP8_GELU_GRAD ? 4 : 5;
 };
 constexpr uint32_t FP8_BOX = 32 * 64;  // 32 rows x 32 columns of bf16
 
 struct Fp8Ctl {
-    uint64_t full[6], empty[6], tfull[2], tempty[2], drain;
+    uint64_t full[6], empty[6], tfull[2], tempty[2], drain[2];
+    uint64_t hbar[FP8_EPI_WARPS];
     uint32_t tmem_base;
     int abort_flag;
     int off[MAX_EXPERTS + 1];
 };
-template <int CG>
+template <int EPI, int CG>
 constexpr size_t fp8_smem() {
-    return 1024 + Fp8Cfg<CG>::STAGES * Fp8Cfg<CG>::STAGE + FP8_EPI_WARPS * 2 * FP8_BOX + sizeof(Fp8Ctl);
+    return 1024 + Fp8Epi<EPI, CG>::STAGES * Fp8Cfg<CG>::STAGE + FP8_EPI_WARPS * Fp8Epi<EPI, CG>::BOXES * FP8_BOX +
+           sizeof(Fp8Ctl);
 }
-static_assert(fp8_smem<1>() <= 232448 && fp8_smem<2>() <= 232448, "shared memory");
+static_assert(fp8_smem<ZB_FP8_STORE, 1>() <= 232448 && fp8_smem<ZB_FP8_STORE, 2>() <= 232448 &&
+                  fp8_smem<ZB_FP8_GELU_GRAD, 1>() <= 232448 && fp8_smem<ZB_FP8_GELU_GRAD, 2>() <= 232448,
+              "shared memory");
 
 struct Fp8Args {
     const int* offsets;  // nullptr: one expert with every row
     const float *xs, *ws;
-    const __nv_bfloat16 *bias, *aux;
+    const __nv_bfloat16* bias;
     __nv_bfloat16 *out0, *out1;
     int rows, experts, N, K, act;
     unsigned int* err;
@@ -146,11 +189,13 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
                          const __grid_constant__ CUtensorMap tmO1, const Fp8Args args) {
     using C = Fp8Cfg<CG>;
     constexpr bool PAIR = CG == 2;
-    constexpr int STAGES = C::STAGES;
+    constexpr int STAGES = Fp8Epi<EPI, CG>::STAGES;
+    constexpr int BOXES = Fp8Epi<EPI, CG>::BOXES;
+    constexpr bool GRAD = EPI == ZB_FP8_GELU_GRAD;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t* staging = smem + STAGES * C::STAGE;
-    Fp8Ctl* ctl = reinterpret_cast<Fp8Ctl*>(staging + FP8_EPI_WARPS * 2 * FP8_BOX);
+    Fp8Ctl* ctl = reinterpret_cast<Fp8Ctl*>(staging + FP8_EPI_WARPS * BOXES * FP8_BOX);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = PAIR ? zbp::cluster_ctarank() : 0u;
@@ -168,15 +213,17 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
         for (int b = 0; b < 2; ++b) {
             zbp::mbar_init(zbp::smem_u32(&ctl->tfull[b]), 1);
             zbp::mbar_init(zbp::smem_u32(&ctl->tempty[b]), FP8_EPI_WARPS * CG);
+            zbp::mbar_init(zbp::smem_u32(&ctl->drain[b]), 1);
         }
-        zbp::mbar_init(zbp::smem_u32(&ctl->drain), 1);
+        if (GRAD)
+            for (int w = 0; w < FP8_EPI_WARPS; ++w) zbp::mbar_init(zbp::smem_u32(&ctl->hbar[w]), 1);
         ctl->abort_flag = 0;
         zbp::fence_mbar_init();
         zbp::tma_prefetch_desc(&tmA128);
         zbp::tma_prefetch_desc(&tmA32);
         zbp::tma_prefetch_desc(&tmB);
         zbp::tma_prefetch_desc(&tmO0);
-        if (EPI == ZB_FP8_GELU) zbp::tma_prefetch_desc(&tmO1);
+        if (EPI != ZB_FP8_STORE) zbp::tma_prefetch_desc(&tmO1);
     }
     if (warp == 1) {
         if (PAIR) {
@@ -257,62 +304,83 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
                     wait_bar<false>(zbp::smem_u32(&ctl->full[i % STAGES]), (i / STAGES) & 1u, abort_flag, args.err,
                                    ERR_WAIT_PRODUCER, DRAIN_LIMIT_NS, false);
             }
-        } else if (warp == 1 && lane == 0 && leader) {
-            // ------------------------------------------------ MMA issuer
+        } else if ((warp == 1 || warp == 2) && lane == 0 && leader) {
+            // ------------------------------------------------ MMA issuers
+            // Warp 1 issues the even blocks of K (into accumulator 0), warp 2
+            // the odd ones: a block's two waits, four MMAs and two commits take
+            // one thread longer than the 512 cycles of its MMAs.
             constexpr uint32_t idesc = zbp::idesc_e4m3_f32(128 * CG, 256);
-            uint32_t it = 0;  // stage and accumulator: one block of K each
+            constexpr uint32_t hi = zbp::desc_hi(1024);
+            const uint32_t buf = static_cast<uint32_t>(warp - 1);
+            const uint32_t d_tmem = tmem_base + buf * ACC_COLS;
+            const uint32_t lo0 = zbp::desc_lo(zbp::smem_u32(smem), 16);
+            const uint32_t full0 = zbp::smem_u32(&ctl->full[0]), empty0 = zbp::smem_u32(&ctl->empty[0]);
+            const uint32_t tfull = zbp::smem_u32(&ctl->tfull[buf]), tempty = zbp::smem_u32(&ctl->tempty[buf]);
+            uint32_t s = buf, sp = 0;  // stage and its phase
+            uint32_t tp = 1;           // phase of the accumulator's last release
+            int k = static_cast<int>(buf);  // next block, counted from the tile's first
             bool ok = true;
             for (int tile = cluster; ok && walk.to(tile, row0, nrows, nb); tile += clusters) {
-                for (int kb = 0; kb < num_kb; ++kb, ++it) {
-                    const uint32_t s = it % STAGES, r = it / STAGES;
-                    const uint32_t buf = it & 1u, tr = it >> 1;
-                    if (!wait_bar<false>(zbp::smem_u32(&ctl->full[s]), r & 1u, abort_flag, args.err, ERR_WAIT_MMA,
-                                        WAIT_LIMIT_NS, true) ||
-                        !wait_bar<false>(zbp::smem_u32(&ctl->tempty[buf]), (tr & 1u) ^ 1u, abort_flag, args.err,
-                                        ERR_WAIT_MMA, WAIT_LIMIT_NS, true)) {
+                for (; k < num_kb; k += 2) {
+                    if (!wait_bar<false>(tempty, tp, abort_flag, args.err, ERR_WAIT_MMA, WAIT_LIMIT_NS, true) ||
+                        !wait_bar<false>(full0 + s * 8u, sp, abort_flag, args.err, ERR_WAIT_MMA, WAIT_LIMIT_NS, true)) {
                         ok = false;
                         break;
                     }
+                    tp ^= 1u;
                     zbp::tc_fence_after();
-                    const uint32_t sa = zbp::smem_u32(smem + s * C::STAGE);
-                    const uint32_t sb = sa + C::A_BYTES8;
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        const uint64_t ad = zbp::smem_desc_sw128(sa + kk * 32, 16, 1024);
-                        const uint64_t bd = zbp::smem_desc_sw128(sb + kk * 32, 16, 1024);
-                        if (PAIR)
-                            zbp::tc_mma_f8_pair(tmem_base + buf * ACC_COLS, ad, bd, idesc, kk != 0);
-                        else
-                            zbp::tc_mma_f8(tmem_base + buf * ACC_COLS, ad, bd, idesc, kk != 0);
-                    }
+                    const uint32_t a = lo0 + s * (C::STAGE >> 4), b = a + (C::A_BYTES8 >> 4);
                     if (PAIR) {
-                        zbp::tc_commit_pair_multicast(zbp::smem_u32(&ctl->empty[s]), 0x3);
-                        zbp::tc_commit_pair_multicast(zbp::smem_u32(&ctl->tfull[buf]), 0x3);
+                        zbp::mma4_f8_pair<2, 2>(d_tmem, a, hi, b, hi, idesc, 0);
+                        zbp::tc_commit_pair_multicast(tfull, 0x3);
+                        zbp::tc_commit_pair_multicast(empty0 + s * 8u, 0x3);
                     } else {
-                        zbp::tc_commit(zbp::smem_u32(&ctl->empty[s]));
-                        zbp::tc_commit(zbp::smem_u32(&ctl->tfull[buf]));
+                        zbp::mma4_f8<2, 2>(d_tmem, a, hi, b, hi, idesc, 0);
+                        zbp::tc_commit(tfull);
+                        zbp::tc_commit(empty0 + s * 8u);
+                    }
+                    s += 2;
+                    if (s >= STAGES) {
+                        s -= STAGES;
+                        sp ^= 1u;
                     }
                 }
+                k -= num_kb;
             }
             // every MMA issued here completes before TMEM is released
+            const uint32_t drain = zbp::smem_u32(&ctl->drain[buf]);
             if (PAIR)
-                zbp::tc_commit_pair(zbp::smem_u32(&ctl->drain));
+                zbp::tc_commit_pair(drain);
             else
-                zbp::tc_commit(zbp::smem_u32(&ctl->drain));
-            wait_bar<false>(zbp::smem_u32(&ctl->drain), 0, abort_flag, args.err, ERR_WAIT_MMA, DRAIN_LIMIT_NS, false);
+                zbp::tc_commit(drain);
+            wait_bar<false>(drain, 0, abort_flag, args.err, ERR_WAIT_MMA, DRAIN_LIMIT_NS, false);
         }
     } else {
         // ---------------------------------------------------- epilogue
         zbp::regs_inc<FP8_REGS_HIGH>();
         const int ew = warp - 4, q = warp & 3;
         const int c_lo = (ew >> 2) * 128;  // this warp's half of the tile's columns: one block of 128
-        const uint32_t stg0 = zbp::smem_u32(staging + ew * 2 * FP8_BOX);
+        const uint32_t stg0 = zbp::smem_u32(staging + ew * BOXES * FP8_BOX);
         uint32_t it = 0, flip = 0;
+        uint32_t asked = 0, taken = 0;  // tiles whose H was asked for and read
         bool ok = true;
         for (int tile = cluster; ok && walk.to(tile, row0, nrows, nb); tile += clusters) {
             const int first = row0 + static_cast<int>(rank) * 128 + q * 32;  // the warp's first row
             const int live = row0 + nrows - first;                           // its live rows
             const int n0 = nb * 256 + c_lo;
+            if (GRAD && live > 0 && n0 < args.N) {
+                // this warp's values of H, into the boxes of its last tile
+                zbp::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    zbp::bulk_wait_read<0>();
+                    const uint32_t bar = zbp::smem_u32(&ctl->hbar[ew]);
+                    zbp::mbar_arrive_expect_tx(bar, 4 * FP8_BOX);  // columns past the edge: zeros
+                    for (int c = 0; c < 4; ++c)
+                        zbp::tma_load_2d(stg0 + static_cast<uint32_t>(c) * FP8_BOX, &tmO1, bar, n0 + 32 * c, first);
+                }
+                ++asked;
+            }
             const bool scaled = lane < live && n0 < args.N;
             const float* xs = args.xs + static_cast<long long>(scaled ? first + lane : 0) * num_kb;
             const float* ws = args.ws + (static_cast<long long>(walk.e) * n_blocks + (scaled ? n0 / BLK : 0)) * num_kb;
@@ -320,15 +388,16 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 64; ++i) sum[i] = 0ull;
             float xn = scaled ? __ldg(xs) : 0.0f, wn = scaled ? __ldg(ws) : 0.0f;
+#pragma unroll 1
             for (int kb = 0; kb < num_kb; ++kb, ++it) {
                 const float f = xn * wn;
                 if (scaled && kb + 1 < num_kb) {
                     xn = __ldg(xs + kb + 1);
                     wn = __ldg(ws + kb + 1);
                 }
-                const uint32_t buf = it & 1u, tr = it >> 1;
-                if (!wait_bar<false>(zbp::smem_u32(&ctl->tfull[buf]), tr & 1u, abort_flag, args.err, ERR_WAIT_EPI,
-                                    WAIT_LIMIT_NS, true)) {
+                const uint32_t buf = it & 1u;
+                if (!wait_bar<false>(zbp::smem_u32(&ctl->tfull[buf]), (it >> 1) & 1u, abort_flag, args.err, ERR_WAIT_EPI,
+                                     WAIT_LIMIT_NS, true)) {
                     ok = false;
                     break;
                 }
@@ -336,14 +405,14 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
                 const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * ACC_COLS + c_lo;
                 const f32x2 ff = pk2(f, f);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t v[32];
-                    zbp::tmem_ld_32x32b_x32(taddr + c * 32, v);
+                for (int c = 0; c < 8; ++c) {
+                    uint32_t v[16];
+                    zbp::tmem_ld_32x32b_x16(taddr + c * 16, v);
                     zbp::tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        sum[c * 16 + i] =
-                            fma2(pk2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), ff, sum[c * 16 + i]);
+                    for (int i = 0; i < 8; ++i)
+                        sum[c * 8 + i] =
+                            fma2(pk2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), ff, sum[c * 8 + i]);
                 }
                 zbp::tc_fence_before();
                 __syncwarp();
@@ -356,14 +425,21 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
                 }
             }
             if (!ok) break;
-            if (live <= 0) continue;
+            if (live <= 0 || n0 >= args.N) continue;
+            if (GRAD) {
+                if (!wait_bar<false>(zbp::smem_u32(&ctl->hbar[ew]), taken & 1u, abort_flag, args.err, ERR_WAIT_EPI,
+                                     WAIT_LIMIT_NS, true))
+                    break;
+                ++taken;
+            }
             const long long at = static_cast<long long>(first + lane) * args.N;
             // a box of 32 rows by TMA, fewer by each row's thread
-            auto store = [&](const CUtensorMap* tm, __nv_bfloat16* out, int col0, const uint32_t (&w)[16]) {
+            auto store = [&](const CUtensorMap* tm, __nv_bfloat16* out, int c, const uint32_t (&w)[16]) {
+                const int col0 = n0 + c * 32;
                 if (live >= 32) {
-                    const uint32_t stg = stg0 + flip * FP8_BOX;
+                    const uint32_t stg = stg0 + (GRAD ? static_cast<uint32_t>(c) : flip) * FP8_BOX;
                     flip ^= 1u;
-                    staging_acquire(lane);
+                    if (!GRAD) staging_acquire(lane);  // GeLU': a lane replaces its own row of H
                     stage_row64(stg, lane, w);
                     zbp::fence_proxy_async_smem();
                     __syncwarp();
@@ -382,7 +458,7 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const int col0 = n0 + c * 32;
-                if (col0 >= args.N) break;
+                if (col0 >= args.N) continue;
                 float x[32];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) up2(sum[c * 16 + i], x[2 * i], x[2 * i + 1]);
@@ -405,13 +481,12 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
                     uint32_t h[16];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                        if (lane < live && col0 + 8 * k < args.N)
-                            v = __ldg(reinterpret_cast<const uint4*>(args.aux + at + col0 + 8 * k));
-                        h[4 * k] = v.x;
-                        h[4 * k + 1] = v.y;
-                        h[4 * k + 2] = v.z;
-                        h[4 * k + 3] = v.w;
+                        const float4 v = zbp::ld_shared_v4(stg0 + static_cast<uint32_t>(c) * FP8_BOX +
+                                                           static_cast<uint32_t>(lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)));
+                        h[4 * k] = __float_as_uint(v.x);
+                        h[4 * k + 1] = __float_as_uint(v.y);
+                        h[4 * k + 2] = __float_as_uint(v.z);
+                        h[4 * k + 3] = __float_as_uint(v.w);
                     }
                     if (args.act == ZB_ACT_GELU_TANH)
                         gelu_grad_mul<true, 32>(x, h);
@@ -421,16 +496,19 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
                 uint32_t w[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-                store(&tmO0, args.out0, col0, w);
+                store(&tmO0, args.out0, c, w);
                 if (EPI == ZB_FP8_GELU) {
                     if (args.act == ZB_ACT_GELU_TANH)
                         gelu_pack<true, 32>(x, w);
                     else
                         gelu_pack<false, 32>(x, w);
-                    store(&tmO1, args.out1, col0, w);
+                    store(&tmO1, args.out1, c, w);
                 }
             }
         }
+        if (GRAD && asked != taken)  // H asked for and not read (after an abort)
+            wait_bar<false>(zbp::smem_u32(&ctl->hbar[ew]), taken & 1u, abort_flag, args.err, ERR_WAIT_EPI, DRAIN_LIMIT_NS,
+                            false);
         if (lane == 0) zbp::bulk_wait<0>();
         __syncwarp();
     }
@@ -461,9 +539,9 @@ zb_status launch_fp8(const CUtensorMap (&mp)[5], const Fp8Args& a, long long til
     auto kern = zb_fp8_matmul_kernel<EPI, CG>;
     static std::atomic<int> cache[64];
     int ctas = 0;
-    zb_status s = full_grid(kern, cache, fp8_smem<CG>(), FP8_THREADS, CG, &ctas);
+    zb_status s = full_grid(kern, cache, fp8_smem<EPI, CG>(), FP8_THREADS, CG, &ctas);
     if (s != ZB_OK) return s;
-    LaunchCfg lc(static_cast<int>(std::min<long long>(tiles * CG, ctas)), FP8_THREADS, fp8_smem<CG>(), CG, stream);
+    LaunchCfg lc(static_cast<int>(std::min<long long>(tiles * CG, ctas)), FP8_THREADS, fp8_smem<EPI, CG>(), CG, stream);
     const cudaError_t e = cudaLaunchKernelEx(&lc.cfg, kern, mp[0], mp[1], mp[2], mp[3], mp[4], a);
     if (e != cudaSuccess) return zb::fail(ZB_ERR_CUDA, std::string("zb_fp8_matmul launch: ") + cudaGetErrorString(e));
     return launched("zb_fp8_matmul");
@@ -501,10 +579,11 @@ extern "C" zb_status zb_fp8_quantize_rows(int64_t rows, int64_t cols, const void
     if (off16(X) || off16(Q) || off4(S))
         return zb::fail(ZB_ERR_ALIGN, "zb_fp8_quantize_rows: pointers must be 16-byte aligned (S: 4)");
     const int blocks = static_cast<int>((cols + BLK - 1) / BLK);
-    const long long grid = (rows * blocks + 7) / 8;
+    const long long per = 8 * 2 * Q_ILP;  // blocks of 128 in a thread block
+    const long long grid = (rows * blocks + per - 1) / per;
     if (grid > 0x7fffffffLL) return zb::fail(ZB_ERR_SHAPE, "zb_fp8_quantize_rows: too many elements");
     zb_fp8_quantize_rows_kernel<<<static_cast<unsigned>(grid), 256, 0, static_cast<cudaStream_t>(stream)>>>(
-        static_cast<const __nv_bfloat16*>(X), static_cast<uint8_t*>(Q), S, rows, static_cast<int>(cols), blocks);
+        static_cast<const uint4*>(X), static_cast<uint2*>(Q), S, rows * blocks, static_cast<int>(cols / 8), blocks);
     return launched("zb_fp8_quantize_rows");
 }
 
@@ -565,7 +644,7 @@ extern "C" zb_status zb_fp8_matmul(const zb_fp8_gemm* g, const int32_t* offsets,
     bool ok = make_map8(&mp[0], Xq, g->K, rows, 128, &why) && make_map8(&mp[1], Xq, g->K, rows, 32, &why) &&
               make_map3(&mp[2], Wq, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g->K, g->N, g->experts, BLK, pair ? 128 : 256, &why) &&
               make_map(&mp[3], out0, false, g->N, rows, g->N, 32, 32, &why, CU_TENSOR_MAP_SWIZZLE_64B) &&
-              make_map(&mp[4], g->epilogue == ZB_FP8_GELU ? out1 : out0, false, g->N, rows, g->N, 32, 32, &why,
+              make_map(&mp[4], g->epilogue == ZB_FP8_GELU ? out1 : g->epilogue == ZB_FP8_GELU_GRAD ? H : out0, false, g->N, rows, g->N, 32, 32, &why,
                        CU_TENSOR_MAP_SWIZZLE_64B);
     if (!ok) return zb::fail(ZB_ERR_CUDA, why);
     unsigned int* err = zb::device_error_word();
@@ -575,7 +654,6 @@ extern "C" zb_status zb_fp8_matmul(const zb_fp8_gemm* g, const int32_t* offsets,
     a.xs = xs;
     a.ws = ws;
     a.bias = static_cast<const __nv_bfloat16*>(bias);
-    a.aux = static_cast<const __nv_bfloat16*>(H);
     a.out0 = static_cast<__nv_bfloat16*>(out0);
     a.out1 = static_cast<__nv_bfloat16*>(out1);
     a.rows = static_cast<int>(g->M);

@@ -199,42 +199,38 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     } else if (warp == 1) {
         if (lane == 0 && leader) {
             // ------------------------------------------------ MMA issuer
-            uint32_t it = 0, local = 0;
+            constexpr uint32_t A_STEP = A_MN ? 2048 >> 4 : 32 >> 4, hi = zbp::desc_hi(1024);
+            const uint32_t a0 = zbp::desc_lo(zbp::smem_u32(smem), A_MN ? MN_ATOM_BYTES : 16);
+            const uint32_t b0 = zbp::desc_lo(zbp::smem_u32(smem) + A_BYTES, 16);
+            const uint32_t full0 = zbp::smem_u32(&ctl->full[0]), empty0 = zbp::smem_u32(&ctl->empty[0]);
+            uint32_t s = 0, sp = 0, local = 0;  // stage and its phase; tile
             bool ok = true;
             for (int tile = cluster; ok && walk.to(tile, row0, nrows, fb); tile += clusters, ++local) {
                 const uint32_t buf = local & 1u, tr = local >> 1;
                 if (!wait_bar<false>(zbp::smem_u32(&ctl->tempty[buf]), (tr & 1u) ^ 1u, abort_flag, args.err,
-                                    ERR_WAIT_MMA, WAIT_LIMIT_NS, true))
+                                     ERR_WAIT_MMA, WAIT_LIMIT_NS, true))
                     break;
-                zbp::tc_fence_after();
                 const uint32_t d_tmem = tmem_base + buf * C::TILE_T;
                 const uint32_t mma_n = static_cast<uint32_t>((nrows + C::N_STEP - 1) / C::N_STEP * C::N_STEP);
                 const uint32_t idesc = zbp::idesc_bf16_f32(128 * CG, mma_n, A_MN, 0);
-                for (int kb = 0; kb < num_kb; ++kb, ++it) {
-                    const uint32_t s = it % STAGES, r = it / STAGES;
-                    if (!wait_bar<false>(zbp::smem_u32(&ctl->full[s]), r & 1u, abort_flag, args.err, ERR_WAIT_MMA,
-                                        WAIT_LIMIT_NS, true)) {
+                for (int kb = 0; kb < num_kb; ++kb) {
+                    if (!wait_bar<false>(full0 + s * 8u, sp, abort_flag, args.err, ERR_WAIT_MMA, WAIT_LIMIT_NS, true)) {
                         ok = false;
                         break;
                     }
                     zbp::tc_fence_after();
-                    const uint32_t sa = zbp::smem_u32(smem + s * C::STAGE);
-                    const uint32_t sb = sa + A_BYTES;
-#pragma unroll
-                    for (int kk = 0; kk < BK / 16; ++kk) {
-                        const uint64_t ad = A_MN ? zbp::smem_desc_sw128(sa + kk * 2048, MN_ATOM_BYTES, 1024)
-                                                 : zbp::smem_desc_sw128(sa + kk * 32, 16, 1024);
-                        const uint64_t bd = zbp::smem_desc_sw128(sb + kk * 32, 16, 1024);
-                        const uint32_t acc = (kb | kk) != 0 ? 1u : 0u;
-                        if (PAIR)
-                            zbp::tc_mma_f16_pair(d_tmem, ad, bd, idesc, acc);
-                        else
-                            zbp::tc_mma_f16(d_tmem, ad, bd, idesc, acc);
+                    const uint32_t off = s * (C::STAGE >> 4);
+                    if (PAIR) {
+                        zbp::mma4_f16_pair<A_STEP, 2>(d_tmem, a0 + off, hi, b0 + off, hi, idesc, kb != 0);
+                        zbp::tc_commit_pair_multicast(empty0 + s * 8u, 0x3);
+                    } else {
+                        zbp::mma4_f16<A_STEP, 2>(d_tmem, a0 + off, hi, b0 + off, hi, idesc, kb != 0);
+                        zbp::tc_commit(empty0 + s * 8u);
                     }
-                    if (PAIR)
-                        zbp::tc_commit_pair_multicast(zbp::smem_u32(&ctl->empty[s]), 0x3);
-                    else
-                        zbp::tc_commit(zbp::smem_u32(&ctl->empty[s]));
+                    if (++s == STAGES) {
+                        s = 0;
+                        sp ^= 1u;
+                    }
                 }
                 if (!ok) break;
                 if (PAIR)
@@ -632,48 +628,43 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (lane == 0 && leader) {
             // ------------------------------------------------ MMA issuer
             constexpr uint32_t idesc = zbp::idesc_bf16_f32(BM * CG, BN, 1, 1);
-            uint32_t it = 0, local = 0;
+            constexpr uint32_t hi = zbp::desc_hi(1024);
+            const uint32_t a0 = zbp::desc_lo(zbp::smem_u32(smem), MN_ATOM_BYTES);
+            const uint32_t full0 = zbp::smem_u32(&ctl->full[0]), empty0 = zbp::smem_u32(&ctl->empty[0]);
+            uint32_t s = 0, sp = 0, local = 0;  // stage and its phase; segment
             bool ok = true;
             for (int tile = cluster; tile < num_tiles && ok; tile += clusters) {
                 int e, mb, nb;
                 locate(tile, e, mb, nb);
                 const int num_kb = blocks_of(e);
-                if (num_kb == 0) continue;
                 for (int kb0 = 0; kb0 < num_kb && ok; kb0 += W_SEG) {
                     const uint32_t buf = local & 1u, tr = local >> 1;
                     ++local;
                     if (!wait_bar<false>(zbp::smem_u32(&ctl->tempty[buf]), (tr & 1u) ^ 1u, abort_flag, args.err,
-                                        ERR_WAIT_MMA, WAIT_LIMIT_NS, true)) {
+                                         ERR_WAIT_MMA, WAIT_LIMIT_NS, true)) {
                         ok = false;
                         break;
                     }
-                    zbp::tc_fence_after();
                     const uint32_t d_tmem = tmem_base + buf * ACC_COLS;
                     const int kb1 = min(kb0 + W_SEG, num_kb);
-                    for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                        const uint32_t s = it % STAGES, r = it / STAGES;
-                        if (!wait_bar<false>(zbp::smem_u32(&ctl->full[s]), r & 1u, abort_flag, args.err, ERR_WAIT_MMA,
-                                            WAIT_LIMIT_NS, true)) {
+                    for (int kb = kb0; kb < kb1; ++kb) {
+                        if (!wait_bar<false>(full0 + s * 8u, sp, abort_flag, args.err, ERR_WAIT_MMA, WAIT_LIMIT_NS, true)) {
                             ok = false;
                             break;
                         }
                         zbp::tc_fence_after();
-                        const uint32_t sa = zbp::smem_u32(smem + s * C::STAGE_BYTES);
-                        const uint32_t sb = sa + A_BYTES;
-#pragma unroll
-                        for (int kk = 0; kk < BK / 16; ++kk) {
-                            const uint64_t ad = zbp::smem_desc_sw128(sa + kk * 2048, MN_ATOM_BYTES, 1024);
-                            const uint64_t bd = zbp::smem_desc_sw128(sb + kk * 2048, MN_ATOM_BYTES, 1024);
-                            const uint32_t acc = (kb != kb0 || kk != 0) ? 1u : 0u;
-                            if (PAIR)
-                                zbp::tc_mma_f16_pair(d_tmem, ad, bd, idesc, acc);
-                            else
-                                zbp::tc_mma_f16(d_tmem, ad, bd, idesc, acc);
+                        const uint32_t a = a0 + s * (C::STAGE_BYTES >> 4), b = a + (A_BYTES >> 4);
+                        if (PAIR) {
+                            zbp::mma4_f16_pair<128, 128>(d_tmem, a, hi, b, hi, idesc, kb != kb0);
+                            zbp::tc_commit_pair_multicast(empty0 + s * 8u, 0x3);
+                        } else {
+                            zbp::mma4_f16<128, 128>(d_tmem, a, hi, b, hi, idesc, kb != kb0);
+                            zbp::tc_commit(empty0 + s * 8u);
                         }
-                        if (PAIR)
-                            zbp::tc_commit_pair_multicast(zbp::smem_u32(&ctl->empty[s]), 0x3);
-                        else
-                            zbp::tc_commit(zbp::smem_u32(&ctl->empty[s]));
+                        if (++s == STAGES) {
+                            s = 0;
+                            sp ^= 1u;
+                        }
                     }
                     if (!ok) break;
                     if (PAIR)

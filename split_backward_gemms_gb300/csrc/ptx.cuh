@@ -497,25 +497,6 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t& a, ui
 namespace zbp {
 
 // ---------------------------------------------------------------- 8 bits
-// D[tmem] (+)= A[smem desc] x B[smem desc], kind::f8f6f4 (K = 32 a call).
-__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                          uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-__device__ __forceinline__ void tc_mma_f8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                               uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
 // Instruction descriptor of kind::f8f6f4: D fp32, A and B e4m3 (format 0),
 // both K-major.
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N) {
@@ -530,6 +511,121 @@ __device__ __forceinline__ void regs_inc() {
 template <int N>
 __device__ __forceinline__ void regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+}  // namespace zbp
+
+namespace zbp {
+
+// ---------------------------------------------------------------- K blocks
+// Low and high words of smem_desc_sw128.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) {
+    return ((saddr & 0x3FFFFu) >> 4) | ((lbo_bytes >> 4) << 16);
+}
+__host__ __device__ constexpr uint32_t desc_hi(uint32_t sbo_bytes) { return (sbo_bytes >> 4) | (1u << 14) | (2u << 29); }
+
+// Four f16 MMAs along K: D (+)= sum_i A_i x B_i, the operands' descriptors
+// given as low and high words, the low ones A_STEP and B_STEP (16-byte units)
+// apart.  The first one adds to D if `accumulate`.  One thread issues every
+// MMA of an SM (or pair), so its instructions between two MMAs bound the rate.
+template <int A_STEP, int B_STEP>
+__device__ __forceinline__ void mma4_f16(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                       uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t.reg .b32 x, y;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t"
+        "add.u32 x, %1, %7;\n\tadd.u32 y, %3, %8;\n\t"
+        "mov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, 1;\n\t"
+        "add.u32 x, %1, %9;\n\tadd.u32 y, %3, %10;\n\t"
+        "mov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, 1;\n\t"
+        "add.u32 x, %1, %11;\n\tadd.u32 y, %3, %12;\n\t"
+        "mov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, 1;\n\t}"
+        ::"r"(d_tmem), "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "n"(A_STEP),
+          "n"(B_STEP), "n"(2 * A_STEP), "n"(2 * B_STEP), "n"(3 * A_STEP), "n"(3 * B_STEP)
+        : "memory");
+}
+
+// Four f16 MMAs along K: D (+)= sum_i A_i x B_i, the operands' descriptors
+// given as low and high words, the low ones A_STEP and B_STEP (16-byte units)
+// apart.  The first one adds to D if `accumulate`.  One thread issues every
+// MMA of an SM (or pair), so its instructions between two MMAs bound the rate.
+template <int A_STEP, int B_STEP>
+__device__ __forceinline__ void mma4_f16_pair(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                       uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t.reg .b32 x, y;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n\t"
+        "add.u32 x, %1, %7;\n\tadd.u32 y, %3, %8;\n\t"
+        "mov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, 1;\n\t"
+        "add.u32 x, %1, %9;\n\tadd.u32 y, %3, %10;\n\t"
+        "mov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, 1;\n\t"
+        "add.u32 x, %1, %11;\n\tadd.u32 y, %3, %12;\n\t"
+        "mov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, 1;\n\t}"
+        ::"r"(d_tmem), "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "n"(A_STEP),
+          "n"(B_STEP), "n"(2 * A_STEP), "n"(2 * B_STEP), "n"(3 * A_STEP), "n"(3 * B_STEP)
+        : "memory");
+}
+
+// Four f8f6f4 MMAs along K: D (+)= sum_i A_i x B_i, the operands' descriptors
+// given as low and high words, the low ones A_STEP and B_STEP (16-byte units)
+// apart.  The first one adds to D if `accumulate`.  One thread issues every
+// MMA of an SM (or pair), so its instructions between two MMAs bound the rate.
+template <int A_STEP, int B_STEP>
+__device__ __forceinline__ void mma4_f8(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                       uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t.reg .b32 x, y;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, p;\n\t"
+        "add.u32 x, %1, %7;\n\tadd.u32 y, %3, %8;\n\t"
+        "mov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, 1;\n\t"
+        "add.u32 x, %1, %9;\n\tadd.u32 y, %3, %10;\n\t"
+        "mov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, 1;\n\t"
+        "add.u32 x, %1, %11;\n\tadd.u32 y, %3, %12;\n\t"
+        "mov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, 1;\n\t}"
+        ::"r"(d_tmem), "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "n"(A_STEP),
+          "n"(B_STEP), "n"(2 * A_STEP), "n"(2 * B_STEP), "n"(3 * A_STEP), "n"(3 * B_STEP)
+        : "memory");
+}
+
+// Four f8f6f4 MMAs along K: D (+)= sum_i A_i x B_i, the operands' descriptors
+// given as low and high words, the low ones A_STEP and B_STEP (16-byte units)
+// apart.  The first one adds to D if `accumulate`.  One thread issues every
+// MMA of an SM (or pair), so its instructions between two MMAs bound the rate.
+template <int A_STEP, int B_STEP>
+__device__ __forceinline__ void mma4_f8_pair(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                       uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t.reg .b32 x, y;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %5, p;\n\t"
+        "add.u32 x, %1, %7;\n\tadd.u32 y, %3, %8;\n\t"
+        "mov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %5, 1;\n\t"
+        "add.u32 x, %1, %9;\n\tadd.u32 y, %3, %10;\n\t"
+        "mov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %5, 1;\n\t"
+        "add.u32 x, %1, %11;\n\tadd.u32 y, %3, %12;\n\t"
+        "mov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %5, 1;\n\t}"
+        ::"r"(d_tmem), "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "n"(A_STEP),
+          "n"(B_STEP), "n"(2 * A_STEP), "n"(2 * B_STEP), "n"(3 * A_STEP), "n"(3 * B_STEP)
+        : "memory");
 }
 
 }  // namespace zbp
