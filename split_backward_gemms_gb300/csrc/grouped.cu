@@ -441,8 +441,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 // pass's products in one launch.  The contraction runs over an expert's rows,
 // so its last block of 64 must not see the next expert's: each expert has
 // tensor maps of its own rows (their start and number set on the device by
-// zb_moe_maps_kernel), and the copies past the last row fill in zeros.  Both
-// operands are read as they lie (MN-major).
+// zb_moe_maps_kernel), and the copies past the last row fill in zeros.  Only a
+// partial last block goes through them; whole blocks use maps of all rows from
+// the launch parameters, whose descriptors need no fetch from memory per
+// expert.  Both operands are read as they lie (MN-major).
 //
 // The tensor core cuts off low bits as it accumulates, so the error of one
 // long accumulator grows with its length (1.4e-6 of the result after ~1024
@@ -452,7 +454,27 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 // next segment fill the other accumulator.  The fp32 tile goes out through 32 x
 // 32 staging boxes, added in place by TMA reduce-adds when accumulating (one
 // add per element: no order to vary).
-constexpr int W_SEG = 4;  // blocks of 64 rows
+//
+// The stores share the copy unit with the next tile's loads and, issued at once,
+// queue before them.  So a tile's four chunks a warp go out W_PACE cycles times
+// its blocks of rows apart (at most W_PACE_MOST), which spreads them over about
+// the time in which the MMAs fill the two accumulators anew.  W of 16384 rows,
+// 16 experts, h 1024, f 4096: 235 us unpaced, 219 at 1500 cycles, 212 at 2000
+// to 2500, 230 at 3500; of 24570 rows, 64 experts (6 blocks each): 394, 374 at
+// 1500, 401 at 2000.
+constexpr int W_SEG = 8;  // blocks of 64 rows
+constexpr int W_PACE = 250, W_PACE_MOST = 2200;
+// Warp 0 copies, warp 1 issues MMAs; warps 4-11 sum and store, with the
+// registers that warps 0-3 give up (128 sums a thread).
+constexpr int W_THREADS = 384;
+constexpr int W_REGS_LOW = 40, W_REGS_HIGH = 232;
+static_assert(128 * W_REGS_LOW + 256 * W_REGS_HIGH <= W_THREADS * 168, "register split");
+constexpr uint32_t W_BOX = 32 * 128;  // 32 x 32 fp32
+constexpr int W_BOXES = 2;            // staging boxes a warp
+template <int CG>
+struct WCfg {
+    static constexpr int STAGES = CG == 1 ? 3 : 5;
+};
 struct MapsArgs {
     const int* offsets;
     int rows, experts, width[4];
@@ -503,23 +525,24 @@ struct WCtl {
 };
 template <int CG>
 constexpr size_t w_smem() {
-    return 1024 + Cfg<CG>::STAGES * Cfg<CG>::STAGE_BYTES + STAGING_BYTES + sizeof(WCtl<CG>);
+    return 1024 + WCfg<CG>::STAGES * Cfg<CG>::STAGE_BYTES + 8 * W_BOXES * W_BOX + sizeof(WCtl<CG>);
 }
 static_assert(w_smem<1>() <= 232448 && w_smem<2>() <= 232448, "shared memory");
 
 template <int CG>
-__global__ void __launch_bounds__(NUM_THREADS, 1)
-    zb_moe_wgrad_kernel(const __grid_constant__ CUtensorMap tmO0, const __grid_constant__ CUtensorMap tmO1,
+__global__ void __launch_bounds__(W_THREADS, 1)
+    zb_moe_wgrad_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmB0,
+                        const __grid_constant__ CUtensorMap tmA1, const __grid_constant__ CUtensorMap tmB1,
+                        const __grid_constant__ CUtensorMap tmO0, const __grid_constant__ CUtensorMap tmO1,
                         const WArgs args) {
     using C = Cfg<CG>;
-    constexpr int STAGES = C::STAGES;
+    constexpr int STAGES = WCfg<CG>::STAGES;
     constexpr bool PAIR = CG == 2;
     constexpr int WARPS = 8;
-    constexpr uint32_t BOX = 32 * 128;  // one staging box a warp
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t* staging = smem + STAGES * C::STAGE_BYTES;
-    WCtl<CG>* ctl = reinterpret_cast<WCtl<CG>*>(staging + STAGING_BYTES);
+    WCtl<CG>* ctl = reinterpret_cast<WCtl<CG>*>(staging + WARPS * W_BOXES * W_BOX);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = PAIR ? zbp::cluster_ctarank() : 0u;
@@ -554,8 +577,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         zbp::mbar_init(zbp::smem_u32(&ctl->drain), 1);
         ctl->abort_flag = 0;
         zbp::fence_mbar_init();
+        zbp::tma_prefetch_desc(&tmA0);
+        zbp::tma_prefetch_desc(&tmB0);
         zbp::tma_prefetch_desc(&tmO0);
-        if (args.products > 1) zbp::tma_prefetch_desc(&tmO1);
+        if (args.products > 1) {
+            zbp::tma_prefetch_desc(&tmA1);
+            zbp::tma_prefetch_desc(&tmB1);
+            zbp::tma_prefetch_desc(&tmO1);
+        }
     }
     if (warp == 1) {
         if (PAIR) {
@@ -577,8 +606,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     load_offsets(ctl->off, args.offsets, args.experts, args.rows);
     auto blocks_of = [&](int e) { return (ctl->off[e + 1] - ctl->off[e] + BK - 1) / BK; };
 
-    if (warp == 0) {
-        if (lane == 0) {
+    if (warp < 4) {
+        zbp::regs_dec<W_REGS_LOW>();
+        if (warp == 0 && lane == 0) {
             // ------------------------------------------------ TMA producer
             uint32_t it = 0;
             bool ok = true;
@@ -587,10 +617,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 const int p = locate(tile, e, mb, nb);
                 const int num_kb = blocks_of(e);
                 if (num_kb == 0) continue;
-                const CUtensorMap* tma = args.maps + 4 * e + 2 * p;
-                const CUtensorMap* tmb = tma + 1;
-                zbp::fence_tensormap_acquire(tma);
-                zbp::fence_tensormap_acquire(tmb);
+                const int first = ctl->off[e], n = ctl->off[e + 1] - first;
+                const CUtensorMap* tail = args.maps + 4 * e + 2 * p;  // A's, then B's
+                if (n % BK) {
+                    zbp::fence_tensormap_acquire(tail);
+                    zbp::fence_tensormap_acquire(tail + 1);
+                    zbp::tma_prefetch_desc(tail);
+                    zbp::tma_prefetch_desc(tail + 1);
+                }
                 const int m0 = mb * C::TILE_M + static_cast<int>(rank) * BM;
                 const int nb0 = nb * BN + static_cast<int>(rank) * C::B_ROWS;
                 for (int kb = 0; kb < num_kb; ++kb, ++it) {
@@ -605,11 +639,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     const uint32_t sa = zbp::smem_u32(smem + s * C::STAGE_BYTES);
                     const uint32_t sb = sa + A_BYTES;
                     if (leader) zbp::mbar_arrive_expect_tx(full_local, C::STAGE_BYTES * CG);
+                    const bool whole = kb * BK + BK <= n;
+                    const CUtensorMap* tma = whole ? (p ? &tmA1 : &tmA0) : tail;
+                    const CUtensorMap* tmb = whole ? (p ? &tmB1 : &tmB0) : tail + 1;
+                    const int y = whole ? first + kb * BK : kb * BK;
                     auto load = [&](uint32_t dst, const CUtensorMap* tm, int x) {
                         if (PAIR)
-                            zbp::tma_load_2d_pair(dst, tm, full, x, kb * BK);
+                            zbp::tma_load_2d_pair(dst, tm, full, x, y);
                         else
-                            zbp::tma_load_2d(dst, tm, full, x, kb * BK);
+                            zbp::tma_load_2d(dst, tm, full, x, y);
                     };
                     load(sa, tma, m0);
                     load(sa + MN_ATOM_BYTES, tma, m0 + 64);
@@ -623,9 +661,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     wait_bar<false>(zbp::smem_u32(&ctl->full[i % STAGES]), (i / STAGES) & 1u, abort_flag, args.err,
                                    ERR_WAIT_PRODUCER, DRAIN_LIMIT_NS, false);
             }
-        }
-    } else if (warp == 1) {
-        if (lane == 0 && leader) {
+        } else if (warp == 1 && lane == 0 && leader) {
             // ------------------------------------------------ MMA issuer
             constexpr uint32_t idesc = zbp::idesc_bf16_f32(BM * CG, BN, 1, 1);
             constexpr uint32_t hi = zbp::desc_hi(1024);
@@ -681,10 +717,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
     } else {
         // ---------------------------------------------------- epilogue
-        const int ew = warp - 2, q = warp & 3;
+        zbp::regs_inc<W_REGS_HIGH>();
+        const int ew = warp - 4, q = warp & 3;
         const int c_lo = (ew >> 2) * (BN / 2);  // this warp's half of the tile's columns
-        const uint32_t stg = zbp::smem_u32(staging + ew * BOX);
-        uint32_t local = 0;
+        const uint32_t stg0 = zbp::smem_u32(staging + ew * W_BOXES * W_BOX);
+        uint32_t local = 0, flip = 0;
         bool ok = true;
         for (int tile = cluster; tile < num_tiles && ok; tile += clusters) {
             int e, mb, nb;
@@ -727,15 +764,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 }
             }
             if (!ok) break;
+            const long long done = clock64();
+            const int pace = tile + clusters < num_tiles ? min(W_PACE * num_kb, W_PACE_MOST) : 0;
 #pragma unroll
             for (int c = 0; c < BN / 64; ++c) {
                 const int col0 = n0 + c * 32;
                 if (row0 >= Mp || col0 >= Np) continue;
+                while (clock64() - done < c * pace) __nanosleep(64);
                 uint32_t v[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(sum[c * 32 + i]);
-                if (lane == 0) zbp::bulk_wait_read<0>();  // the box's last store has read it
-                __syncwarp();
+                const uint32_t stg = stg0 + flip * W_BOX;
+                flip ^= 1u;
+                staging_acquire(lane);
                 stage_row(stg, lane, v);
                 zbp::fence_proxy_async_smem();
                 __syncwarp();
@@ -878,14 +919,14 @@ struct WProduct {
 };
 
 template <int CG>
-zb_status launch_wgrad(const CUtensorMap (&mo)[2], const WArgs& a, long long tiles, void* stream) {
+zb_status launch_wgrad(const CUtensorMap (&mi)[4], const CUtensorMap (&mo)[2], const WArgs& a, long long tiles, void* stream) {
     auto kern = zb_moe_wgrad_kernel<CG>;
     static std::atomic<int> cache[64];
     int ctas = 0;
-    zb_status s = full_grid(kern, cache, w_smem<CG>(), NUM_THREADS, CG, &ctas);
+    zb_status s = full_grid(kern, cache, w_smem<CG>(), W_THREADS, CG, &ctas);
     if (s != ZB_OK) return s;
-    LaunchCfg lc(static_cast<int>(std::min<long long>(tiles * CG, ctas)), NUM_THREADS, w_smem<CG>(), CG, stream);
-    const cudaError_t e = cudaLaunchKernelEx(&lc.cfg, kern, mo[0], mo[1], a);
+    LaunchCfg lc(static_cast<int>(std::min<long long>(tiles * CG, ctas)), W_THREADS, w_smem<CG>(), CG, stream);
+    const cudaError_t e = cudaLaunchKernelEx(&lc.cfg, kern, mi[0], mi[1], mi[2], mi[3], mo[0], mo[1], a);
     if (e != cudaSuccess)
         return zb::fail(ZB_ERR_CUDA, std::string("grouped weight gradient launch: ") + cudaGetErrorString(e));
     return launched("grouped weight gradient");
@@ -941,7 +982,8 @@ zb_status wgrad(const zb_moe& m, const int32_t* offsets, const WProduct* p, int 
     a.err = err;
     tiles1 *= m.experts;
     tiles2 *= m.experts;
-    return tiles2 >= sm_count() / 2 ? launch_wgrad<2>(mo, a, tiles2, stream) : launch_wgrad<1>(mo, a, tiles1, stream);
+    return tiles2 >= sm_count() / 2 ? launch_wgrad<2>(mi, mo, a, tiles2, stream)
+                                     : launch_wgrad<1>(mi, mo, a, tiles1, stream);
 }
 
 }  // namespace
