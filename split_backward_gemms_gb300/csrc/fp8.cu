@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
     uint8_t* staging = smem + STAGES * C::STAGE;
     Fp8Ctl* ctl = reinterpret_cast<Fp8Ctl*>(staging + FP8_EPI_WARPS * BOXES * FP8_BOX);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = PAIR ? zbp::cluster_ctarank() : 0u;
     const bool leader = rank == 0;
     const int cluster = blockIdx.x / CG, clusters = gridDim.x / CG;
@@ -256,9 +256,12 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
     int row0 = 0, nrows = 0, nb = 0;
     if (warp < 4) {
         zbp::regs_dec<FP8_REGS_LOW>();
-        if (warp == 0 && lane == 0) {
+        if (warp == 0) {
             // ------------------------------------------------ TMA producer
-            uint32_t it = 0;
+            const uint32_t full0 = zbp::smem_u32(&ctl->full[0]), empty0 = zbp::smem_u32(&ctl->empty[0]);
+            const uint32_t full0_lead = PAIR ? zbp::mapa_shared(full0, 0) : full0;
+            const uint32_t sa0 = zbp::smem_u32(smem);
+            uint32_t s = 0, sp = 1, it = 0;  // stage and the phase of its last release; stages filled
             bool ok = true;
             for (int tile = cluster; ok && walk.to(tile, row0, nrows, nb); tile += clusters) {
                 // 32-row boxes of rows in this CTA, and in both
@@ -269,32 +272,39 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
                 const uint32_t bytes = static_cast<uint32_t>(all) * 32u * 128u + 256u * 128u;
                 const int n0 = nb * 256 + static_cast<int>(rank) * C::B_ROWS;
                 for (int kb = 0; kb < num_kb; ++kb, ++it) {
-                    const uint32_t s = it % STAGES, r = it / STAGES;
-                    if (!wait_bar<false>(zbp::smem_u32(&ctl->empty[s]), (r & 1u) ^ 1u, abort_flag, args.err,
-                                        ERR_WAIT_PRODUCER, WAIT_LIMIT_NS, true)) {
+                    if (!wait_bar<false>(empty0 + s * 8u, sp, abort_flag, args.err, ERR_WAIT_PRODUCER, WAIT_LIMIT_NS,
+                                         true)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t full_local = zbp::smem_u32(&ctl->full[s]);
-                    const uint32_t full = PAIR ? zbp::mapa_shared(full_local, 0) : full_local;
-                    const uint32_t sa = zbp::smem_u32(smem + s * C::STAGE);
-                    const uint32_t sb = sa + C::A_BYTES8;
-                    const int k0 = kb * BLK;
-                    if (leader) zbp::mbar_arrive_expect_tx(full_local, bytes);
-                    auto load_a = [&](uint32_t dst, const CUtensorMap* tm, int y) {
+                    if (zbp::elect_one()) {
+                        const uint32_t full = full0_lead + s * 8u;
+                        const uint32_t sa = sa0 + s * C::STAGE, sb = sa + C::A_BYTES8;
+                        const int k0 = kb * BLK;
+                        if (leader) zbp::mbar_arrive_expect_tx(full0 + s * 8u, bytes);
+                        auto load_a = [&](uint32_t dst, const CUtensorMap* tm, int y) {
+                            if (PAIR)
+                                zbp::tma_load_2d_pair(dst, tm, full, k0, y);
+                            else
+                                zbp::tma_load_2d(dst, tm, full, k0, y);
+                        };
+                        if (boxes == 4) {
+                            load_a(sa, &tmA128, r0);
+                        } else {
+#pragma unroll
+                            for (int b = 0; b < 3; ++b)
+                                if (b < boxes) load_a(sa + static_cast<uint32_t>(b) * 32u * 128u, &tmA32, r0 + 32 * b);
+                        }
                         if (PAIR)
-                            zbp::tma_load_2d_pair(dst, tm, full, k0, y);
+                            zbp::tma_load_3d_pair(sb, &tmB, full, k0, n0, walk.e);
                         else
-                            zbp::tma_load_2d(dst, tm, full, k0, y);
-                    };
-                    if (boxes == 4)
-                        load_a(sa, &tmA128, r0);
-                    else
-                        for (int b = 0; b < boxes; ++b) load_a(sa + static_cast<uint32_t>(b) * 32u * 128u, &tmA32, r0 + 32 * b);
-                    if (PAIR)
-                        zbp::tma_load_3d_pair(sb, &tmB, full, k0, n0, walk.e);
-                    else
-                        zbp::tma_load_3d(sb, &tmB, full, k0, n0, walk.e);
+                            zbp::tma_load_3d(sb, &tmB, full, k0, n0, walk.e);
+                    }
+                    __syncwarp();
+                    if (++s == STAGES) {
+                        s = 0;
+                        sp ^= 1u;
+                    }
                 }
             }
             if (!ok && leader) {
@@ -302,9 +312,9 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
                 const uint32_t first = it > STAGES ? it - STAGES : 0;
                 for (uint32_t i = first; i < it; ++i)
                     wait_bar<false>(zbp::smem_u32(&ctl->full[i % STAGES]), (i / STAGES) & 1u, abort_flag, args.err,
-                                   ERR_WAIT_PRODUCER, DRAIN_LIMIT_NS, false);
+                                    ERR_WAIT_PRODUCER, DRAIN_LIMIT_NS, false);
             }
-        } else if ((warp == 1 || warp == 2) && lane == 0 && leader) {
+        } else if ((warp == 1 || warp == 2) && leader) {
             // ------------------------------------------------ MMA issuers
             // Warp 1 issues the even blocks of K (into accumulator 0), warp 2
             // the odd ones: a block's two waits, four MMAs and two commits take
@@ -329,16 +339,19 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
                     }
                     tp ^= 1u;
                     zbp::tc_fence_after();
-                    const uint32_t a = lo0 + s * (C::STAGE >> 4), b = a + (C::A_BYTES8 >> 4);
-                    if (PAIR) {
-                        zbp::mma4_f8_pair<2, 2>(d_tmem, a, hi, b, hi, idesc, 0);
-                        zbp::tc_commit_pair_multicast(tfull, 0x3);
-                        zbp::tc_commit_pair_multicast(empty0 + s * 8u, 0x3);
-                    } else {
-                        zbp::mma4_f8<2, 2>(d_tmem, a, hi, b, hi, idesc, 0);
-                        zbp::tc_commit(tfull);
-                        zbp::tc_commit(empty0 + s * 8u);
+                    if (zbp::elect_one()) {
+                        const uint32_t a = lo0 + s * (C::STAGE >> 4), b = a + (C::A_BYTES8 >> 4);
+                        if (PAIR) {
+                            zbp::mma4_f8_pair<2, 2>(d_tmem, a, hi, b, hi, idesc, 0);
+                            zbp::tc_commit_pair_multicast(tfull, 0x3);
+                            zbp::tc_commit_pair_multicast(empty0 + s * 8u, 0x3);
+                        } else {
+                            zbp::mma4_f8<2, 2>(d_tmem, a, hi, b, hi, idesc, 0);
+                            zbp::tc_commit(tfull);
+                            zbp::tc_commit(empty0 + s * 8u);
+                        }
                     }
+                    __syncwarp();
                     s += 2;
                     if (s >= STAGES) {
                         s -= STAGES;
@@ -349,10 +362,13 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
             }
             // every MMA issued here completes before TMEM is released
             const uint32_t drain = zbp::smem_u32(&ctl->drain[buf]);
-            if (PAIR)
-                zbp::tc_commit_pair(drain);
-            else
-                zbp::tc_commit(drain);
+            if (zbp::elect_one()) {
+                if (PAIR)
+                    zbp::tc_commit_pair(drain);
+                else
+                    zbp::tc_commit(drain);
+            }
+            __syncwarp();
             wait_bar<false>(drain, 0, abort_flag, args.err, ERR_WAIT_MMA, DRAIN_LIMIT_NS, false);
         }
     } else {

@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint8_t* staging = smem + STAGES * C::STAGE;
     RowsCtl* ctl = reinterpret_cast<RowsCtl*>(staging + EPI_WARPS * BOXES * ROW_BOX);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = PAIR ? zbp::cluster_ctarank() : 0u;
     const bool leader = rank == 0;
     const int cluster = blockIdx.x / CG, clusters = gridDim.x / CG;
@@ -139,30 +139,29 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     Walk<C::TILE_T, true> walk(ctl->off, args.experts, tiles_f);
     int row0 = 0, nrows = 0, fb = 0;
     if (warp == 0) {
-        if (lane == 0) {
-            // ------------------------------------------------ TMA producer
-            uint32_t it = 0;
-            bool ok = true;
-            for (int tile = cluster; ok && walk.to(tile, row0, nrows, fb); tile += clusters) {
-                const int f0 = fb * C::TILE_F + static_cast<int>(rank) * 128;
-                const int mma_n = (nrows + C::N_STEP - 1) / C::N_STEP * C::N_STEP;
-                const int half = mma_n / CG;  // rows in this CTA
-                const int r0 = row0 + static_cast<int>(rank) * half;
-                const int boxes = (half + 31) / 32;
-                const uint32_t bytes = CG * (A_BYTES + static_cast<uint32_t>(boxes) * 32u * BK * 2u);
-                for (int kb = 0; kb < num_kb; ++kb, ++it) {
-                    const uint32_t s = it % STAGES, r = it / STAGES;
-                    if (!wait_bar<false>(zbp::smem_u32(&ctl->empty[s]), (r & 1u) ^ 1u, abort_flag, args.err,
-                                        ERR_WAIT_PRODUCER, WAIT_LIMIT_NS, true)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t full_local = zbp::smem_u32(&ctl->full[s]);
-                    const uint32_t full = PAIR ? zbp::mapa_shared(full_local, 0) : full_local;
-                    const uint32_t sa = zbp::smem_u32(smem + s * C::STAGE);
-                    const uint32_t sb = sa + A_BYTES;
+        // ---------------------------------------------------- TMA producer
+        const uint32_t full0 = zbp::smem_u32(&ctl->full[0]), empty0 = zbp::smem_u32(&ctl->empty[0]);
+        const uint32_t full0_lead = PAIR ? zbp::mapa_shared(full0, 0) : full0;
+        const uint32_t sa0 = zbp::smem_u32(smem);
+        uint32_t s = 0, sp = 1, it = 0;  // stage and the phase of its last release; stages filled
+        bool ok = true;
+        for (int tile = cluster; ok && walk.to(tile, row0, nrows, fb); tile += clusters) {
+            const int f0 = fb * C::TILE_F + static_cast<int>(rank) * 128;
+            const int mma_n = (nrows + C::N_STEP - 1) / C::N_STEP * C::N_STEP;
+            const int half = mma_n / CG;  // rows in this CTA
+            const int r0 = row0 + static_cast<int>(rank) * half;
+            const int boxes = (half + 31) / 32;
+            const uint32_t bytes = CG * (A_BYTES + static_cast<uint32_t>(boxes) * 32u * BK * 2u);
+            for (int kb = 0; kb < num_kb; ++kb, ++it) {
+                if (!wait_bar<false>(empty0 + s * 8u, sp, abort_flag, args.err, ERR_WAIT_PRODUCER, WAIT_LIMIT_NS, true)) {
+                    ok = false;
+                    break;
+                }
+                if (zbp::elect_one()) {
+                    const uint32_t full = full0_lead + s * 8u;
+                    const uint32_t sa = sa0 + s * C::STAGE, sb = sa + A_BYTES;
                     const int k0 = kb * BK;
-                    if (leader) zbp::mbar_arrive_expect_tx(full_local, bytes);
+                    if (leader) zbp::mbar_arrive_expect_tx(full0 + s * 8u, bytes);
                     auto load_w = [&](uint32_t dst, int x, int y) {
                         if (PAIR)
                             zbp::tma_load_3d_pair(dst, &tmW, full, x, y, walk.e);
@@ -184,20 +183,27 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     if (boxes == 4) {
                         load_a(sb, &tmA128, r0);
                     } else {
-                        for (int b = 0; b < boxes; ++b) load_a(sb + static_cast<uint32_t>(b) * 32u * BK * 2u, &tmA32, r0 + 32 * b);
+#pragma unroll
+                        for (int b = 0; b < 3; ++b)
+                            if (b < boxes) load_a(sb + static_cast<uint32_t>(b) * 32u * BK * 2u, &tmA32, r0 + 32 * b);
                     }
                 }
-            }
-            if (!ok && leader) {
-                // wait for the copies that were issued but may not have landed
-                const uint32_t first = it > STAGES ? it - STAGES : 0;
-                for (uint32_t i = first; i < it; ++i)
-                    wait_bar<false>(zbp::smem_u32(&ctl->full[i % STAGES]), (i / STAGES) & 1u, abort_flag, args.err,
-                                   ERR_WAIT_PRODUCER, DRAIN_LIMIT_NS, false);
+                __syncwarp();
+                if (++s == STAGES) {
+                    s = 0;
+                    sp ^= 1u;
+                }
             }
         }
+        if (!ok && leader) {
+            // wait for the copies that were issued but may not have landed
+            const uint32_t first = it > STAGES ? it - STAGES : 0;
+            for (uint32_t i = first; i < it; ++i)
+                wait_bar<false>(zbp::smem_u32(&ctl->full[i % STAGES]), (i / STAGES) & 1u, abort_flag, args.err,
+                                ERR_WAIT_PRODUCER, DRAIN_LIMIT_NS, false);
+        }
     } else if (warp == 1) {
-        if (lane == 0 && leader) {
+        if (leader) {
             // ------------------------------------------------ MMA issuer
             constexpr uint32_t A_STEP = A_MN ? 2048 >> 4 : 32 >> 4, hi = zbp::desc_hi(1024);
             const uint32_t a0 = zbp::desc_lo(zbp::smem_u32(smem), A_MN ? MN_ATOM_BYTES : 16);
@@ -219,30 +225,33 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         break;
                     }
                     zbp::tc_fence_after();
-                    const uint32_t off = s * (C::STAGE >> 4);
-                    if (PAIR) {
-                        zbp::mma4_f16_pair<A_STEP, 2>(d_tmem, a0 + off, hi, b0 + off, hi, idesc, kb != 0);
-                        zbp::tc_commit_pair_multicast(empty0 + s * 8u, 0x3);
-                    } else {
-                        zbp::mma4_f16<A_STEP, 2>(d_tmem, a0 + off, hi, b0 + off, hi, idesc, kb != 0);
-                        zbp::tc_commit(empty0 + s * 8u);
+                    if (zbp::elect_one()) {
+                        const uint32_t off = s * (C::STAGE >> 4);
+                        if (PAIR) {
+                            zbp::mma4_f16_pair<A_STEP, 2>(d_tmem, a0 + off, hi, b0 + off, hi, idesc, kb != 0);
+                            zbp::tc_commit_pair_multicast(empty0 + s * 8u, 0x3);
+                            if (kb + 1 == num_kb) zbp::tc_commit_pair_multicast(zbp::smem_u32(&ctl->tfull[buf]), 0x3);
+                        } else {
+                            zbp::mma4_f16<A_STEP, 2>(d_tmem, a0 + off, hi, b0 + off, hi, idesc, kb != 0);
+                            zbp::tc_commit(empty0 + s * 8u);
+                            if (kb + 1 == num_kb) zbp::tc_commit(zbp::smem_u32(&ctl->tfull[buf]));
+                        }
                     }
+                    __syncwarp();
                     if (++s == STAGES) {
                         s = 0;
                         sp ^= 1u;
                     }
                 }
-                if (!ok) break;
-                if (PAIR)
-                    zbp::tc_commit_pair_multicast(zbp::smem_u32(&ctl->tfull[buf]), 0x3);
-                else
-                    zbp::tc_commit(zbp::smem_u32(&ctl->tfull[buf]));
             }
             // every MMA issued here completes before TMEM is released
-            if (PAIR)
-                zbp::tc_commit_pair(zbp::smem_u32(&ctl->drain));
-            else
-                zbp::tc_commit(zbp::smem_u32(&ctl->drain));
+            if (zbp::elect_one()) {
+                if (PAIR)
+                    zbp::tc_commit_pair(zbp::smem_u32(&ctl->drain));
+                else
+                    zbp::tc_commit(zbp::smem_u32(&ctl->drain));
+            }
+            __syncwarp();
             wait_bar<false>(zbp::smem_u32(&ctl->drain), 0, abort_flag, args.err, ERR_WAIT_MMA, DRAIN_LIMIT_NS, false);
         }
     } else {
@@ -544,7 +553,7 @@ __global__ void __launch_bounds__(W_THREADS, 1)
     uint8_t* staging = smem + STAGES * C::STAGE_BYTES;
     WCtl<CG>* ctl = reinterpret_cast<WCtl<CG>*>(staging + WARPS * W_BOXES * W_BOX);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = PAIR ? zbp::cluster_ctarank() : 0u;
     const bool leader = rank == 0;
     const int cluster = blockIdx.x / CG, clusters = gridDim.x / CG;
@@ -608,9 +617,12 @@ __global__ void __launch_bounds__(W_THREADS, 1)
 
     if (warp < 4) {
         zbp::regs_dec<W_REGS_LOW>();
-        if (warp == 0 && lane == 0) {
+        if (warp == 0) {
             // ------------------------------------------------ TMA producer
-            uint32_t it = 0;
+            const uint32_t full0 = zbp::smem_u32(&ctl->full[0]), empty0 = zbp::smem_u32(&ctl->empty[0]);
+            const uint32_t full0_lead = PAIR ? zbp::mapa_shared(full0, 0) : full0;
+            const uint32_t sa0 = zbp::smem_u32(smem);
+            uint32_t s = 0, sp = 1, it = 0;  // stage and the phase of its last release; stages filled
             bool ok = true;
             for (int tile = cluster; tile < num_tiles && ok; tile += clusters) {
                 int e, mb, nb;
@@ -619,49 +631,55 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                 if (num_kb == 0) continue;
                 const int first = ctl->off[e], n = ctl->off[e + 1] - first;
                 const CUtensorMap* tail = args.maps + 4 * e + 2 * p;  // A's, then B's
-                if (n % BK) {
+                if (n % BK && zbp::elect_one()) {
                     zbp::fence_tensormap_acquire(tail);
                     zbp::fence_tensormap_acquire(tail + 1);
                     zbp::tma_prefetch_desc(tail);
                     zbp::tma_prefetch_desc(tail + 1);
                 }
+                __syncwarp();
                 const int m0 = mb * C::TILE_M + static_cast<int>(rank) * BM;
                 const int nb0 = nb * BN + static_cast<int>(rank) * C::B_ROWS;
                 for (int kb = 0; kb < num_kb; ++kb, ++it) {
-                    const uint32_t s = it % STAGES, r = it / STAGES;
-                    if (!wait_bar<false>(zbp::smem_u32(&ctl->empty[s]), (r & 1u) ^ 1u, abort_flag, args.err,
-                                        ERR_WAIT_PRODUCER, WAIT_LIMIT_NS, true)) {
+                    if (!wait_bar<false>(empty0 + s * 8u, sp, abort_flag, args.err, ERR_WAIT_PRODUCER, WAIT_LIMIT_NS,
+                                         true)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t full_local = zbp::smem_u32(&ctl->full[s]);
-                    const uint32_t full = PAIR ? zbp::mapa_shared(full_local, 0) : full_local;
-                    const uint32_t sa = zbp::smem_u32(smem + s * C::STAGE_BYTES);
-                    const uint32_t sb = sa + A_BYTES;
-                    if (leader) zbp::mbar_arrive_expect_tx(full_local, C::STAGE_BYTES * CG);
-                    const bool whole = kb * BK + BK <= n;
-                    const CUtensorMap* tma = whole ? (p ? &tmA1 : &tmA0) : tail;
-                    const CUtensorMap* tmb = whole ? (p ? &tmB1 : &tmB0) : tail + 1;
-                    const int y = whole ? first + kb * BK : kb * BK;
-                    auto load = [&](uint32_t dst, const CUtensorMap* tm, int x) {
-                        if (PAIR)
-                            zbp::tma_load_2d_pair(dst, tm, full, x, y);
-                        else
-                            zbp::tma_load_2d(dst, tm, full, x, y);
-                    };
-                    load(sa, tma, m0);
-                    load(sa + MN_ATOM_BYTES, tma, m0 + 64);
+                    if (zbp::elect_one()) {
+                        const uint32_t full = full0_lead + s * 8u;
+                        const uint32_t sa = sa0 + s * C::STAGE_BYTES, sb = sa + A_BYTES;
+                        if (leader) zbp::mbar_arrive_expect_tx(full0 + s * 8u, C::STAGE_BYTES * CG);
+                        const bool whole = kb * BK + BK <= n;
+                        const CUtensorMap* tma = whole ? (p ? &tmA1 : &tmA0) : tail;
+                        const CUtensorMap* tmb = whole ? (p ? &tmB1 : &tmB0) : tail + 1;
+                        const int y = whole ? first + kb * BK : kb * BK;
+                        auto load = [&](uint32_t dst, const CUtensorMap* tm, int x) {
+                            if (PAIR)
+                                zbp::tma_load_2d_pair(dst, tm, full, x, y);
+                            else
+                                zbp::tma_load_2d(dst, tm, full, x, y);
+                        };
+                        load(sa, tma, m0);
+                        load(sa + MN_ATOM_BYTES, tma, m0 + 64);
 #pragma unroll
-                    for (int i = 0; i < C::B_ROWS / 64; ++i) load(sb + i * MN_ATOM_BYTES, tmb, nb0 + 64 * i);
+                        for (int i = 0; i < C::B_ROWS / 64; ++i) load(sb + i * MN_ATOM_BYTES, tmb, nb0 + 64 * i);
+                    }
+                    __syncwarp();
+                    if (++s == STAGES) {
+                        s = 0;
+                        sp ^= 1u;
+                    }
                 }
             }
             if (!ok && leader) {
+                // wait for the copies that were issued but may not have landed
                 const uint32_t first = it > STAGES ? it - STAGES : 0;
                 for (uint32_t i = first; i < it; ++i)
                     wait_bar<false>(zbp::smem_u32(&ctl->full[i % STAGES]), (i / STAGES) & 1u, abort_flag, args.err,
-                                   ERR_WAIT_PRODUCER, DRAIN_LIMIT_NS, false);
+                                    ERR_WAIT_PRODUCER, DRAIN_LIMIT_NS, false);
             }
-        } else if (warp == 1 && lane == 0 && leader) {
+        } else if (warp == 1 && leader) {
             // ------------------------------------------------ MMA issuer
             constexpr uint32_t idesc = zbp::idesc_bf16_f32(BM * CG, BN, 1, 1);
             constexpr uint32_t hi = zbp::desc_hi(1024);
@@ -689,30 +707,33 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                             break;
                         }
                         zbp::tc_fence_after();
-                        const uint32_t a = a0 + s * (C::STAGE_BYTES >> 4), b = a + (A_BYTES >> 4);
-                        if (PAIR) {
-                            zbp::mma4_f16_pair<128, 128>(d_tmem, a, hi, b, hi, idesc, kb != kb0);
-                            zbp::tc_commit_pair_multicast(empty0 + s * 8u, 0x3);
-                        } else {
-                            zbp::mma4_f16<128, 128>(d_tmem, a, hi, b, hi, idesc, kb != kb0);
-                            zbp::tc_commit(empty0 + s * 8u);
+                        if (zbp::elect_one()) {
+                            const uint32_t a = a0 + s * (C::STAGE_BYTES >> 4), b = a + (A_BYTES >> 4);
+                            if (PAIR) {
+                                zbp::mma4_f16_pair<128, 128>(d_tmem, a, hi, b, hi, idesc, kb != kb0);
+                                zbp::tc_commit_pair_multicast(empty0 + s * 8u, 0x3);
+                                if (kb + 1 == kb1) zbp::tc_commit_pair_multicast(zbp::smem_u32(&ctl->tfull[buf]), 0x3);
+                            } else {
+                                zbp::mma4_f16<128, 128>(d_tmem, a, hi, b, hi, idesc, kb != kb0);
+                                zbp::tc_commit(empty0 + s * 8u);
+                                if (kb + 1 == kb1) zbp::tc_commit(zbp::smem_u32(&ctl->tfull[buf]));
+                            }
                         }
+                        __syncwarp();
                         if (++s == STAGES) {
                             s = 0;
                             sp ^= 1u;
                         }
                     }
-                    if (!ok) break;
-                    if (PAIR)
-                        zbp::tc_commit_pair_multicast(zbp::smem_u32(&ctl->tfull[buf]), 0x3);
-                    else
-                        zbp::tc_commit(zbp::smem_u32(&ctl->tfull[buf]));
                 }
             }
-            if (PAIR)
-                zbp::tc_commit_pair(zbp::smem_u32(&ctl->drain));
-            else
-                zbp::tc_commit(zbp::smem_u32(&ctl->drain));
+            if (zbp::elect_one()) {
+                if (PAIR)
+                    zbp::tc_commit_pair(zbp::smem_u32(&ctl->drain));
+                else
+                    zbp::tc_commit(zbp::smem_u32(&ctl->drain));
+            }
+            __syncwarp();
             wait_bar<false>(zbp::smem_u32(&ctl->drain), 0, abort_flag, args.err, ERR_WAIT_MMA, DRAIN_LIMIT_NS, false);
         }
     } else {

@@ -518,6 +518,16 @@ __device__ __forceinline__ void regs_dec() {
 namespace zbp {
 
 // ---------------------------------------------------------------- K blocks
+// True in one lane of the (converged) warp.  A role's loop runs in all lanes
+// and only its copies, MMAs and commits in the elected one: inside a branch of
+// one lane the compiler cannot keep addresses and descriptors in uniform
+// registers, which these instructions take.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // Low and high words of smem_desc_sw128.
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) {
     return ((saddr & 0x3FFFFu) >> 4) | ((lbo_bytes >> 4) << 16);
