@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import sys
 
 from . import build as _build
 
@@ -202,22 +203,27 @@ LIB = _load()
 def _ptr(x):
     if x is None:
         return None
+    try:
+        return x.data_ptr() or None
+    except AttributeError:
+        pass
     if isinstance(x, int):
         return x or None
-    if hasattr(x, "data_ptr"):
-        return x.data_ptr() or None
     raise TypeError(f"cannot take a device pointer of {type(x)!r}")
+
+
+def _current_stream():
+    """The current torch stream's handle when torch's CUDA is initialised, else None."""
+    torch = sys.modules.get("torch")
+    if torch is None or not torch.cuda.is_initialized():
+        return None
+    # the raw handle: small kernels take less time than making a Stream object
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) or None
 
 
 def _stream(s):
     if s is None:
-        try:
-            import torch
-            if torch.cuda.is_available() and torch.cuda.is_initialized():
-                return torch.cuda.current_stream().cuda_stream or None
-        except Exception:  # pragma: no cover - torch missing
-            pass
-        return None
+        return _current_stream()
     if isinstance(s, int):
         return s or None
     return s.cuda_stream or None
