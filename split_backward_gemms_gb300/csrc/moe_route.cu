@@ -56,72 +56,90 @@ struct RouteArgs {
     int* hist;  // [blocks, experts]
 };
 
-// One warp chooses for one token: element i of the row is held by lane
-// i mod 32.  Each of the k rounds takes the largest key (a warp maximum of the
-// lanes' largest) and among its holders the lowest index (a warp minimum); the
-// lane that held it finds its next largest, lane j keeps choice j.  What bounds
-// it is instructions (~300 a token), not the 4 bytes an expert that it reads:
-// 16384 tokens, 128 experts, 8 choices take 6 us where the bytes take 1.3.
+// A token's logits, element v * 32 + lane in z[v].
 template <int VPL, typename T>
-__device__ __forceinline__ void choose(const RouteArgs& a, long long t, int lane, int* cnt) {
-    const T* z = static_cast<const T*>(a.logits) + t * a.experts;
-    float zv[VPL];
-    uint32_t key[VPL];
+__device__ __forceinline__ void load_row(const RouteArgs& a, long long t, int lane, float (&z)[VPL]) {
+    const T* p = static_cast<const T*>(a.logits) + t * a.experts;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) z[v] = v * 32 + lane < a.experts ? ld_logit<T>(p + v * 32 + lane) : -INFINITY;
+}
+
+// One warp chooses for one token.  A lane first sorts its elements by
+// descending key (adjacent exchanges of strictly larger keys, so equal ones
+// stay in the order of their indices).  Each of the k rounds then takes the
+// largest first key (a warp maximum) and among its holders the lowest index (a
+// warp minimum), and that lane drops its first element; lane j keeps choice j.
+template <int VPL>
+__device__ __forceinline__ void choose(const RouteArgs& a, long long t, int lane, const float (&z)[VPL], int* cnt) {
+    uint32_t key[VPL], at[VPL];
     bool nan = false;
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
-        const int i = v * 32 + lane;
-        const bool in = i < a.experts;
-        zv[v] = in ? ld_logit<T>(z + i) : -INFINITY;
-        key[v] = in ? key_of(zv[v]) : 0u;
+        key[v] = v * 32 + lane < a.experts ? key_of(z[v]) : 0u;
+        at[v] = v;
         nan |= key[v] == 2u;
     }
     nan = __any_sync(FULL, nan);
-    uint32_t best = key[0];
-    int at = lane;
-    auto find = [&] {
-        best = key[0];
-        at = lane;
 #pragma unroll
-        for (int v = 1; v < VPL; ++v)
-            if (key[v] > best) {
-                best = key[v];
-                at = v * 32 + lane;
-            }
-    };
-    find();
-    int mine = -1;
-    float val = 0.0f, top = 0.0f;
-    for (int j = 0; j < a.topk; ++j) {
-        const uint32_t m = __reduce_max_sync(FULL, best);
-        if (m < 2u) break;
-        const int e = __reduce_min_sync(FULL, best == m ? at : 0x7fffffff);
-        if (at == e) {
+    for (int n = VPL - 1; n > 0; --n)
 #pragma unroll
-            for (int v = 0; v < VPL; ++v)
-                if (v * 32 + lane == e) key[v] = 0u;
-            find();
+        for (int v = 0; v < n; ++v) {
+            const bool swap = key[v + 1] > key[v];
+            const uint32_t k = key[v], i = at[v];
+            key[v] = swap ? key[v + 1] : k;
+            at[v] = swap ? at[v + 1] : i;
+            key[v + 1] = swap ? k : key[v + 1];
+            at[v + 1] = swap ? i : at[v + 1];
         }
-        __syncwarp();
-        const float x = logit_of(m);
-        if (j == 0) top = x;
+    uint32_t order = 0;  // four bits an element, the first lowest
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) order |= at[v] << (4 * v);
+    int mine = -1;
+    uint32_t won = 0u;
+    for (int j = 0; j < a.topk; ++j) {
+        const uint32_t m = __reduce_max_sync(FULL, key[0]);
+        if (m < 2u) break;
+        const int i = static_cast<int>((order & 15u) * 32u) + lane;
+        const int e = __reduce_min_sync(FULL, key[0] == m ? i : 0x7fffffff);
+        if (i == e) {
+#pragma unroll
+            for (int v = 0; v < VPL; ++v) key[v] = v + 1 < VPL ? key[v + 1] : 0u;
+            order >>= 4;
+        }
         if (lane == j) {
             mine = e;
-            val = x;
+            won = m;
         }
     }
+    const float val = logit_of(won), top = __shfl_sync(FULL, val, 0);
     const float w = mine >= 0 ? expf(val - top) : 0.0f;
     float total = w;
     if (!a.renorm) {
         total = 0.0f;
 #pragma unroll
-        for (int v = 0; v < VPL; ++v) total += v * 32 + lane < a.experts ? expf(zv[v] - top) : 0.0f;
+        for (int v = 0; v < VPL; ++v) total += v * 32 + lane < a.experts ? expf(z[v] - top) : 0.0f;
     }
     total = warp_sum(total);
     if (lane < a.topk) {
         a.gates[t * a.topk + lane] = mine < 0 ? 0.0f : nan ? __uint_as_float(0x7fc00000u) : w / total;
         a.expert[t * a.topk + lane] = mine;
         if (mine >= 0) atomicAdd(&cnt[mine], 1);  // integer sums: no order
+    }
+}
+
+// Every warp's tokens of [t0, t1); the next token's logits are on their way
+// while one is worked on.
+template <int VPL, typename T>
+__device__ __forceinline__ void choose_all(const RouteArgs& a, long long t0, long long t1, int* cnt) {
+    const int lane = threadIdx.x & 31, step = blockDim.x / 32;
+    long long t = t0 + (threadIdx.x >> 5);
+    float z[VPL], zn[VPL];
+    if (t < t1) load_row<VPL, T>(a, t, lane, z);
+    for (; t < t1; t += step) {
+        if (t + step < t1) load_row<VPL, T>(a, t + step, lane, zn);
+        choose<VPL>(a, t, lane, z, cnt);
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) z[v] = zn[v];
     }
 }
 
@@ -156,28 +174,47 @@ constexpr int SUB = 128;  // tokens whose ranks are counted at once
 // token chooses an expert at most once, so a choice's rank among 128 tokens is
 // the number of lower bits of its expert's 128-bit mask: no order of atomics
 // can change it.
-__device__ __forceinline__ void place(const RouteArgs& a, long long t0, long long t1, int* base,
+// Choices of 128 tokens that a thread has, at most (the small kernel's smaller
+// blocks have no more than one a thread).
+constexpr int PER_THREAD = SUB * MAX_TOPK / ROUTE_THREADS;
+
+// The thread's choices among the tokens [s, min(s + SUB, t1)).
+__device__ __forceinline__ int load_choices(const RouteArgs& a, long long s, long long t1, int (&e)[PER_THREAD]) {
+    const int n = static_cast<int>(min(t1 - s, static_cast<long long>(SUB))) * a.topk;
+#pragma unroll
+    for (int u = 0; u < PER_THREAD; ++u) {
+        const int i = threadIdx.x + u * blockDim.x;
+        e[u] = i < n ? a.expert[s * a.topk + i] : -1;
+    }
+    return n;
+}
+
+// e: load_choices() of the first SUB tokens.
+__device__ __forceinline__ void place(const RouteArgs& a, long long t0, long long t1, int (&e)[PER_THREAD], int* base,
                                       unsigned (*mask)[SUB / 32]) {
     const int tid = threadIdx.x;
     for (long long s = t0; s < t1; s += SUB) {
+        if (s > t0) load_choices(a, s, t1, e);
         const int n = static_cast<int>(min(t1 - s, static_cast<long long>(SUB))) * a.topk;
         for (int i = tid; i < MAX_EXPERTS * (SUB / 32); i += blockDim.x) (&mask[0][0])[i] = 0u;
         __syncthreads();
-        for (int i = tid; i < n; i += blockDim.x) {
-            const int e = a.expert[s * a.topk + i];
-            const int tl = i / a.topk;
-            if (e >= 0) atomicOr(&mask[e][tl >> 5], 1u << (tl & 31));
+#pragma unroll
+        for (int u = 0; u < PER_THREAD; ++u) {
+            const int tl = (tid + u * static_cast<int>(blockDim.x)) / a.topk;
+            if (e[u] >= 0) atomicOr(&mask[e[u]][tl >> 5], 1u << (tl & 31));
         }
         __syncthreads();
-        for (int i = tid; i < n; i += blockDim.x) {
-            const int e = a.expert[s * a.topk + i];
+#pragma unroll
+        for (int u = 0; u < PER_THREAD; ++u) {
+            const int i = tid + u * static_cast<int>(blockDim.x);
+            if (i >= n) break;
             const int tl = i / a.topk;
             int row = -1;
-            if (e >= 0) {
-                row = base[e];
+            if (e[u] >= 0) {
+                row = base[e[u]];
 #pragma unroll
                 for (int w = 0; w < SUB / 32; ++w) {
-                    const unsigned m = mask[e][w];
+                    const unsigned m = mask[e[u]][w];
                     const int lo = tl - w * 32;  // tokens below this one in word w
                     row += __popc(lo >= 32 ? m : lo > 0 ? m & ((1u << lo) - 1u) : 0u);
                 }
@@ -200,13 +237,13 @@ __device__ __forceinline__ void place(const RouteArgs& a, long long t0, long lon
 template <int VPL, typename T>
 __global__ void __launch_bounds__(ROUTE_THREADS) zb_moe_choose_kernel(const RouteArgs a) {
     __shared__ int cnt[MAX_EXPERTS];
-    const int tid = threadIdx.x, lane = tid & 31;
+    const int tid = threadIdx.x;
     if (tid < MAX_EXPERTS) cnt[tid] = 0;
     zbp::allow_dependent_launch();
     __syncthreads();
     const long long t0 = static_cast<long long>(blockIdx.x) * a.per_block;
     const long long t1 = min(t0 + a.per_block, a.tokens);
-    for (long long t = t0 + (tid >> 5); t < t1; t += ROUTE_THREADS / 32) choose<VPL, T>(a, t, lane, cnt);
+    choose_all<VPL, T>(a, t0, t1, cnt);
     __syncthreads();
     if (tid < a.experts) a.hist[static_cast<long long>(blockIdx.x) * a.experts + tid] = cnt[tid];
 }
@@ -222,6 +259,10 @@ __global__ void __launch_bounds__(ROUTE_THREADS) zb_moe_place_kernel(const Route
     if (tid < MAX_EXPERTS) base[tid] = before[tid] = 0;
     __syncthreads();
     zbp::grid_dependency_wait();
+    const long long t0 = static_cast<long long>(blockIdx.x) * a.per_block;
+    const long long t1 = min(t0 + a.per_block, a.tokens);
+    int mine[PER_THREAD];
+    load_choices(a, t0, t1, mine);
     const int blocks = gridDim.x;
     // as many threads an expert as fit, each with every such-th block
     const int lg = 32 - __clz(a.experts - 1 | 1);  // 2^lg >= experts
@@ -254,8 +295,7 @@ __global__ void __launch_bounds__(ROUTE_THREADS) zb_moe_place_kernel(const Route
     __syncthreads();
     if (tid < MAX_EXPERTS) base[tid] += before[tid];
     __syncthreads();
-    const long long t0 = static_cast<long long>(blockIdx.x) * a.per_block;
-    place(a, t0, min(t0 + a.per_block, a.tokens), base, mask);
+    place(a, t0, t1, mine, base, mask);
 }
 
 // Few tokens: one block does all of it in one launch.
@@ -264,11 +304,13 @@ __global__ void __launch_bounds__(ROUTE_THREADS) zb_moe_route_small_kernel(const
     __shared__ int base[MAX_EXPERTS];
     __shared__ unsigned mask[MAX_EXPERTS][SUB / 32];
     __shared__ int total;
-    const int tid = threadIdx.x, lane = tid & 31;
+    const int tid = threadIdx.x;
     if (tid < MAX_EXPERTS) base[tid] = 0;
     __syncthreads();
-    for (long long t = tid >> 5; t < a.tokens; t += blockDim.x / 32) choose<VPL, T>(a, t, lane, base);
+    choose_all<VPL, T>(a, 0, a.tokens, base);
     __syncthreads();  // also: the block's expert[] is visible to all of it
+    int e[PER_THREAD];
+    load_choices(a, 0, a.tokens, e);
     if (tid < 32) {
         const int sum = scan_experts(base, tid);
         if (tid == 0) total = sum;
@@ -277,7 +319,7 @@ __global__ void __launch_bounds__(ROUTE_THREADS) zb_moe_route_small_kernel(const
     if (tid < a.experts) a.offsets[tid] = base[tid];
     if (tid == 0) a.offsets[a.experts] = total;
     for (long long p = total + tid; p < a.tokens * a.topk; p += blockDim.x) a.token_of[p] = -1;
-    place(a, 0, a.tokens, base, mask);
+    place(a, 0, a.tokens, e, base, mask);
 }
 
 // ---------------------------------------------------------------- gradient
