@@ -181,3 +181,30 @@ def by_expert(offsets, A, W, bias=None):
 
 
 gelu, gelu_prime = ob.gelu, ob.gelu_prime
+
+
+# --------------------------------------------------------------------------
+# a whole layer
+# --------------------------------------------------------------------------
+def layer_forward(X, logits, k, renorm, W1, W2, act="gelu_erf"):
+    """Router, dispatch, experts and combine: (out, everything B and W need)."""
+    gates, expert, offsets, row_of, token_of = route(logits, k, renorm)
+    Xp = X[token_of[:int(offsets[-1])]]
+    H, _ = by_expert(offsets, Xp, W1)
+    A = gelu(H, act)
+    Y, _ = by_expert(offsets, A, W2)
+    return combine(Y, row_of, gates), dict(gates=gates, expert=expert, offsets=offsets, row_of=row_of, X=Xp, H=H, A=A,
+                                           Y=Y)
+
+
+def layer_backward(dout, logits, renorm, W1, W2, s, act="gelu_erf"):
+    """Gradients of sum(out * dout): (dX, dlogits, dW1, dW2)."""
+    dY, dg = combine_backward(dout, s["Y"], s["row_of"], s["gates"])
+    dA, _ = by_expert(s["offsets"], dY, W2.transpose(0, 2, 1))
+    dH = dA * gelu_prime(s["H"], act)
+    dXp, _ = by_expert(s["offsets"], dH, W1.transpose(0, 2, 1))
+    dW1, dW2 = np.zeros_like(W1), np.zeros_like(W2)
+    for e, a, b in spans(s["offsets"]):
+        dW1[e] = s["X"][a:b].T @ dH[a:b]
+        dW2[e] = s["A"][a:b].T @ dY[a:b]
+    return combine(dXp, s["row_of"]), route_backward(logits, s["expert"], dg, renorm), dW1, dW2

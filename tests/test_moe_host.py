@@ -178,3 +178,30 @@ def test_route_backward_by_differences():
                 d[t, i] = 1e-6
                 up, down = om.route(z + d, 2, renorm)[0], om.route(z - d, 2, renorm)[0]
                 assert abs(((up - down) * dg).sum() / 2e-6 - grad[t, i]) < 1e-8
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+def test_oracle_layer_gradients_by_differences(renorm):
+    """Router, dispatch, experts, combine: every gradient against central
+    differences of the layer's output (choices do not change at these steps)."""
+    rng = np.random.default_rng(3)
+    T, E, k, h, f = 5, 4, 2, 3, 4
+    X, z = rng.normal(size=(T, h)), rng.normal(size=(T, E))
+    W1, W2, dout = rng.normal(size=(E, h, f)), rng.normal(size=(E, f, h)), rng.normal(size=(T, h))
+    _, s = om.layer_forward(X, z, k, renorm, W1, W2)
+    grads = om.layer_backward(dout, z, renorm, W1, W2, s)
+    args = [X, z, W1, W2]
+
+    def value():
+        return (om.layer_forward(args[0], args[1], k, renorm, args[2], args[3])[0] * dout).sum()
+
+    for a, g in zip(args, grads):
+        for i in np.ndindex(a.shape):
+            old = a[i]
+            a[i] = old + 1e-6
+            up = value()
+            a[i] = old - 1e-6
+            down = value()
+            a[i] = old
+            # central differences: O(step^2) plus rounding of the values over the step
+            assert abs((up - down) / 2e-6 - g[i]) < 1e-7 * max(1.0, abs(g[i]))
