@@ -673,8 +673,7 @@ zb_status zb_moe_backward_weight(const zb_moe* m, const int32_t* offsets, const 
  * for each 128 x 128 block of W: x = scale * q.  The quantisers take as scale
  * the least power of two s with amax / s <= 448 (at least 2^-126; 1 for a
  * block of zeros), so that x / s is exact and the only rounding is e4m3's own
- * (to nearest, ties to even); the product takes any fp32 scales.  A block with
- * a NaN or an infinity gets the scale NaN, so that what it touches is NaN.  A
+ * (to nearest, ties to even).  A block with a NaN or an infinity gets the scale NaN, so that what it touches is NaN.  A
  * last block may be narrower than 128. */
 
 /* X[rows,cols] bf16 -> Q[rows,cols] e4m3 and S[rows, ceil(cols/128)].  cols is
@@ -695,6 +694,11 @@ typedef enum zb_fp8_epilogue {
     ZB_FP8_GELU_GRAD = 2  /* out0 = D * GeLU'(H)                                */
 } zb_fp8_epilogue;
 
+/* Powers of two, as the quantisers make them, are applied by the tensor cores
+ * (of another positive scale only the power of two below it would count);
+ * other fp32 scales, block by block, on the way to fp32 sums (slower). */
+typedef enum zb_fp8_scales { ZB_FP8_SCALE_POW2 = 0, ZB_FP8_SCALE_ANY = 1 } zb_fp8_scales;
+
 /* D[M,N] = X W_e^T by expert: row r of expert e has
  *   D[r,n] = sum_b xs[r,b] ws[e,n/128,b] sum_{k in block b} xq[r,k] wq[e,n,k]
  * with xq[M,K], xs[M,ceil(K/128)], wq[E,N,K], ws[E,ceil(N/128),ceil(K/128)].
@@ -706,7 +710,7 @@ typedef struct zb_fp8_gemm {
     int32_t experts;
     int32_t epilogue;  /* zb_fp8_epilogue                                      */
     int32_t act;       /* ZB_ACT_GELU_ERF or ZB_ACT_GELU_TANH (GeLU epilogues) */
-    int32_t reserved;  /* must be 0                                            */
+    int32_t scales;    /* zb_fp8_scales                                        */
 } zb_fp8_gemm;
 zb_status zb_fp8_matmul(const zb_fp8_gemm* g, const int32_t* offsets, const void* Xq, const float* xs,
                         const void* Wq, const float* ws, const void* bias, const void* H, void* out0,

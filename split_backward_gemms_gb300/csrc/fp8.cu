@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(256)
 // loaded values: more than the 168 of an equal share.
 constexpr int FP8_THREADS = 384;
 constexpr int FP8_EPI_WARPS = 8;
-constexpr int FP8_REGS_LOW = 40, FP8_REGS_HIGH = 232;
+constexpr int FP8_REGS_LOW = 72, FP8_REGS_HIGH = 216;
 static_assert(128 * FP8_REGS_LOW + 256 * FP8_REGS_HIGH <= FP8_THREADS * 168, "register split");
 
 template <int CG>
@@ -155,11 +155,23 @@ struct Fp8Epi {
     static constexpr int BOXES = EPI == ZB_FP8_GELU_GRAD ? 4 : 2;
     static constexpr int STAGES = CG == 1 ? 3 : EPI == ZB_FP8_GELU_GRAD ? 4 : 5;
 };
+// Scales that are powers of two (MX) are applied by the tensor core itself.
+// Warps 2 and 3 write a group of four K blocks' exponents into shared memory as
+// the MMA reads them: 32 rows of 16 bytes for 128 rows of an operand, byte 4 r + k
+// of row i the scale of operand row i + 32 r in block k.
+constexpr int MX_SLOTS = 4;       // groups in shared memory
+constexpr uint32_t MX_TMEM = 256;  // first TMEM column of the scales, 16 a group
+struct __align__(128) MxGroup {
+    uint4 a[32];     // the CTA's 128 rows
+    uint4 b[2][32];  // the tile's 256 columns
+};
 constexpr uint32_t FP8_BOX = 32 * 64;  // 32 rows x 32 columns of bf16
 
 struct Fp8Ctl {
+    MxGroup scale[MX_SLOTS];
     uint64_t full[6], empty[6], tfull[2], tempty[2], drain[2];
     uint64_t hbar[FP8_EPI_WARPS];
+    uint64_t sfull[MX_SLOTS], sempty[MX_SLOTS];
     uint32_t tmem_base;
     int abort_flag;
     int off[MAX_EXPERTS + 1];
@@ -182,7 +194,7 @@ struct Fp8Args {
     unsigned int* err;
 };
 
-template <int EPI, int CG>
+template <int EPI, int CG, int MX>
 __global__ void __launch_bounds__(FP8_THREADS, 1)
     zb_fp8_matmul_kernel(const __grid_constant__ CUtensorMap tmA128, const __grid_constant__ CUtensorMap tmA32,
                          const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmO0,
@@ -214,6 +226,10 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
             zbp::mbar_init(zbp::smem_u32(&ctl->tfull[b]), 1);
             zbp::mbar_init(zbp::smem_u32(&ctl->tempty[b]), FP8_EPI_WARPS * CG);
             zbp::mbar_init(zbp::smem_u32(&ctl->drain[b]), 1);
+        }
+        for (int g = 0; g < MX_SLOTS; ++g) {
+            zbp::mbar_init(zbp::smem_u32(&ctl->sfull[g]), 2 * CG);
+            zbp::mbar_init(zbp::smem_u32(&ctl->sempty[g]), 1);
         }
         if (GRAD)
             for (int w = 0; w < FP8_EPI_WARPS; ++w) zbp::mbar_init(zbp::smem_u32(&ctl->hbar[w]), 1);
@@ -314,7 +330,148 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
                     wait_bar<false>(zbp::smem_u32(&ctl->full[i % STAGES]), (i / STAGES) & 1u, abort_flag, args.err,
                                     ERR_WAIT_PRODUCER, DRAIN_LIMIT_NS, false);
             }
-        } else if ((warp == 1 || warp == 2) && leader) {
+        } else if (MX && warp == 1 && leader) {
+            // ------------------------------------------------ MMA issuer (MX)
+            // One accumulator of 256 columns for the whole of K: the epilogue
+            // takes it into registers before it does anything else.
+            constexpr uint32_t idesc = zbp::idesc_mx_e4m3(128 * CG, 256, 0);
+            constexpr uint32_t hi = zbp::desc_hi(1024);
+            const uint32_t lo0 = zbp::desc_lo(zbp::smem_u32(smem), 16);
+            const uint32_t full0 = zbp::smem_u32(&ctl->full[0]), empty0 = zbp::smem_u32(&ctl->empty[0]);
+            const uint32_t sfull0 = zbp::smem_u32(&ctl->sfull[0]), sempty0 = zbp::smem_u32(&ctl->sempty[0]);
+            uint32_t s = 0, sp = 0, g = 0, done = 0;  // stage and phase; scale groups; tiles
+            bool ok = true;
+            for (int tile = cluster; ok && walk.to(tile, row0, nrows, nb); tile += clusters, ++done) {
+                if (!wait_bar<false>(zbp::smem_u32(&ctl->tempty[0]), (done & 1u) ^ 1u, abort_flag, args.err, ERR_WAIT_MMA,
+                                     WAIT_LIMIT_NS, true))
+                    break;
+                zbp::tc_fence_after();
+                for (int kb = 0; kb < num_kb; ++kb) {
+                    const uint32_t slot = g % MX_SLOTS, sf = tmem_base + MX_TMEM + (g & 7u) * 16u;
+                    if ((kb & 3) == 0) {
+                        if (!wait_bar<true>(sfull0 + slot * 8u, (g / MX_SLOTS) & 1u, abort_flag, args.err, ERR_WAIT_MMA,
+                                            WAIT_LIMIT_NS, true)) {
+                            ok = false;
+                            break;
+                        }
+                        zbp::tc_fence_after();
+                        if (zbp::elect_one()) {
+                            const uint32_t src = zbp::smem_u32(&ctl->scale[slot]);
+#pragma unroll
+                            for (uint32_t i = 0; i < 3; ++i) {
+                                if (PAIR)
+                                    zbp::tc_copy_32x128b_pair(sf + 4 * i, zbp::smem_desc_rows16(src + 512 * i));
+                                else
+                                    zbp::tc_copy_32x128b(sf + 4 * i, zbp::smem_desc_rows16(src + 512 * i));
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    if (!wait_bar<false>(full0 + s * 8u, sp, abort_flag, args.err, ERR_WAIT_MMA, WAIT_LIMIT_NS, true)) {
+                        ok = false;
+                        break;
+                    }
+                    zbp::tc_fence_after();
+                    const bool last = kb + 1 == num_kb, group_end = last || (kb & 3) == 3;
+                    if (zbp::elect_one()) {
+                        const uint32_t a = lo0 + s * (C::STAGE >> 4), b = a + (C::A_BYTES8 >> 4);
+                        const uint32_t id = static_cast<uint32_t>(kb & 3), dsc = idesc | (id << 4) | (id << 29);
+                        if (PAIR) {
+                            zbp::mma4_mx_pair(tmem_base, a, b, hi, dsc, sf, sf + 4, kb != 0);
+                            zbp::tc_commit_pair_multicast(empty0 + s * 8u, 0x3);
+                            if (group_end) zbp::tc_commit_pair_multicast(sempty0 + slot * 8u, 0x3);
+                            if (last) zbp::tc_commit_pair_multicast(zbp::smem_u32(&ctl->tfull[0]), 0x3);
+                        } else {
+                            zbp::mma4_mx(tmem_base, a, b, hi, dsc, sf, sf + 4, kb != 0);
+                            zbp::tc_commit(empty0 + s * 8u);
+                            if (group_end) zbp::tc_commit(sempty0 + slot * 8u);
+                            if (last) zbp::tc_commit(zbp::smem_u32(&ctl->tfull[0]));
+                        }
+                    }
+                    __syncwarp();
+                    if (group_end) ++g;
+                    if (++s == STAGES) {
+                        s = 0;
+                        sp ^= 1u;
+                    }
+                }
+            }
+            // every MMA issued here completes before TMEM is released
+            const uint32_t drain = zbp::smem_u32(&ctl->drain[0]);
+            if (zbp::elect_one()) {
+                if (PAIR)
+                    zbp::tc_commit_pair(drain);
+                else
+                    zbp::tc_commit(drain);
+            }
+            __syncwarp();
+            wait_bar<false>(drain, 0, abort_flag, args.err, ERR_WAIT_MMA, DRAIN_LIMIT_NS, false);
+        } else if (MX && warp >= 2) {
+            // ------------------------------------------------ scales (MX)
+            // Warp 2 has the CTA's rows 0-63 and the tile's first 128 columns,
+            // warp 3 the others; a lane has two rows.  The next group is asked
+            // for before the current one is handed over.
+            const int hw = warp - 2;
+            const bool vec = (num_kb & 3) == 0 && (reinterpret_cast<uintptr_t>(args.xs) & 15u) == 0;
+            uint32_t g = 0;
+            bool ok = true;
+            for (int tile = cluster; ok && walk.to(tile, row0, nrows, nb); tile += clusters) {
+                const int row = row0 + static_cast<int>(rank) * 128 + hw * 64 + lane, end = row0 + nrows;
+                const float* x0 = args.xs + static_cast<long long>(min(row, end - 1)) * num_kb;
+                const float* x1 = args.xs + static_cast<long long>(min(row + 32, end - 1)) * num_kb;
+                const float* w =
+                    args.ws + (static_cast<long long>(walk.e) * n_blocks + min(nb * 2 + hw, n_blocks - 1)) * num_kb;
+                float a[4], b[4], c = 0.0f;
+                auto ask = [&](int k0) {
+                    if (vec) {
+                        const float4 u = __ldg(reinterpret_cast<const float4*>(x0 + k0));
+                        const float4 v = __ldg(reinterpret_cast<const float4*>(x1 + k0));
+                        a[0] = u.x, a[1] = u.y, a[2] = u.z, a[3] = u.w;
+                        b[0] = v.x, b[1] = v.y, b[2] = v.z, b[3] = v.w;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int k = min(k0 + i, num_kb - 1);
+                            a[i] = __ldg(x0 + k);
+                            b[i] = __ldg(x1 + k);
+                        }
+                    }
+                    c = __ldg(w + min(k0 + (lane & 3), num_kb - 1));
+                };
+                // a scale's exponent in byte i
+                auto byte = [](float f, int i) { return ((__float_as_uint(f) >> 23) & 0xffu) << (8 * i); };
+                ask(0);
+                for (int k0 = 0; k0 < num_kb; k0 += 4, ++g) {
+                    const uint32_t slot = g % MX_SLOTS;
+                    uint32_t wa = 0, wb = 0, wc = byte(c, lane & 3);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        wa |= byte(a[i], i);
+                        wb |= byte(b[i], i);
+                    }
+                    wc |= __shfl_xor_sync(0xffffffffu, wc, 1);
+                    wc |= __shfl_xor_sync(0xffffffffu, wc, 2);
+                    if (k0 + 4 < num_kb) ask(k0 + 4);
+                    if (!wait_bar<false>(zbp::smem_u32(&ctl->sempty[slot]), ((g / MX_SLOTS) & 1u) ^ 1u, abort_flag, args.err,
+                                         ERR_WAIT_PRODUCER, WAIT_LIMIT_NS, true)) {
+                        ok = false;
+                        break;
+                    }
+                    MxGroup& m = ctl->scale[slot];
+                    reinterpret_cast<uint2*>(&m.a[lane])[hw] = make_uint2(wa, wb);
+                    m.b[hw][lane] = make_uint4(wc, wc, wc, wc);
+                    zbp::fence_proxy_async_smem();  // read by the tensor core's copies next
+                    __syncwarp();
+                    if (lane == 0) {
+                        const uint32_t bar = zbp::smem_u32(&ctl->sfull[slot]);
+                        if (PAIR)
+                            zbp::mbar_arrive_cluster(zbp::mapa_shared(bar, 0));
+                        else
+                            zbp::mbar_arrive(bar);
+                    }
+                }
+            }
+        } else if (!MX && (warp == 1 || warp == 2) && leader) {
             // ------------------------------------------------ MMA issuers
             // Warp 1 issues the even blocks of K (into accumulator 0), warp 2
             // the odd ones: a block's two waits, four MMAs and two commits take
@@ -397,10 +554,38 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
                 }
                 ++asked;
             }
+            f32x2 sum[64];
+            if (MX) {
+                if (!wait_bar<false>(zbp::smem_u32(&ctl->tfull[0]), it & 1u, abort_flag, args.err, ERR_WAIT_EPI, WAIT_LIMIT_NS,
+                                     true)) {
+                    ok = false;
+                    break;
+                }
+                ++it;
+                zbp::tc_fence_after();
+                const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + c_lo;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t v[32];
+                    zbp::tmem_ld_32x32b_x32(taddr + c * 32, v);
+                    zbp::tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        sum[c * 16 + i] = pk2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                }
+                zbp::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    const uint32_t te = zbp::smem_u32(&ctl->tempty[0]);
+                    if (PAIR)
+                        zbp::mbar_arrive_remote(zbp::mapa_shared(te, 0));
+                    else
+                        zbp::mbar_arrive(te);
+                }
+            } else {
             const bool scaled = lane < live && n0 < args.N;
             const float* xs = args.xs + static_cast<long long>(scaled ? first + lane : 0) * num_kb;
             const float* ws = args.ws + (static_cast<long long>(walk.e) * n_blocks + (scaled ? n0 / BLK : 0)) * num_kb;
-            f32x2 sum[64];
 #pragma unroll
             for (int i = 0; i < 64; ++i) sum[i] = 0ull;
             float xn = scaled ? __ldg(xs) : 0.0f, wn = scaled ? __ldg(ws) : 0.0f;
@@ -439,6 +624,7 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
                     else
                         zbp::mbar_arrive(te);
                 }
+            }
             }
             if (!ok) break;
             if (live <= 0 || n0 >= args.N) continue;
@@ -550,9 +736,9 @@ zb_status launched(const char* who) {
     return ZB_OK;
 }
 
-template <int EPI, int CG>
+template <int EPI, int CG, int MX>
 zb_status launch_fp8(const CUtensorMap (&mp)[5], const Fp8Args& a, long long tiles, void* stream) {
-    auto kern = zb_fp8_matmul_kernel<EPI, CG>;
+    auto kern = zb_fp8_matmul_kernel<EPI, CG, MX>;
     static std::atomic<int> cache[64];
     int ctas = 0;
     zb_status s = full_grid(kern, cache, fp8_smem<EPI, CG>(), FP8_THREADS, CG, &ctas);
@@ -561,6 +747,12 @@ zb_status launch_fp8(const CUtensorMap (&mp)[5], const Fp8Args& a, long long til
     const cudaError_t e = cudaLaunchKernelEx(&lc.cfg, kern, mp[0], mp[1], mp[2], mp[3], mp[4], a);
     if (e != cudaSuccess) return zb::fail(ZB_ERR_CUDA, std::string("zb_fp8_matmul launch: ") + cudaGetErrorString(e));
     return launched("zb_fp8_matmul");
+}
+
+template <int EPI>
+zb_status launch_fp8_by(bool pair, bool mx, const CUtensorMap (&mp)[5], const Fp8Args& a, long long tiles, void* stream) {
+    if (mx) return pair ? launch_fp8<EPI, 2, 1>(mp, a, tiles, stream) : launch_fp8<EPI, 1, 1>(mp, a, tiles, stream);
+    return pair ? launch_fp8<EPI, 2, 0>(mp, a, tiles, stream) : launch_fp8<EPI, 1, 0>(mp, a, tiles, stream);
 }
 
 // 2-D map of e4m3 rows, 128 bytes wide boxes, 128-byte swizzle.
@@ -625,7 +817,8 @@ extern "C" zb_status zb_fp8_matmul(const zb_fp8_gemm* g, const int32_t* offsets,
                                    const void* Wq, const float* ws, const void* bias, const void* H, void* out0,
                                    void* out1, void* stream) {
     if (!g) return zb::fail(ZB_ERR_INVALID_ARG, "zb_fp8_matmul: descriptor is NULL");
-    if (g->reserved) return zb::fail(ZB_ERR_INVALID_ARG, "zb_fp8_matmul: reserved must be 0");
+    if (g->scales != ZB_FP8_SCALE_POW2 && g->scales != ZB_FP8_SCALE_ANY)
+        return zb::fail(ZB_ERR_INVALID_ARG, "zb_fp8_matmul: unknown kind of scales");
     if (g->epilogue < ZB_FP8_STORE || g->epilogue > ZB_FP8_GELU_GRAD)
         return zb::fail(ZB_ERR_INVALID_ARG, "zb_fp8_matmul: unknown epilogue");
     if (g->epilogue != ZB_FP8_STORE && g->act != ZB_ACT_GELU_ERF && g->act != ZB_ACT_GELU_TANH)
@@ -678,13 +871,10 @@ extern "C" zb_status zb_fp8_matmul(const zb_fp8_gemm* g, const int32_t* offsets,
     a.K = static_cast<int>(g->K);
     a.act = g->act;
     a.err = err;
+    const bool mx = g->scales == ZB_FP8_SCALE_POW2;
     switch (g->epilogue) {
-        case ZB_FP8_STORE:
-            return pair ? launch_fp8<ZB_FP8_STORE, 2>(mp, a, most, stream) : launch_fp8<ZB_FP8_STORE, 1>(mp, a, most, stream);
-        case ZB_FP8_GELU:
-            return pair ? launch_fp8<ZB_FP8_GELU, 2>(mp, a, most, stream) : launch_fp8<ZB_FP8_GELU, 1>(mp, a, most, stream);
-        default:
-            return pair ? launch_fp8<ZB_FP8_GELU_GRAD, 2>(mp, a, most, stream)
-                        : launch_fp8<ZB_FP8_GELU_GRAD, 1>(mp, a, most, stream);
+        case ZB_FP8_STORE: return launch_fp8_by<ZB_FP8_STORE>(pair, mx, mp, a, most, stream);
+        case ZB_FP8_GELU: return launch_fp8_by<ZB_FP8_GELU>(pair, mx, mp, a, most, stream);
+        default: return launch_fp8_by<ZB_FP8_GELU_GRAD>(pair, mx, mp, a, most, stream);
     }
 }

@@ -41,6 +41,7 @@ ZB_ACT_NONE = 0
 ZB_ACT_GELU_ERF = 1
 ZB_ACT_GELU_TANH = 2
 ZB_FP8_STORE, ZB_FP8_GELU, ZB_FP8_GELU_GRAD = range(3)
+ZB_FP8_SCALE_POW2, ZB_FP8_SCALE_ANY = range(2)
 ZB_BLOCK_NO_SPLIT_K = 1  # zb_block.flags: single passes never split K
 
 ZB_OP_F, ZB_OP_B, ZB_OP_W, ZB_OP_BW, ZB_OP_OPT = range(5)
@@ -122,7 +123,7 @@ class zb_moe(C.Structure):
 
 class zb_fp8_gemm(C.Structure):
     _fields_ = [("M", C.c_int64), ("N", C.c_int64), ("K", C.c_int64), ("experts", C.c_int32),
-                ("epilogue", C.c_int32), ("act", C.c_int32), ("reserved", C.c_int32)]
+                ("epilogue", C.c_int32), ("act", C.c_int32), ("scales", C.c_int32)]
 
 
 class ZBError(RuntimeError):
@@ -565,8 +566,9 @@ def zb_fp8_quantize_weight(experts: int, rows: int, cols: int, W, Q, S, QT, ST, 
 
 
 def make_fp8_matmul(M: int, N: int, K: int, experts: int = 1, epilogue: int = ZB_FP8_STORE,
-                    act: int = ZB_ACT_GELU_ERF) -> zb_fp8_gemm:
-    return zb_fp8_gemm(M, N, K, experts, epilogue, act, 0)
+                    act: int = ZB_ACT_GELU_ERF, scales: int = ZB_FP8_SCALE_POW2) -> zb_fp8_gemm:
+    """scales: ZB_FP8_SCALE_POW2 (what the quantisers make) or ZB_FP8_SCALE_ANY."""
+    return zb_fp8_gemm(M, N, K, experts, epilogue, act, scales)
 
 
 def zb_fp8_matmul(g, offsets, Xq, xs, Wq, ws, H, out0, out1, bias=None, stream=None):

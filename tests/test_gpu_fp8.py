@@ -140,7 +140,8 @@ def test_matmul(zb, case, scales):
     o0, o1 = empty_bf16(M, N), empty_bf16(M, N)
     acts = {"erf": zb.ZB_ACT_GELU_ERF, "tanh": zb.ZB_ACT_GELU_TANH}
     epis = {"store": zb.ZB_FP8_STORE, "gelu": zb.ZB_FP8_GELU, "grad": zb.ZB_FP8_GELU_GRAD}
-    g = zb.make_fp8_matmul(M, N, K, E, epis[epi], acts[act])
+    g = zb.make_fp8_matmul(M, N, K, E, epis[epi], acts[act],
+                           zb.ZB_FP8_SCALE_ANY if scales == "any" else zb.ZB_FP8_SCALE_POW2)
     zb.zb_fp8_matmul(g, None if dense else i32(off), Xq, Xs, Wq, ST, H if epi == "grad" else None, o0,
                      o1 if epi == "gelu" else None, bias=b)
     sync(zb)

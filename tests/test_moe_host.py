@@ -132,7 +132,7 @@ def test_fp8_refuses(zb):
     for field, value, status in (("K", 24, "ALIGN"), ("N", 12, "ALIGN"), ("M", -1, "SHAPE"), ("K", 0, "SHAPE"),
                                  ("N", 0, "SHAPE"), ("experts", 0, "SHAPE"), ("experts", 300, "SHAPE"),
                                  ("epilogue", 3, "INVALID_ARG"), ("act", 0, "INVALID_ARG"),
-                                 ("reserved", 1, "INVALID_ARG")):
+                                 ("scales", 2, "INVALID_ARG")):
         g = zb.make_fp8_matmul(4, 64, 32, experts=2, epilogue=zb.ZB_FP8_GELU)
         setattr(g, field, value)
         refused(zb, getattr(zb, "ZB_ERR_" + status), zb.zb_fp8_matmul, g, *good, stream=0)
