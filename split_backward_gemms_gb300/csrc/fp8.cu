@@ -158,8 +158,11 @@ struct Fp8Epi {
 // Scales that are powers of two (MX) are applied by the tensor core itself.
 // Warps 2 and 3 write a group of four K blocks' exponents into shared memory as
 // the MMA reads them: 32 rows of 16 bytes for 128 rows of an operand, byte 4 r + k
-// of row i the scale of operand row i + 32 r in block k.
-constexpr int MX_SLOTS = 4;       // groups in shared memory
+// of row i the scale of operand row i + 32 r in block k.  Four groups are loaded
+// and handed over at once: with one, the loads' latency and the cluster-scope
+// release (about 2000 cycles) took longer than the group's MMAs.
+constexpr int MX_GROUPS = 4;      // groups in a batch
+constexpr int MX_SLOTS = 2;       // batches in shared memory
 constexpr uint32_t MX_TMEM = 256;  // first TMEM column of the scales, 16 a group
 struct __align__(128) MxGroup {
     uint4 a[32];     // the CTA's 128 rows
@@ -168,7 +171,7 @@ struct __align__(128) MxGroup {
 constexpr uint32_t FP8_BOX = 32 * 64;  // 32 rows x 32 columns of bf16
 
 struct Fp8Ctl {
-    MxGroup scale[MX_SLOTS];
+    MxGroup scale[MX_SLOTS][MX_GROUPS];
     uint64_t full[6], empty[6], tfull[2], tempty[2], drain[2];
     uint64_t hbar[FP8_EPI_WARPS];
     uint64_t sfull[MX_SLOTS], sempty[MX_SLOTS];
@@ -339,7 +342,7 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
             const uint32_t lo0 = zbp::desc_lo(zbp::smem_u32(smem), 16);
             const uint32_t full0 = zbp::smem_u32(&ctl->full[0]), empty0 = zbp::smem_u32(&ctl->empty[0]);
             const uint32_t sfull0 = zbp::smem_u32(&ctl->sfull[0]), sempty0 = zbp::smem_u32(&ctl->sempty[0]);
-            uint32_t s = 0, sp = 0, g = 0, done = 0;  // stage and phase; scale groups; tiles
+            uint32_t s = 0, sp = 0, g = 0, batch = 0, done = 0;  // stage and phase; scale groups and batches; tiles
             bool ok = true;
             for (int tile = cluster; ok && walk.to(tile, row0, nrows, nb); tile += clusters, ++done) {
                 if (!wait_bar<false>(zbp::smem_u32(&ctl->tempty[0]), (done & 1u) ^ 1u, abort_flag, args.err, ERR_WAIT_MMA,
@@ -347,16 +350,18 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
                     break;
                 zbp::tc_fence_after();
                 for (int kb = 0; kb < num_kb; ++kb) {
-                    const uint32_t slot = g % MX_SLOTS, sf = tmem_base + MX_TMEM + (g & 7u) * 16u;
-                    if ((kb & 3) == 0) {
-                        if (!wait_bar<true>(sfull0 + slot * 8u, (g / MX_SLOTS) & 1u, abort_flag, args.err, ERR_WAIT_MMA,
-                                            WAIT_LIMIT_NS, true)) {
+                    const uint32_t slot = batch % MX_SLOTS, sf = tmem_base + MX_TMEM + (g & 7u) * 16u;
+                    if ((kb & 15) == 0) {
+                        if (!wait_bar<true>(sfull0 + slot * 8u, (batch / MX_SLOTS) & 1u, abort_flag, args.err,
+                                            ERR_WAIT_MMA, WAIT_LIMIT_NS, true)) {
                             ok = false;
                             break;
                         }
                         zbp::tc_fence_after();
+                    }
+                    if ((kb & 3) == 0) {
                         if (zbp::elect_one()) {
-                            const uint32_t src = zbp::smem_u32(&ctl->scale[slot]);
+                            const uint32_t src = zbp::smem_u32(&ctl->scale[slot][(kb >> 2) & 3]);
 #pragma unroll
                             for (uint32_t i = 0; i < 3; ++i) {
                                 if (PAIR)
@@ -372,24 +377,25 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
                         break;
                     }
                     zbp::tc_fence_after();
-                    const bool last = kb + 1 == num_kb, group_end = last || (kb & 3) == 3;
+                    const bool last = kb + 1 == num_kb, batch_end = last || (kb & 15) == 15;
                     if (zbp::elect_one()) {
                         const uint32_t a = lo0 + s * (C::STAGE >> 4), b = a + (C::A_BYTES8 >> 4);
                         const uint32_t id = static_cast<uint32_t>(kb & 3), dsc = idesc | (id << 4) | (id << 29);
                         if (PAIR) {
                             zbp::mma4_mx_pair(tmem_base, a, b, hi, dsc, sf, sf + 4, kb != 0);
                             zbp::tc_commit_pair_multicast(empty0 + s * 8u, 0x3);
-                            if (group_end) zbp::tc_commit_pair_multicast(sempty0 + slot * 8u, 0x3);
+                            if (batch_end) zbp::tc_commit_pair_multicast(sempty0 + slot * 8u, 0x3);
                             if (last) zbp::tc_commit_pair_multicast(zbp::smem_u32(&ctl->tfull[0]), 0x3);
                         } else {
                             zbp::mma4_mx(tmem_base, a, b, hi, dsc, sf, sf + 4, kb != 0);
                             zbp::tc_commit(empty0 + s * 8u);
-                            if (group_end) zbp::tc_commit(sempty0 + slot * 8u);
+                            if (batch_end) zbp::tc_commit(sempty0 + slot * 8u);
                             if (last) zbp::tc_commit(zbp::smem_u32(&ctl->tfull[0]));
                         }
                     }
                     __syncwarp();
-                    if (group_end) ++g;
+                    if (last || (kb & 3) == 3) ++g;
+                    if (batch_end) ++batch;
                     if (++s == STAGES) {
                         s = 0;
                         sp ^= 1u;
@@ -409,11 +415,10 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
         } else if (MX && warp >= 2) {
             // ------------------------------------------------ scales (MX)
             // Warp 2 has the CTA's rows 0-63 and the tile's first 128 columns,
-            // warp 3 the others; a lane has two rows.  The next group is asked
-            // for before the current one is handed over.
+            // warp 3 the others; a lane has two rows.
             const int hw = warp - 2;
             const bool vec = (num_kb & 3) == 0 && (reinterpret_cast<uintptr_t>(args.xs) & 15u) == 0;
-            uint32_t g = 0;
+            uint32_t batch = 0;
             bool ok = true;
             for (int tile = cluster; ok && walk.to(tile, row0, nrows, nb); tile += clusters) {
                 const int row = row0 + static_cast<int>(rank) * 128 + hw * 64 + lane, end = row0 + nrows;
@@ -421,45 +426,50 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
                 const float* x1 = args.xs + static_cast<long long>(min(row + 32, end - 1)) * num_kb;
                 const float* w =
                     args.ws + (static_cast<long long>(walk.e) * n_blocks + min(nb * 2 + hw, n_blocks - 1)) * num_kb;
-                float a[4], b[4], c = 0.0f;
-                auto ask = [&](int k0) {
+                for (int k16 = 0; k16 < num_kb; k16 += 16, ++batch) {
+                    float a[16], b[16];
                     if (vec) {
-                        const float4 u = __ldg(reinterpret_cast<const float4*>(x0 + k0));
-                        const float4 v = __ldg(reinterpret_cast<const float4*>(x1 + k0));
-                        a[0] = u.x, a[1] = u.y, a[2] = u.z, a[3] = u.w;
-                        b[0] = v.x, b[1] = v.y, b[2] = v.z, b[3] = v.w;
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4) {
+                            if (k16 + i >= num_kb) break;
+                            const float4 u = __ldg(reinterpret_cast<const float4*>(x0 + k16 + i));
+                            const float4 v = __ldg(reinterpret_cast<const float4*>(x1 + k16 + i));
+                            a[i] = u.x, a[i + 1] = u.y, a[i + 2] = u.z, a[i + 3] = u.w;
+                            b[i] = v.x, b[i + 1] = v.y, b[i + 2] = v.z, b[i + 3] = v.w;
+                        }
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int k = min(k0 + i, num_kb - 1);
-                            a[i] = __ldg(x0 + k);
-                            b[i] = __ldg(x1 + k);
+                        for (int i = 0; i < 16; ++i) {
+                            a[i] = b[i] = 1.0f;
+                            if (k16 + i < num_kb) {
+                                a[i] = __ldg(x0 + k16 + i);
+                                b[i] = __ldg(x1 + k16 + i);
+                            }
                         }
                     }
-                    c = __ldg(w + min(k0 + (lane & 3), num_kb - 1));
-                };
-                // a scale's exponent in byte i
-                auto byte = [](float f, int i) { return ((__float_as_uint(f) >> 23) & 0xffu) << (8 * i); };
-                ask(0);
-                for (int k0 = 0; k0 < num_kb; k0 += 4, ++g) {
-                    const uint32_t slot = g % MX_SLOTS;
-                    uint32_t wa = 0, wb = 0, wc = byte(c, lane & 3);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        wa |= byte(a[i], i);
-                        wb |= byte(b[i], i);
-                    }
-                    wc |= __shfl_xor_sync(0xffffffffu, wc, 1);
-                    wc |= __shfl_xor_sync(0xffffffffu, wc, 2);
-                    if (k0 + 4 < num_kb) ask(k0 + 4);
-                    if (!wait_bar<false>(zbp::smem_u32(&ctl->sempty[slot]), ((g / MX_SLOTS) & 1u) ^ 1u, abort_flag, args.err,
-                                         ERR_WAIT_PRODUCER, WAIT_LIMIT_NS, true)) {
+                    // a scale's exponent; lane i has that of the columns' block i
+                    auto exponent = [](float f) { return (__float_as_uint(f) >> 23) & 0xffu; };
+                    const uint32_t c = exponent(__ldg(w + min(k16 + (lane & 15), num_kb - 1)));
+                    const uint32_t slot = batch % MX_SLOTS;
+                    if (!wait_bar<false>(zbp::smem_u32(&ctl->sempty[slot]), ((batch / MX_SLOTS) & 1u) ^ 1u, abort_flag,
+                                         args.err, ERR_WAIT_PRODUCER, WAIT_LIMIT_NS, true)) {
                         ok = false;
                         break;
                     }
-                    MxGroup& m = ctl->scale[slot];
-                    reinterpret_cast<uint2*>(&m.a[lane])[hw] = make_uint2(wa, wb);
-                    m.b[hw][lane] = make_uint4(wc, wc, wc, wc);
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4) {
+                        if (k16 + j >= num_kb) break;
+                        uint32_t wa = 0, wb = 0, wc = 0;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            wa |= exponent(a[j + i]) << (8 * i);
+                            wb |= exponent(b[j + i]) << (8 * i);
+                            wc |= __shfl_sync(0xffffffffu, c, j + i) << (8 * i);
+                        }
+                        MxGroup& m = ctl->scale[slot][j / 4];
+                        reinterpret_cast<uint2*>(&m.a[lane])[hw] = make_uint2(wa, wb);
+                        m.b[hw][lane] = make_uint4(wc, wc, wc, wc);
+                    }
                     zbp::fence_proxy_async_smem();  // read by the tensor core's copies next
                     __syncwarp();
                     if (lane == 0) {
