@@ -134,13 +134,6 @@ __global__ void __launch_bounds__(256)
 // cycles for a block of a 128 x 256 tile, the FMAs of 8 warps 128 a scheduler,
 // the TMEM reads 256.
 //
-// Warps 0-3 give registers to warps 4-11, whose threads hold 128 sums and 32
-// loaded values: more than the 168 of an equal share.
-constexpr int FP8_THREADS = 384;
-constexpr int FP8_EPI_WARPS = 8;
-constexpr int FP8_REGS_LOW = 72, FP8_REGS_HIGH = 216;
-static_assert(128 * FP8_REGS_LOW + 256 * FP8_REGS_HIGH <= FP8_THREADS * 168, "register split");
-
 template <int CG>
 struct Fp8Cfg {
     static constexpr int TILE_T = 128 * CG;                       // rows of D per tile
@@ -148,13 +141,21 @@ struct Fp8Cfg {
     static constexpr uint32_t A_BYTES8 = 128 * 128;               // 128 rows x 128 k
     static constexpr uint32_t STAGE = A_BYTES8 + B_ROWS * 128;
 };
-// GeLU' keeps a warp's 32 x 128 values of H in four staging boxes (copied while
-// the product runs) and stores from them; the others store through two.
-template <int EPI, int CG>
+// Warps 0-3 give registers to the epilogue warps behind them.  MX: 16 of these,
+// with 64 columns each; else 8, whose threads hold 128 sums and 32 loaded values.
+// GeLU' keeps a warp's values of H in its staging boxes (copied while the product
+// runs) and stores from them; the others store through one box, or two.
+constexpr uint32_t FP8_BOX = 32 * 64;  // 32 rows x 32 columns of bf16
+template <int EPI, int CG, int MX>
 struct Fp8Epi {
-    static constexpr int BOXES = EPI == ZB_FP8_GELU_GRAD ? 4 : 2;
+    static constexpr int WARPS = MX ? 16 : 8;
+    static constexpr int THREADS = 128 + 32 * WARPS;
+    static constexpr int REGS_LOW = MX ? 64 : 72, REGS_HIGH = MX ? 104 : 216;
+    static constexpr int COLS = 1024 / WARPS;  // columns of a warp (four warps have the tile's rows)
+    static constexpr int BOXES = EPI == ZB_FP8_GELU_GRAD ? COLS / 32 : MX ? 1 : 2;
     static constexpr int STAGES = CG == 1 ? 3 : EPI == ZB_FP8_GELU_GRAD ? 4 : 5;
 };
+static_assert(128 * 64 + 512 * 104 <= 640 * 96 && 128 * 72 + 256 * 216 <= 384 * 168, "register split");
 // Scales that are powers of two (MX) are applied by the tensor core itself.
 // Warps 2 and 3 write a group of four K blocks' exponents into shared memory as
 // the MMA reads them: 32 rows of 16 bytes for 128 rows of an operand, byte 4 r + k
@@ -168,25 +169,26 @@ struct __align__(128) MxGroup {
     uint4 a[32];     // the CTA's 128 rows
     uint4 b[2][32];  // the tile's 256 columns
 };
-constexpr uint32_t FP8_BOX = 32 * 64;  // 32 rows x 32 columns of bf16
-
 struct Fp8Ctl {
     MxGroup scale[MX_SLOTS][MX_GROUPS];
     uint64_t full[6], empty[6], tfull[2], tempty[2], drain[2];
-    uint64_t hbar[FP8_EPI_WARPS];
+    uint64_t hbar[16];
     uint64_t sfull[MX_SLOTS], sempty[MX_SLOTS];
     uint32_t tmem_base;
     int abort_flag;
     int off[MAX_EXPERTS + 1];
 };
-template <int EPI, int CG>
+template <int EPI, int CG, int MX>
 constexpr size_t fp8_smem() {
-    return 1024 + Fp8Epi<EPI, CG>::STAGES * Fp8Cfg<CG>::STAGE + FP8_EPI_WARPS * Fp8Epi<EPI, CG>::BOXES * FP8_BOX +
-           sizeof(Fp8Ctl);
+    using E = Fp8Epi<EPI, CG, MX>;
+    return 1024 + E::STAGES * Fp8Cfg<CG>::STAGE + E::WARPS * E::BOXES * FP8_BOX + sizeof(Fp8Ctl);
 }
-static_assert(fp8_smem<ZB_FP8_STORE, 1>() <= 232448 && fp8_smem<ZB_FP8_STORE, 2>() <= 232448 &&
-                  fp8_smem<ZB_FP8_GELU_GRAD, 1>() <= 232448 && fp8_smem<ZB_FP8_GELU_GRAD, 2>() <= 232448,
-              "shared memory");
+template <int EPI>
+constexpr bool fp8_fits() {
+    return fp8_smem<EPI, 1, 0>() <= 232448 && fp8_smem<EPI, 2, 0>() <= 232448 && fp8_smem<EPI, 1, 1>() <= 232448 &&
+           fp8_smem<EPI, 2, 1>() <= 232448;
+}
+static_assert(fp8_fits<ZB_FP8_STORE>() && fp8_fits<ZB_FP8_GELU>() && fp8_fits<ZB_FP8_GELU_GRAD>(), "shared memory");
 
 struct Fp8Args {
     const int* offsets;  // nullptr: one expert with every row
@@ -198,19 +200,20 @@ struct Fp8Args {
 };
 
 template <int EPI, int CG, int MX>
-__global__ void __launch_bounds__(FP8_THREADS, 1)
+__global__ void __launch_bounds__(Fp8Epi<EPI, CG, MX>::THREADS, 1)
     zb_fp8_matmul_kernel(const __grid_constant__ CUtensorMap tmA128, const __grid_constant__ CUtensorMap tmA32,
                          const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmO0,
                          const __grid_constant__ CUtensorMap tmO1, const Fp8Args args) {
     using C = Fp8Cfg<CG>;
     constexpr bool PAIR = CG == 2;
-    constexpr int STAGES = Fp8Epi<EPI, CG>::STAGES;
-    constexpr int BOXES = Fp8Epi<EPI, CG>::BOXES;
+    using E = Fp8Epi<EPI, CG, MX>;
+    constexpr int STAGES = E::STAGES, BOXES = E::BOXES;
+    constexpr int CHUNKS = E::COLS / 32;  // a warp's columns, 32 at a time
     constexpr bool GRAD = EPI == ZB_FP8_GELU_GRAD;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t* staging = smem + STAGES * C::STAGE;
-    Fp8Ctl* ctl = reinterpret_cast<Fp8Ctl*>(staging + FP8_EPI_WARPS * BOXES * FP8_BOX);
+    Fp8Ctl* ctl = reinterpret_cast<Fp8Ctl*>(staging + E::WARPS * BOXES * FP8_BOX);
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = PAIR ? zbp::cluster_ctarank() : 0u;
@@ -227,7 +230,7 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
         }
         for (int b = 0; b < 2; ++b) {
             zbp::mbar_init(zbp::smem_u32(&ctl->tfull[b]), 1);
-            zbp::mbar_init(zbp::smem_u32(&ctl->tempty[b]), FP8_EPI_WARPS * CG);
+            zbp::mbar_init(zbp::smem_u32(&ctl->tempty[b]), E::WARPS * CG);
             zbp::mbar_init(zbp::smem_u32(&ctl->drain[b]), 1);
         }
         for (int g = 0; g < MX_SLOTS; ++g) {
@@ -235,7 +238,7 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
             zbp::mbar_init(zbp::smem_u32(&ctl->sempty[g]), 1);
         }
         if (GRAD)
-            for (int w = 0; w < FP8_EPI_WARPS; ++w) zbp::mbar_init(zbp::smem_u32(&ctl->hbar[w]), 1);
+            for (int w = 0; w < E::WARPS; ++w) zbp::mbar_init(zbp::smem_u32(&ctl->hbar[w]), 1);
         ctl->abort_flag = 0;
         zbp::fence_mbar_init();
         zbp::tma_prefetch_desc(&tmA128);
@@ -274,7 +277,7 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
     Walk<C::TILE_T, false> walk(ctl->off, args.experts, tiles_n);
     int row0 = 0, nrows = 0, nb = 0;
     if (warp < 4) {
-        zbp::regs_dec<FP8_REGS_LOW>();
+        zbp::regs_dec<E::REGS_LOW>();
         if (warp == 0) {
             // ------------------------------------------------ TMA producer
             const uint32_t full0 = zbp::smem_u32(&ctl->full[0]), empty0 = zbp::smem_u32(&ctl->empty[0]);
@@ -540,9 +543,9 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
         }
     } else {
         // ---------------------------------------------------- epilogue
-        zbp::regs_inc<FP8_REGS_HIGH>();
+        zbp::regs_inc<E::REGS_HIGH>();
         const int ew = warp - 4, q = warp & 3;
-        const int c_lo = (ew >> 2) * 128;  // this warp's half of the tile's columns: one block of 128
+        const int c_lo = (ew >> 2) * E::COLS;  // this warp's part of the tile's columns
         const uint32_t stg0 = zbp::smem_u32(staging + ew * BOXES * FP8_BOX);
         uint32_t it = 0, flip = 0;
         uint32_t asked = 0, taken = 0;  // tiles whose H was asked for and read
@@ -558,13 +561,13 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
                 if (lane == 0) {
                     zbp::bulk_wait_read<0>();
                     const uint32_t bar = zbp::smem_u32(&ctl->hbar[ew]);
-                    zbp::mbar_arrive_expect_tx(bar, 4 * FP8_BOX);  // columns past the edge: zeros
-                    for (int c = 0; c < 4; ++c)
+                    zbp::mbar_arrive_expect_tx(bar, BOXES * FP8_BOX);  // columns past the edge: zeros
+                    for (int c = 0; c < BOXES; ++c)
                         zbp::tma_load_2d(stg0 + static_cast<uint32_t>(c) * FP8_BOX, &tmO1, bar, n0 + 32 * c, first);
                 }
                 ++asked;
             }
-            f32x2 sum[64];
+            f32x2 sum[E::COLS / 2];
             if (MX) {
                 if (!wait_bar<false>(zbp::smem_u32(&ctl->tfull[0]), it & 1u, abort_flag, args.err, ERR_WAIT_EPI, WAIT_LIMIT_NS,
                                      true)) {
@@ -575,7 +578,7 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
                 zbp::tc_fence_after();
                 const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + c_lo;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < CHUNKS; ++c) {
                     uint32_t v[32];
                     zbp::tmem_ld_32x32b_x32(taddr + c * 32, v);
                     zbp::tmem_ld_wait();
@@ -597,7 +600,7 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
             const float* xs = args.xs + static_cast<long long>(scaled ? first + lane : 0) * num_kb;
             const float* ws = args.ws + (static_cast<long long>(walk.e) * n_blocks + (scaled ? n0 / BLK : 0)) * num_kb;
 #pragma unroll
-            for (int i = 0; i < 64; ++i) sum[i] = 0ull;
+            for (int i = 0; i < E::COLS / 2; ++i) sum[i] = 0ull;
             float xn = scaled ? __ldg(xs) : 0.0f, wn = scaled ? __ldg(ws) : 0.0f;
 #pragma unroll 1
             for (int kb = 0; kb < num_kb; ++kb, ++it) {
@@ -616,7 +619,7 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
                 const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * ACC_COLS + c_lo;
                 const f32x2 ff = pk2(f, f);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
+                for (int c = 0; c < 2 * CHUNKS; ++c) {
                     uint32_t v[16];
                     zbp::tmem_ld_32x32b_x16(taddr + c * 16, v);
                     zbp::tmem_ld_wait();
@@ -650,8 +653,11 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
                 const int col0 = n0 + c * 32;
                 if (live >= 32) {
                     const uint32_t stg = stg0 + (GRAD ? static_cast<uint32_t>(c) : flip) * FP8_BOX;
-                    flip ^= 1u;
-                    if (!GRAD) staging_acquire(lane);  // GeLU': a lane replaces its own row of H
+                    if (BOXES == 2) flip ^= 1u;
+                    if (!GRAD) {  // GeLU': a lane replaces its own row of H
+                        if (lane == 0) zbp::bulk_wait_read<BOXES - 1>();
+                        __syncwarp();
+                    }
                     stage_row64(stg, lane, w);
                     zbp::fence_proxy_async_smem();
                     __syncwarp();
@@ -668,7 +674,7 @@ __global__ void __launch_bounds__(FP8_THREADS, 1)
                 }
             };
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < CHUNKS; ++c) {
                 const int col0 = n0 + c * 32;
                 if (col0 >= args.N) continue;
                 float x[32];
@@ -748,12 +754,14 @@ zb_status launched(const char* who) {
 
 template <int EPI, int CG, int MX>
 zb_status launch_fp8(const CUtensorMap (&mp)[5], const Fp8Args& a, long long tiles, void* stream) {
+    using E = Fp8Epi<EPI, CG, MX>;
     auto kern = zb_fp8_matmul_kernel<EPI, CG, MX>;
     static std::atomic<int> cache[64];
     int ctas = 0;
-    zb_status s = full_grid(kern, cache, fp8_smem<EPI, CG>(), FP8_THREADS, CG, &ctas);
+    zb_status s = full_grid(kern, cache, fp8_smem<EPI, CG, MX>(), E::THREADS, CG, &ctas);
     if (s != ZB_OK) return s;
-    LaunchCfg lc(static_cast<int>(std::min<long long>(tiles * CG, ctas)), FP8_THREADS, fp8_smem<EPI, CG>(), CG, stream);
+    LaunchCfg lc(static_cast<int>(std::min<long long>(tiles * CG, ctas)), E::THREADS, fp8_smem<EPI, CG, MX>(),
+                 CG, stream);
     const cudaError_t e = cudaLaunchKernelEx(&lc.cfg, kern, mp[0], mp[1], mp[2], mp[3], mp[4], a);
     if (e != cudaSuccess) return zb::fail(ZB_ERR_CUDA, std::string("zb_fp8_matmul launch: ") + cudaGetErrorString(e));
     return launched("zb_fp8_matmul");
