@@ -37,12 +37,24 @@ __device__ __forceinline__ void expert_rows(const int* offsets, int e, int rows,
 // by stmatrix; H (for GeLU') comes the same way back, by TMA and ldmatrix.  A
 // box of 32 rows leaves by a TMA store; the last, partial box of an expert by
 // plain stores of its live rows, since the rows after it are another expert's.
-template <int CG>
+//
+// With a few rows an expert (SHAPE FEW) the weights are all that counts, and a
+// CTA's rate is that of its MMA thread: a wait, four small MMAs and a commit take
+// 370 cycles a K block, whatever the block's bytes, which the MMAs of larger
+// tiles hide.  So a stage there has four K blocks (and 32 rows, not 128), one
+// wait and one commit; and where tiles of 128 columns would leave half of the
+// SMs idle, they have 64.  The MMA has 128 columns all the same: the upper 64 of
+// a narrow tile are whatever lies behind its weights in the ring, and their
+// products are not read back.  16 rows, 8 experts, K 4096, N 1024: 17.3 us with
+// one block a stage, 13.8 with two, 12.1 with four (5.5 TB/s).
+enum Shape { FEW = 0, ONE = 1, PAIRS = 2 };
+template <int SHAPE>
 struct RowsCfg {
-    static constexpr int TILE_F = 128 * CG;   // columns of D per tile
-    static constexpr int TILE_T = 128 * CG;   // rows of D per tile, at most
-    static constexpr int N_STEP = 16 * CG;    // granularity of the MMA's N
-    static constexpr uint32_t STAGE = 32 * 1024;  // 16 KiB of weights, 16 KiB of rows
+    static constexpr int CG = SHAPE == PAIRS ? 2 : 1;
+    static constexpr int TILE_T = SHAPE == FEW ? 32 : 128 * CG;  // rows of D per tile, at most
+    static constexpr int N_STEP = 16 * CG;                       // granularity of the MMA's N
+    static constexpr int KPS = SHAPE == FEW ? 4 : 1;             // K blocks of a stage
+    static constexpr uint32_t STAGE = 32 * 1024;                 // 16 KiB of weights, 16 KiB of rows (not FEW)
     static constexpr uint32_t TMEM = 2 * TILE_T;
 };
 template <int EPI>
@@ -52,9 +64,10 @@ struct RowsEpi {
 };
 constexpr uint32_t ROW_BOX = 32 * 64;  // 32 rows x 32 columns of bf16
 constexpr int EPI_WARPS = 8;
+constexpr int MAX_STAGES = 16;
 
 struct RowsCtl {
-    uint64_t full[6], empty[6], tfull[2], tempty[2], drain;
+    uint64_t full[MAX_STAGES], empty[MAX_STAGES], tfull[2], tempty[2], drain;
     uint64_t hbar[EPI_WARPS][4];  // H boxes
     uint32_t tmem_base;
     int abort_flag;
@@ -63,7 +76,7 @@ struct RowsCtl {
 
 template <int EPI>
 constexpr size_t rows_smem() {
-    return 1024 + RowsEpi<EPI>::STAGES * RowsCfg<1>::STAGE + EPI_WARPS * RowsEpi<EPI>::BOXES * ROW_BOX + sizeof(RowsCtl);
+    return 1024 + RowsEpi<EPI>::STAGES * RowsCfg<ONE>::STAGE + EPI_WARPS * RowsEpi<EPI>::BOXES * ROW_BOX + sizeof(RowsCtl);
 }
 static_assert(rows_smem<zb::EPI_GELU_BWD>() <= 232448 && rows_smem<zb::EPI_GELU_DUAL>() <= 232448, "shared memory");
 
@@ -72,28 +85,35 @@ struct RowsArgs {
     const __nv_bfloat16* bias;  // [E, N] or nullptr
     __nv_bfloat16 *out0, *out1;
     int rows, experts, N, K, act;
+    int tile_f;  // columns of D per tile: 128, 64 (FEW) or 256 (PAIRS)
     unsigned int* err;
 };
 
-template <int EPI, int A_MN, int CG>
+template <int EPI, int A_MN, int SHAPE>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     zb_moe_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA128,
                        const __grid_constant__ CUtensorMap tmA32, const __grid_constant__ CUtensorMap tmO0,
                        const __grid_constant__ CUtensorMap tmO1, const RowsArgs args) {
-    using C = RowsCfg<CG>;
+    using C = RowsCfg<SHAPE>;
+    constexpr int CG = C::CG;
     constexpr bool PAIR = CG == 2;
-    constexpr int STAGES = RowsEpi<EPI>::STAGES;
     constexpr int BOXES = RowsEpi<EPI>::BOXES;
+    constexpr uint32_t RING = RowsEpi<EPI>::STAGES * C::STAGE;
+    const int tile_f = SHAPE == FEW ? args.tile_f : 128 * CG;
+    const uint32_t w_bytes = static_cast<uint32_t>(tile_f / CG) * BK * 2u;  // of a stage in one CTA; the rows follow
+    const uint32_t BLOCK = SHAPE == FEW ? w_bytes + 32u * BK * 2u : C::STAGE;  // a K block in the ring
+    const uint32_t STAGE = C::KPS * BLOCK;
+    const int STAGES = SHAPE == FEW ? min(MAX_STAGES, static_cast<int>(RING / STAGE)) : RowsEpi<EPI>::STAGES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint8_t* staging = smem + STAGES * C::STAGE;
+    uint8_t* staging = smem + RING;
     RowsCtl* ctl = reinterpret_cast<RowsCtl*>(staging + EPI_WARPS * BOXES * ROW_BOX);
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = PAIR ? zbp::cluster_ctarank() : 0u;
     const bool leader = rank == 0;
     const int cluster = blockIdx.x / CG, clusters = gridDim.x / CG;
-    const int tiles_f = (args.N + C::TILE_F - 1) / C::TILE_F;
+    const int tiles_f = (args.N + tile_f - 1) / tile_f;
     const int num_kb = (args.K + BK - 1) / BK;
 
     if (threadIdx.x == 0) {
@@ -146,46 +166,51 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         uint32_t s = 0, sp = 1, it = 0;  // stage and the phase of its last release; stages filled
         bool ok = true;
         for (int tile = cluster; ok && walk.to(tile, row0, nrows, fb); tile += clusters) {
-            const int f0 = fb * C::TILE_F + static_cast<int>(rank) * 128;
+            const int f0 = fb * tile_f + static_cast<int>(rank) * 128;
             const int mma_n = (nrows + C::N_STEP - 1) / C::N_STEP * C::N_STEP;
             const int half = mma_n / CG;  // rows in this CTA
             const int r0 = row0 + static_cast<int>(rank) * half;
             const int boxes = (half + 31) / 32;
-            const uint32_t bytes = CG * (A_BYTES + static_cast<uint32_t>(boxes) * 32u * BK * 2u);
-            for (int kb = 0; kb < num_kb; ++kb, ++it) {
+            const uint32_t bytes = CG * (w_bytes + static_cast<uint32_t>(boxes) * 32u * BK * 2u);
+            for (int kb = 0; kb < num_kb; kb += C::KPS, ++it) {
                 if (!wait_bar<false>(empty0 + s * 8u, sp, abort_flag, args.err, ERR_WAIT_PRODUCER, WAIT_LIMIT_NS, true)) {
                     ok = false;
                     break;
                 }
                 if (zbp::elect_one()) {
                     const uint32_t full = full0_lead + s * 8u;
-                    const uint32_t sa = sa0 + s * C::STAGE, sb = sa + A_BYTES;
-                    const int k0 = kb * BK;
-                    if (leader) zbp::mbar_arrive_expect_tx(full0 + s * 8u, bytes);
-                    auto load_w = [&](uint32_t dst, int x, int y) {
-                        if (PAIR)
-                            zbp::tma_load_3d_pair(dst, &tmW, full, x, y, walk.e);
-                        else
-                            zbp::tma_load_3d(dst, &tmW, full, x, y, walk.e);
-                    };
-                    auto load_a = [&](uint32_t dst, const CUtensorMap* tm, int y) {
-                        if (PAIR)
-                            zbp::tma_load_2d_pair(dst, tm, full, k0, y);
-                        else
-                            zbp::tma_load_2d(dst, tm, full, k0, y);
-                    };
-                    if (A_MN) {
-                        load_w(sa, f0, k0);
-                        load_w(sa + MN_ATOM_BYTES, f0 + 64, k0);
-                    } else {
-                        load_w(sa, k0, f0);
-                    }
-                    if (boxes == 4) {
-                        load_a(sb, &tmA128, r0);
-                    } else {
+                    const int blocks = min(C::KPS, num_kb - kb);
+                    if (leader) zbp::mbar_arrive_expect_tx(full0 + s * 8u, bytes * static_cast<uint32_t>(blocks));
 #pragma unroll
-                        for (int b = 0; b < 3; ++b)
-                            if (b < boxes) load_a(sb + static_cast<uint32_t>(b) * 32u * BK * 2u, &tmA32, r0 + 32 * b);
+                    for (int j = 0; j < C::KPS; ++j) {
+                        if (j >= blocks) break;
+                        const uint32_t sa = sa0 + s * STAGE + static_cast<uint32_t>(j) * BLOCK, sb = sa + w_bytes;
+                        const int k0 = (kb + j) * BK;
+                        auto load_w = [&](uint32_t dst, int x, int y) {
+                            if (PAIR)
+                                zbp::tma_load_3d_pair(dst, &tmW, full, x, y, walk.e);
+                            else
+                                zbp::tma_load_3d(dst, &tmW, full, x, y, walk.e);
+                        };
+                        auto load_a = [&](uint32_t dst, const CUtensorMap* tm, int y) {
+                            if (PAIR)
+                                zbp::tma_load_2d_pair(dst, tm, full, k0, y);
+                            else
+                                zbp::tma_load_2d(dst, tm, full, k0, y);
+                        };
+                        if (A_MN) {
+                            load_w(sa, f0, k0);
+                            if (tile_f > 64) load_w(sa + MN_ATOM_BYTES, f0 + 64, k0);
+                        } else {
+                            load_w(sa, k0, f0);
+                        }
+                        if (boxes == 4) {
+                            load_a(sb, &tmA128, r0);
+                        } else {
+#pragma unroll
+                            for (int b = 0; b < 3; ++b)
+                                if (b < boxes) load_a(sb + static_cast<uint32_t>(b) * 32u * BK * 2u, &tmA32, r0 + 32 * b);
+                        }
                     }
                 }
                 __syncwarp();
@@ -207,7 +232,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             // ------------------------------------------------ MMA issuer
             constexpr uint32_t A_STEP = A_MN ? 2048 >> 4 : 32 >> 4, hi = zbp::desc_hi(1024);
             const uint32_t a0 = zbp::desc_lo(zbp::smem_u32(smem), A_MN ? MN_ATOM_BYTES : 16);
-            const uint32_t b0 = zbp::desc_lo(zbp::smem_u32(smem) + A_BYTES, 16);
+            const uint32_t b0 = zbp::desc_lo(zbp::smem_u32(smem) + w_bytes, 16);
             const uint32_t full0 = zbp::smem_u32(&ctl->full[0]), empty0 = zbp::smem_u32(&ctl->empty[0]);
             uint32_t s = 0, sp = 0, local = 0;  // stage and its phase; tile
             bool ok = true;
@@ -219,22 +244,27 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 const uint32_t d_tmem = tmem_base + buf * C::TILE_T;
                 const uint32_t mma_n = static_cast<uint32_t>((nrows + C::N_STEP - 1) / C::N_STEP * C::N_STEP);
                 const uint32_t idesc = zbp::idesc_bf16_f32(128 * CG, mma_n, A_MN, 0);
-                for (int kb = 0; kb < num_kb; ++kb) {
+                for (int kb = 0; kb < num_kb; kb += C::KPS) {
                     if (!wait_bar<false>(full0 + s * 8u, sp, abort_flag, args.err, ERR_WAIT_MMA, WAIT_LIMIT_NS, true)) {
                         ok = false;
                         break;
                     }
                     zbp::tc_fence_after();
                     if (zbp::elect_one()) {
-                        const uint32_t off = s * (C::STAGE >> 4);
+                        const uint32_t off = s * (STAGE >> 4);
                         if (PAIR) {
                             zbp::mma4_f16_pair<A_STEP, 2>(d_tmem, a0 + off, hi, b0 + off, hi, idesc, kb != 0);
                             zbp::tc_commit_pair_multicast(empty0 + s * 8u, 0x3);
                             if (kb + 1 == num_kb) zbp::tc_commit_pair_multicast(zbp::smem_u32(&ctl->tfull[buf]), 0x3);
                         } else {
                             zbp::mma4_f16<A_STEP, 2>(d_tmem, a0 + off, hi, b0 + off, hi, idesc, kb != 0);
+#pragma unroll
+                            for (int j = 1; j < C::KPS; ++j) {
+                                const uint32_t o = off + static_cast<uint32_t>(j) * (BLOCK >> 4);
+                                if (kb + j < num_kb) zbp::mma4_f16<A_STEP, 2>(d_tmem, a0 + o, hi, b0 + o, hi, idesc, 1);
+                            }
                             zbp::tc_commit(empty0 + s * 8u);
-                            if (kb + 1 == num_kb) zbp::tc_commit(zbp::smem_u32(&ctl->tfull[buf]));
+                            if (kb + C::KPS >= num_kb) zbp::tc_commit(zbp::smem_u32(&ctl->tfull[buf]));
                         }
                     }
                     __syncwarp();
@@ -267,9 +297,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         bool ok = true;
         for (int tile = cluster; ok && walk.to(tile, row0, nrows, fb); tile += clusters, ++local) {
             const uint32_t buf = local & 1u, tr = local >> 1;
-            const int n0 = fb * C::TILE_F + static_cast<int>(rank) * 128 + q * 32;  // first column of D
+            const int n0 = fb * tile_f + static_cast<int>(rank) * 128 + q * 32;  // first column of D
             const int chunks = (nrows + MAX_TOK - 1) / MAX_TOK;
-            const bool cols_live = n0 < args.N;
+            const bool cols_live = n0 < args.N && (SHAPE != FEW || q * 32 < tile_f);
             const int mine = cols_live ? (chunks - hf + 1) / 2 : 0;  // chunks hf, hf + 2, ...
             auto ask_h = [&](int i) {  // chunk i of mine: H into box (g0 + i) % 4
                 if (lane == 0) {
@@ -866,9 +896,10 @@ zb_status launched(const char* who) {
     return ZB_OK;
 }
 
-template <int EPI, int A_MN, int CG>
+template <int EPI, int A_MN, int SHAPE>
 zb_status launch_rows(const CUtensorMap (&mp)[5], const RowsArgs& a, long long tiles, void* stream) {
-    auto kern = zb_moe_rows_kernel<EPI, A_MN, CG>;
+    constexpr int CG = RowsCfg<SHAPE>::CG;
+    auto kern = zb_moe_rows_kernel<EPI, A_MN, SHAPE>;
     static std::atomic<int> cache[64];
     int ctas = 0;
     zb_status s = full_grid(kern, cache, rows_smem<EPI>(), NUM_THREADS, CG, &ctas);
@@ -880,30 +911,43 @@ zb_status launch_rows(const CUtensorMap (&mp)[5], const RowsArgs& a, long long t
     return launched("grouped product");
 }
 
+template <int EPI, int A_MN>
+zb_status launch_rows_of(Shape shape, const CUtensorMap (&mp)[5], const RowsArgs& a, long long tiles, void* stream) {
+    if (shape == FEW) return launch_rows<EPI, A_MN, FEW>(mp, a, tiles, stream);
+    return shape == PAIRS ? launch_rows<EPI, A_MN, PAIRS>(mp, a, tiles, stream)
+                          : launch_rows<EPI, A_MN, ONE>(mp, a, tiles, stream);
+}
+
 // D[row, n] = sum_k A[row, k] W[e](k, n): W[e] is [K, N] or, transposed, [N, K].
 zb_status rows_product(const zb_moe& m, const int32_t* offsets, const void* A, const void* W, bool transposed,
                        int64_t N, int64_t K, const void* bias, const void* aux, int epi, void* out0, void* out1,
                        void* stream) {
-    // Pairs take tiles of 256 columns x up to 256 rows, single CTAs 128 x 128.
-    // A pair halves the weights' copies a row, so it is taken once its tiles
-    // fill the SMs; with few rows an expert the time is reading the weights, and
-    // twice as many tiles spread them more evenly (16 rows, 8 experts, h 1024,
-    // f 4096: 33.7 against 36.7 us; 3000 rows, 16 experts: 89 against 83).
+    // Pairs take tiles of 256 columns x up to 256 rows, single CTAs 128 x 128 or,
+    // with few rows an expert, 128 or 64 x 32.  A pair halves the weights' copies
+    // a row, so it is taken once its tiles fill the SMs; with fewer rows the time
+    // is reading the weights, and twice as many tiles spread them more evenly (3000
+    // rows, 16 experts, h 1024, f 4096: 89 us with pairs against 83).  The
+    // smallest tiles read an expert's weights again after 32 rows: from L2, but
+    // with 32 rows an expert, unevenly spread, already 2 us in 47 slower than
+    // tiles of 128; with 2 rows an expert they are 119 against 127 us (64
+    // experts, h 2048, f 1536), with 2 rows each of 8 experts 39 against 43.
     // The number of row tiles depends on counts that only the device knows;
     // this is their number when the rows are spread evenly over the experts.
     const int64_t used = std::min<int64_t>(m.experts, m.rows);
     const int64_t each = (m.rows + used - 1) / used;
     const long long pair_tiles = used * ((each + 255) / 256) * ((N + 255) / 256);
     const bool pair = each > 64 && pair_tiles >= sm_count() / 2;
+    const Shape shape = pair ? PAIRS : each <= 16 ? FEW : ONE;
+    const bool narrow = shape == FEW && used * ((N + 127) / 128) <= sm_count() / 2;
+    const int tt = pair ? 256 : shape == FEW ? 32 : 128, tf = pair ? 256 : narrow ? 64 : 128;
     // no launch has more tiles than this
-    const int tt = pair ? 256 : 128;
-    const long long most = (m.rows / tt + used) * ((N + tt - 1) / tt);
+    const long long most = (m.rows / tt + used) * ((N + tf - 1) / tf);
 
     constexpr CUtensorMapDataType BF16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     std::string why;
     CUtensorMap mp[5];
     const uint64_t rows = static_cast<uint64_t>(m.rows);
-    bool ok = transposed ? make_map3(&mp[0], W, BF16, 2, K, N, m.experts, BK, 128, &why)
+    bool ok = transposed ? make_map3(&mp[0], W, BF16, 2, K, N, m.experts, BK, std::min(tf, 128), &why)
                          : make_map3(&mp[0], W, BF16, 2, N, K, m.experts, 64, BK, &why);
     ok = ok && make_map(&mp[1], A, false, K, rows, K, BK, 128, &why);
     ok = ok && make_map(&mp[2], A, false, K, rows, K, BK, 32, &why);
@@ -923,18 +967,12 @@ zb_status rows_product(const zb_moe& m, const int32_t* offsets, const void* A, c
     a.N = static_cast<int>(N);
     a.K = static_cast<int>(K);
     a.act = m.act;
+    a.tile_f = tf;
     a.err = err;
-    if (epi == zb::EPI_GELU_DUAL)
-        return pair ? launch_rows<zb::EPI_GELU_DUAL, 1, 2>(mp, a, most, stream)
-                    : launch_rows<zb::EPI_GELU_DUAL, 1, 1>(mp, a, most, stream);
-    if (epi == zb::EPI_GELU_BWD)
-        return pair ? launch_rows<zb::EPI_GELU_BWD, 0, 2>(mp, a, most, stream)
-                    : launch_rows<zb::EPI_GELU_BWD, 0, 1>(mp, a, most, stream);
-    if (transposed)
-        return pair ? launch_rows<zb::EPI_STORE_BF16, 0, 2>(mp, a, most, stream)
-                    : launch_rows<zb::EPI_STORE_BF16, 0, 1>(mp, a, most, stream);
-    return pair ? launch_rows<zb::EPI_STORE_BF16, 1, 2>(mp, a, most, stream)
-                : launch_rows<zb::EPI_STORE_BF16, 1, 1>(mp, a, most, stream);
+    if (epi == zb::EPI_GELU_DUAL) return launch_rows_of<zb::EPI_GELU_DUAL, 1>(shape, mp, a, most, stream);
+    if (epi == zb::EPI_GELU_BWD) return launch_rows_of<zb::EPI_GELU_BWD, 0>(shape, mp, a, most, stream);
+    if (transposed) return launch_rows_of<zb::EPI_STORE_BF16, 0>(shape, mp, a, most, stream);
+    return launch_rows_of<zb::EPI_STORE_BF16, 1>(shape, mp, a, most, stream);
 }
 
 struct WProduct {
