@@ -179,6 +179,13 @@ CASES = [
     ([290, 1, 257, 0, 40, 513, 96, 33] * 2, 1288, 136, "tanh", False, 0),
     ([200, 90], 320, 136, "none", True, 1),
     ([3, 0, 70], 40, 72, "none", False, 0),
+    # few rows an expert on average: tiles of 32 rows, 64 and 128 columns wide; some experts have more
+    ([100, 1, 0, 2, 1, 1, 1, 33], 264, 1032, "erf", True, 3),
+    ([7, 1, 0, 2, 33, 1, 1, 1], 136, 1288, "tanh", True, 0),
+    ([1], 1352, 72, "none", True, 0),
+    # long experts: bias gradients summed in parts
+    ([1100, 3, 0, 2500], 72, 136, "erf", True, 1),
+    ([5001], 8, 72, "none", True, 0),
 ]
 
 
