@@ -39,8 +39,10 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 }
 
 // HBM-bound: 3 bytes a value.  16 lanes share a 1 x 128 block (16 bytes each,
-// read once and kept), a warp two neighbouring blocks of Q_ILP row groups, all
-// loads in flight before the first is used.
+// read once and kept), a warp Q_ILP pairs of neighbouring blocks, all loads in
+// flight before the first is used (two or eight pairs: the same within 3 %, but
+// 8190 x 1040 takes 10.5 us with eight, 8.4 with four).  16384 x 8192: 70 us, 5.8
+// TB/s; 4096 x 4096: 10.7 us.
 constexpr int Q_ILP = 4;
 __global__ void __launch_bounds__(256)
     zb_fp8_quantize_rows_kernel(const uint4* __restrict__ X, uint2* __restrict__ Q, float* __restrict__ S,
@@ -50,12 +52,19 @@ __global__ void __launch_bounds__(256)
     const long long item0 = (static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * 2 * Q_ILP + half;
     uint4 v[Q_ILP];
     long long at[Q_ILP], item[Q_ILP];
+    const bool whole = cols8 == blocks * 16;  // no partial blocks: a block's place needs no division
 #pragma unroll
     for (int u = 0; u < Q_ILP; ++u) {
         item[u] = item0 + 2 * u;
-        const long long r = item[u] / blocks;
-        const int c = static_cast<int>(item[u] - r * blocks) * 16 + l;
-        at[u] = item[u] < total && c < cols8 ? r * cols8 + c : -1;
+        at[u] = item[u] * 16 + l;
+        if (!whole) {
+            const long long r = total <= 0xffffffffll
+                                    ? static_cast<uint32_t>(item[u]) / static_cast<uint32_t>(blocks)
+                                    : item[u] / blocks;
+            const int c = static_cast<int>(item[u] - r * blocks) * 16 + l;
+            at[u] = c < cols8 ? r * cols8 + c : -1;
+        }
+        if (item[u] >= total) at[u] = -1;
         v[u] = at[u] >= 0 ? __ldg(X + at[u]) : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
@@ -157,18 +166,27 @@ __global__ void __launch_bounds__(256)
 
 // ---------------------------------------------------------------- product
 // D[r, n] = sum_b xs[r, b] ws[n/128, b] P_b[r, n], P_b the product over the
-// b-th block of 128 of K.  The scales change from block to block, so a tensor
-// core accumulator holds one P_b only (4 MMAs of K = 32), and the epilogue
-// warps add xs ws P_b to fp32 sums in registers while the next is computed.
-// TMEM holds two blocks' results.  They are handed over as four accumulators of
-// 128 columns rather than two of 256: the way round (commit, wake, read,
-// arrive, wake: over 1000 cycles on a pair) then has to fit in three quarters
-// of two blocks' MMA time instead of half.  A tile's M side is rows, so
-// that a thread (one TMEM lane) has one row: its factor xs ws is one scalar for
-// its 128 columns, one packed FMA per two elements.  The tensor core needs 512
-// cycles for a block of a 128 x 256 tile, the FMAs of 8 warps 128 a scheduler,
-// the TMEM reads 256.
+// b-th block of 128 of K (4 MMAs of K = 32).  A tile's M side is rows, so that a
+// thread of the epilogue (one TMEM lane) has one row.  Warp 0 copies; the scales
+// are applied in one of two ways:
 //
+// Powers of two (MX; what the quantisers make).  The tensor core's block-scaled
+// form multiplies by 2^(xs exponent + ws exponent) itself: a factor for each row
+// and 32 of K, here the same for a block's four.  Warp 1 issues the MMAs over the
+// whole of K into one accumulator of 256 columns, warps 2 and 3 feed it the
+// exponents.  The epilogue takes the accumulator into registers at once and
+// gives it back, so that the next tile's MMAs run beside the rest of it.  Bound
+// by the MMAs where K is long: [4096, 4096] x [4096, 16384] 155 us, 3.55 PFLOP/s
+// (the tensor pipe active 83 % of the time); with K 1040 and GeLU' by the epilogue
+// and the number of tiles a CTA pair (16 experts, 8190 rows, N 4104: 79 us).
+//
+// Any other scales.  The accumulator holds one P_b only, and the 8 epilogue
+// warps add xs ws P_b to fp32 sums in registers (a packed FMA for two elements)
+// while the next is computed: two accumulators of 256 columns fill TMEM.  A
+// block's MMAs take 512 cycles, but the way round an accumulator (commit, wake,
+// read, arrive, wake) over 1000 on a pair, which bounds it: [4096, 4096] x
+// [4096, 16384] 217 us.  Warps 1 and 2 issue a block each in turn, since a block's
+// waits, MMAs and commits take one thread longer than 512 cycles.
 template <int CG>
 struct Fp8Cfg {
     static constexpr int TILE_T = 128 * CG;                       // rows of D per tile
@@ -177,7 +195,10 @@ struct Fp8Cfg {
     static constexpr uint32_t STAGE = A_BYTES8 + B_ROWS * 128;
 };
 // Warps 0-3 give registers to the epilogue warps behind them.  MX: 16 of these,
-// with 64 columns each; else 8, whose threads hold 128 sums and 32 loaded values.
+// with 64 columns each, four to a scheduler to hide the latency of GeLU's special
+// functions, of H and of the stores (with 8: GeLU' of 16 experts, 8190 rows, K
+// 1040, N 4104 92 us against 79); else 8, whose threads hold 128 sums and 32
+// loaded values.
 // GeLU' keeps a warp's values of H in its staging boxes (copied while the product
 // runs) and stores from them; the others store through one box, or two.
 constexpr uint32_t FP8_BOX = 32 * 64;  // 32 rows x 32 columns of bf16

@@ -74,6 +74,7 @@ def _route(zb, z, k, renorm, dtype):
 
 @pytest.mark.parametrize("T,E,k,renorm,dtype", [
     (1, 1, 1, False, torch.float32), (1, 8, 2, True, torch.float32), (5, 33, 3, False, torch.bfloat16),
+    (17, 64, 6, True, torch.float32), (32, 256, 32, False, torch.bfloat16), (33, 256, 8, True, torch.float32),
     (127, 64, 6, True, torch.float32), (128, 256, 8, False, torch.float32), (129, 60, 4, True, torch.bfloat16),
     (300, 65, 32, False, torch.float32), (1000, 129, 8, True, torch.float32), (4867, 16, 2, False, torch.bfloat16),
     (20011, 40, 2, True, torch.float32)])
