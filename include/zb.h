@@ -673,8 +673,9 @@ zb_status zb_moe_backward_weight(const zb_moe* m, const int32_t* offsets, const 
  * for each 128 x 128 block of W: x = scale * q.  The quantisers take as scale
  * the least power of two s with amax / s <= 448 (at least 2^-126; 1 for a
  * block of zeros), so that x / s is exact and the only rounding is e4m3's own
- * (to nearest, ties to even).  A block with a NaN or an infinity gets the scale NaN, so that what it touches is NaN.  A
- * last block may be narrower than 128. */
+ * (to nearest, ties to even).  A block with a NaN or an infinity gets the
+ * scale NaN, so that what it touches is NaN.  A last block may be narrower
+ * than 128. */
 
 /* X[rows,cols] bf16 -> Q[rows,cols] e4m3 and S[rows, ceil(cols/128)].  cols is
  * a multiple of 16. */
