@@ -478,12 +478,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 // ---------------------------------------------------------------- W
 // dW[e][m][n] (+)= sum over the rows r of e of A[r][m] B[r][n], both of the
 // pass's products in one launch.  The contraction runs over an expert's rows,
-// so its last block of 64 must not see the next expert's: each expert has
-// tensor maps of its own rows (their start and number set on the device by
-// zb_moe_maps_kernel), and the copies past the last row fill in zeros.  Only a
-// partial last block goes through them; whole blocks use maps of all rows from
-// the launch parameters, whose descriptors need no fetch from memory per
-// expert.  Both operands are read as they lie (MN-major).
+// so its last block of 64 must not see the next expert's: once a partial block
+// has landed, warps 2 and 3 overwrite the rows past the expert's end with zeros
+// in both operands (an infinity or NaN there would not vanish times zero).  Its
+// copies complete on a barrier of their own CTA (part), and the two warps of
+// each CTA arrive on the MMA's (edge).  Both operands are read as they lie
+// (MN-major: a row of 64 values is a line of 128 bytes, whatever the swizzle).
 //
 // The tensor core cuts off low bits as it accumulates, so the error of one
 // long accumulator grows with its length (1.4e-6 of the result after ~1024
@@ -503,8 +503,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 // 1500, 401 at 2000.
 constexpr int W_SEG = 8;  // blocks of 64 rows
 constexpr int W_PACE = 250, W_PACE_MOST = 2200;
-// Warp 0 copies, warp 1 issues MMAs; warps 4-11 sum and store, with the
-// registers that warps 0-3 give up (128 sums a thread).
+// Warp 0 copies, warp 1 issues MMAs, warps 2 and 3 clear rows; warps 4-11 sum
+// and store, with the registers that warps 0-3 give up (128 sums a thread).
 constexpr int W_THREADS = 384;
 constexpr int W_REGS_LOW = 40, W_REGS_HIGH = 232;
 static_assert(128 * W_REGS_LOW + 256 * W_REGS_HIGH <= W_THREADS * 168, "register split");
@@ -514,42 +514,8 @@ template <int CG>
 struct WCfg {
     static constexpr int STAGES = CG == 1 ? 3 : 5;
 };
-struct MapsArgs {
-    const int* offsets;
-    int rows, experts, width[4];
-    const __nv_bfloat16* base[4];
-    CUtensorMap* out;  // [experts][4]
-};
-__global__ void __launch_bounds__(128)
-    zb_moe_maps_kernel(const __grid_constant__ CUtensorMap t0, const __grid_constant__ CUtensorMap t1,
-                       const __grid_constant__ CUtensorMap t2, const __grid_constant__ CUtensorMap t3,
-                       const MapsArgs a) {
-    const int i = blockIdx.x * blockDim.x + threadIdx.x;
-    zbp::grid_dependency_wait();
-    zbp::allow_dependent_launch();
-    if (i >= 4 * a.experts) return;
-    const int e = i >> 2, k = i & 3;
-    const CUtensorMap* t = k == 0 ? &t0 : k == 1 ? &t1 : k == 2 ? &t2 : &t3;
-    if (a.base[k] == nullptr) return;
-    // the rows of e as load_offsets() makes them legal
-    int lo = 0, hi = 0;
-    for (int x = 0; x <= e + 1; ++x) {
-        const int o = max(hi, min(max(a.offsets[x], 0), a.rows));
-        lo = hi;
-        hi = o;
-    }
-    uint4* dst = reinterpret_cast<uint4*>(a.out + i);
-    const uint4* src = reinterpret_cast<const uint4*>(t);
-#pragma unroll
-    for (int w = 0; w < 8; ++w) dst[w] = src[w];
-    // a map has at least one row; an expert without rows does not use its maps
-    zbp::tensormap_set(dst, a.base[k] + static_cast<long long>(lo) * a.width[k],
-                       static_cast<uint32_t>(max(hi - lo, 1)));
-}
-
 struct WArgs {
     const int* offsets;
-    const CUtensorMap* maps;  // [experts][4]: A and B of product 0, of product 1
     int rows, experts, products;
     int M[2], N[2];
     int accumulate;
@@ -557,7 +523,7 @@ struct WArgs {
 };
 template <int CG>
 struct WCtl {
-    uint64_t full[6], empty[6], tfull[2], tempty[2], drain;
+    uint64_t full[6], empty[6], part[6], edge[6], tfull[2], tempty[2], drain;
     uint32_t tmem_base;
     int abort_flag;
     int off[MAX_EXPERTS + 1];
@@ -608,6 +574,8 @@ __global__ void __launch_bounds__(W_THREADS, 1)
         for (int s = 0; s < STAGES; ++s) {
             zbp::mbar_init(zbp::smem_u32(&ctl->full[s]), 1);
             zbp::mbar_init(zbp::smem_u32(&ctl->empty[s]), 1);
+            zbp::mbar_init(zbp::smem_u32(&ctl->part[s]), 1);
+            zbp::mbar_init(zbp::smem_u32(&ctl->edge[s]), 2 * CG);
         }
         for (int b = 0; b < 2; ++b) {
             zbp::mbar_init(zbp::smem_u32(&ctl->tfull[b]), 1);
@@ -652,7 +620,9 @@ __global__ void __launch_bounds__(W_THREADS, 1)
             const uint32_t full0 = zbp::smem_u32(&ctl->full[0]), empty0 = zbp::smem_u32(&ctl->empty[0]);
             const uint32_t full0_lead = PAIR ? zbp::mapa_shared(full0, 0) : full0;
             const uint32_t sa0 = zbp::smem_u32(smem);
+            const uint32_t part0 = zbp::smem_u32(&ctl->part[0]);
             uint32_t s = 0, sp = 1, it = 0;  // stage and the phase of its last release; stages filled
+            uint32_t pending = 0, pp = 0;    // a bit a stage: last filled with a partial block; phase of part
             bool ok = true;
             for (int tile = cluster; tile < num_tiles && ok; tile += clusters) {
                 int e, mb, nb;
@@ -660,14 +630,6 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                 const int num_kb = blocks_of(e);
                 if (num_kb == 0) continue;
                 const int first = ctl->off[e], n = ctl->off[e + 1] - first;
-                const CUtensorMap* tail = args.maps + 4 * e + 2 * p;  // A's, then B's
-                if (n % BK && zbp::elect_one()) {
-                    zbp::fence_tensormap_acquire(tail);
-                    zbp::fence_tensormap_acquire(tail + 1);
-                    zbp::tma_prefetch_desc(tail);
-                    zbp::tma_prefetch_desc(tail + 1);
-                }
-                __syncwarp();
                 const int m0 = mb * C::TILE_M + static_cast<int>(rank) * BM;
                 const int nb0 = nb * BN + static_cast<int>(rank) * C::B_ROWS;
                 for (int kb = 0; kb < num_kb; ++kb, ++it) {
@@ -676,19 +638,27 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                         ok = false;
                         break;
                     }
+                    const bool partial = kb * BK + BK > n;
+                    // a stage is filled again after its partial block was used
+                    if ((pending >> s) & 1u) pp ^= 1u << s;
+                    pending = (pending & ~(1u << s)) | (partial ? 1u << s : 0u);
                     if (zbp::elect_one()) {
-                        const uint32_t full = full0_lead + s * 8u;
                         const uint32_t sa = sa0 + s * C::STAGE_BYTES, sb = sa + A_BYTES;
-                        if (leader) zbp::mbar_arrive_expect_tx(full0 + s * 8u, C::STAGE_BYTES * CG);
-                        const bool whole = kb * BK + BK <= n;
-                        const CUtensorMap* tma = whole ? (p ? &tmA1 : &tmA0) : tail;
-                        const CUtensorMap* tmb = whole ? (p ? &tmB1 : &tmB0) : tail + 1;
-                        const int y = whole ? first + kb * BK : kb * BK;
+                        const uint32_t bar = partial ? part0 + s * 8u : full0_lead + s * 8u;
+                        if (partial) {
+                            zbp::mbar_arrive_expect_tx(bar, C::STAGE_BYTES);
+                            if (leader) zbp::mbar_arrive(full0 + s * 8u);
+                        } else if (leader) {
+                            zbp::mbar_arrive_expect_tx(full0 + s * 8u, C::STAGE_BYTES * CG);
+                        }
+                        const CUtensorMap* tma = p ? &tmA1 : &tmA0;
+                        const CUtensorMap* tmb = p ? &tmB1 : &tmB0;
+                        const int y = first + kb * BK;
                         auto load = [&](uint32_t dst, const CUtensorMap* tm, int x) {
-                            if (PAIR)
-                                zbp::tma_load_2d_pair(dst, tm, full, x, y);
+                            if (PAIR && !partial)
+                                zbp::tma_load_2d_pair(dst, tm, bar, x, y);
                             else
-                                zbp::tma_load_2d(dst, tm, full, x, y);
+                                zbp::tma_load_2d(dst, tm, bar, x, y);
                         };
                         load(sa, tma, m0);
                         load(sa + MN_ATOM_BYTES, tma, m0 + 64);
@@ -702,25 +672,63 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                     }
                 }
             }
-            if (!ok && leader) {
+            if (!ok) {
                 // wait for the copies that were issued but may not have landed
                 const uint32_t first = it > STAGES ? it - STAGES : 0;
-                for (uint32_t i = first; i < it; ++i)
-                    wait_bar<false>(zbp::smem_u32(&ctl->full[i % STAGES]), (i / STAGES) & 1u, abort_flag, args.err,
-                                    ERR_WAIT_PRODUCER, DRAIN_LIMIT_NS, false);
+                for (uint32_t i = first; i < it; ++i) {
+                    const uint32_t st = i % STAGES;
+                    if ((pending >> st) & 1u)
+                        wait_bar<false>(part0 + st * 8u, (pp >> st) & 1u, abort_flag, args.err, ERR_WAIT_PRODUCER,
+                                        DRAIN_LIMIT_NS, false);
+                    else if (leader)
+                        wait_bar<false>(full0 + st * 8u, (i / STAGES) & 1u, abort_flag, args.err, ERR_WAIT_PRODUCER,
+                                        DRAIN_LIMIT_NS, false);
+                }
             }
-        } else if (warp == 1 && leader) {
+        } else if (warp >= 2) {
+            // ------------------------------------------------ rows past an expert's end
+            uint32_t it = 0, pp = 0;  // blocks so far; phase of each stage's part
+            bool ok = true;
+            for (int tile = cluster; tile < num_tiles && ok; tile += clusters) {
+                const int e = tile / per, num_kb = blocks_of(e);
+                it += static_cast<uint32_t>(num_kb);
+                const int live = (ctl->off[e + 1] - ctl->off[e]) % BK;
+                if (live == 0) continue;
+                const uint32_t s = (it - 1) % STAGES;
+                if (!wait_bar<false>(zbp::smem_u32(&ctl->part[s]), (pp >> s) & 1u, abort_flag, args.err,
+                                     ERR_WAIT_PRODUCER, WAIT_LIMIT_NS, true)) {
+                    ok = false;
+                    break;
+                }
+                pp ^= 1u << s;
+                uint8_t* at = smem + s * C::STAGE_BYTES + (lane & 7) * 16;
+                for (int r = live + (warp - 2) * 4 + lane / 8; r < BK; r += 8)
+#pragma unroll
+                    for (int atom = 0; atom < static_cast<int>(C::STAGE_BYTES / MN_ATOM_BYTES); ++atom)
+                        *reinterpret_cast<uint4*>(at + atom * MN_ATOM_BYTES + r * 128) = make_uint4(0, 0, 0, 0);
+                zbp::fence_proxy_async_smem();  // the tensor core reads the zeros
+                __syncwarp();
+                if (lane == 0) {
+                    const uint32_t bar = zbp::smem_u32(&ctl->edge[s]);
+                    if (PAIR)
+                        zbp::mbar_arrive_cluster(zbp::mapa_shared(bar, 0));
+                    else
+                        zbp::mbar_arrive(bar);
+                }
+            }
+        } else if (leader) {
             // ------------------------------------------------ MMA issuer
             constexpr uint32_t idesc = zbp::idesc_bf16_f32(BM * CG, BN, 1, 1);
             constexpr uint32_t hi = zbp::desc_hi(1024);
             const uint32_t a0 = zbp::desc_lo(zbp::smem_u32(smem), MN_ATOM_BYTES);
             const uint32_t full0 = zbp::smem_u32(&ctl->full[0]), empty0 = zbp::smem_u32(&ctl->empty[0]);
             uint32_t s = 0, sp = 0, local = 0;  // stage and its phase; segment
+            uint32_t ep = 0;                    // phase of each stage's edge
             bool ok = true;
             for (int tile = cluster; tile < num_tiles && ok; tile += clusters) {
                 int e, mb, nb;
                 locate(tile, e, mb, nb);
-                const int num_kb = blocks_of(e);
+                const int num_kb = blocks_of(e), n = ctl->off[e + 1] - ctl->off[e];
                 for (int kb0 = 0; kb0 < num_kb && ok; kb0 += W_SEG) {
                     const uint32_t buf = local & 1u, tr = local >> 1;
                     ++local;
@@ -735,6 +743,14 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                         if (!wait_bar<false>(full0 + s * 8u, sp, abort_flag, args.err, ERR_WAIT_MMA, WAIT_LIMIT_NS, true)) {
                             ok = false;
                             break;
+                        }
+                        if (kb * BK + BK > n) {
+                            if (!wait_bar<true>(zbp::smem_u32(&ctl->edge[s]), (ep >> s) & 1u, abort_flag, args.err,
+                                                ERR_WAIT_MMA, WAIT_LIMIT_NS, true)) {
+                                ok = false;
+                                break;
+                            }
+                            ep ^= 1u << s;
                         }
                         zbp::tc_fence_after();
                         if (zbp::elect_one()) {
@@ -1039,21 +1055,17 @@ zb_status launch_wgrad(const CUtensorMap (&mi)[4], const CUtensorMap (&mo)[2], c
 }
 
 zb_status wgrad(const zb_moe& m, const int32_t* offsets, const WProduct* p, int products, int accumulate,
-                void* workspace, void* stream) {
+                void* stream) {
     std::string why;
     CUtensorMap mi[4], mo[2];
-    MapsArgs ma;
     WArgs a;
     const uint64_t rows = static_cast<uint64_t>(std::max<int64_t>(m.rows, 1));
     bool ok = true;
     long long tiles2 = 0, tiles1 = 0;
     for (int i = 0; i < 2; ++i) {
         const WProduct& w = p[i < products ? i : 0];
-        // without rows there is nothing to read and no map of it
-        ma.base[2 * i] = i < products && m.rows ? static_cast<const __nv_bfloat16*>(w.A) : nullptr;
-        ma.base[2 * i + 1] = i < products && m.rows ? static_cast<const __nv_bfloat16*>(w.B) : nullptr;
-        ma.width[2 * i] = a.M[i] = static_cast<int>(w.M);
-        ma.width[2 * i + 1] = a.N[i] = static_cast<int>(w.N);
+        a.M[i] = static_cast<int>(w.M);
+        a.N[i] = static_cast<int>(w.N);
         ok = ok && make_map3(&mo[i], w.dW, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, w.N, w.M, m.experts, 32, 32, &why);
         if (m.rows) {
             ok = ok && make_map(&mi[2 * i], w.A, false, w.M, rows, w.M, 64, BK, &why);
@@ -1069,19 +1081,8 @@ zb_status wgrad(const zb_moe& m, const int32_t* offsets, const WProduct* p, int 
     if (!ok) return zb::fail(ZB_ERR_CUDA, why);
     unsigned int* err = zb::device_error_word();
     if (!err) return ZB_ERR_CUDA;
-    ma.offsets = offsets;
-    ma.rows = static_cast<int>(m.rows);
-    ma.experts = m.experts;
-    ma.out = static_cast<CUtensorMap*>(workspace);
-    {
-        LaunchCfg lc((4 * m.experts + 127) / 128, 128, 0, 1, stream);
-        const cudaError_t e = cudaLaunchKernelEx(&lc.cfg, zb_moe_maps_kernel, mi[0], mi[1], mi[2], mi[3], ma);
-        if (e != cudaSuccess)
-            return zb::fail(ZB_ERR_CUDA, std::string("grouped weight gradient launch: ") + cudaGetErrorString(e));
-    }
     a.offsets = offsets;
-    a.maps = ma.out;
-    a.rows = ma.rows;
+    a.rows = static_cast<int>(m.rows);
     a.experts = m.experts;
     a.products = products;
     a.accumulate = accumulate;
@@ -1173,7 +1174,7 @@ extern "C" zb_status zb_moe_backward_input(const zb_moe* m, const int32_t* offse
 
 extern "C" size_t zb_moe_workspace_bytes(const zb_moe* m) {
     if (check_moe(m) != ZB_OK) return 0;
-    return static_cast<size_t>(m->experts) * 4 * 128;
+    return static_cast<size_t>(m->experts) * 4 * 128;  // part of the interface; the kernels keep nothing in it
 }
 
 extern "C" zb_status zb_moe_backward_weight(const zb_moe* m, const int32_t* offsets, const void* X, const void* A_save,
@@ -1202,10 +1203,10 @@ extern "C" zb_status zb_moe_backward_weight(const zb_moe* m, const int32_t* offs
     };
     if (mlp) {
         const WProduct p[2] = {{A_save, dY, dW2, f, h}, {X, dH, dW1, h, f}};
-        s = wgrad(*m, offsets, p, 2, accumulate ? 1 : 0, workspace, stream);
+        s = wgrad(*m, offsets, p, 2, accumulate ? 1 : 0, stream);
     } else {
         const WProduct p[1] = {{X, dY, dW1, h, f}};
-        s = wgrad(*m, offsets, p, 1, accumulate ? 1 : 0, workspace, stream);
+        s = wgrad(*m, offsets, p, 1, accumulate ? 1 : 0, stream);
     }
     if (s == ZB_OK && m->has_bias) s = colsum(mlp ? dH : dY, db1, f);
     if (s == ZB_OK && m->has_bias && mlp) s = colsum(dY, db2, h);

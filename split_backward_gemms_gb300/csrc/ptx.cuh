@@ -439,15 +439,6 @@ __device__ __forceinline__ void tma_reduce_add_3d(const void* tmap, uint32_t src
         : "memory");
 }
 
-// Set the base address and the extent of dimension 1 of the tensor map at
-// `tmap` (global memory).
-__device__ __forceinline__ void tensormap_set(void* tmap, const void* base, uint32_t dim1) {
-    asm volatile("tensormap.replace.tile.global_address.global.b1024.b64 [%0], %1;"
-                 ::"l"(reinterpret_cast<uint64_t>(tmap)), "l"(reinterpret_cast<uint64_t>(base)) : "memory");
-    asm volatile("tensormap.replace.tile.global_dim.global.b1024.b32 [%0], 1, %1;"
-                 ::"l"(reinterpret_cast<uint64_t>(tmap)), "r"(dim1) : "memory");
-}
-
 // Arrive on an mbarrier of another CTA of the cluster where the phase hands
 // over tensor memory only (its loads have completed: tcgen05.wait, then
 // tcgen05.fence::before_thread_sync): no generic memory is released at cluster

@@ -187,6 +187,9 @@ CASES = [
     # long experts: bias gradients summed in parts
     ([1100, 3, 0, 2500], 72, 136, "erf", True, 1),
     ([5001], 8, 72, "none", True, 0),
+    # many experts, nearly all with a partial last block, narrow matrices on CTA pairs
+    ([148, 286, 0, 138, 60, 165, 78, 12, 81, 57, 307, 23, 277, 37, 14, 472] * 4, 48, 48, "erf", False, 2),
+    ([17, 3, 7, 0, 30, 0, 6, 15, 2, 64, 5, 1, 128] * 10, 264, 136, "tanh", True, 0),
 ]
 
 
