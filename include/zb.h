@@ -652,7 +652,8 @@ typedef struct zb_moe {
  * zb_backward_weight with one weight per expert.  An expert without rows is
  * not read in F and B; in W it gets zeros (accumulate = 0) or keeps what it
  * has (accumulate = 1).  W needs zb_moe_workspace_bytes of device memory,
- * 256-byte aligned, until its work on the stream has ended.  The sums over an
+ * 256-byte aligned, until its work on the stream has ended (reserved: the present
+ * kernels keep nothing in it).  The sums over an
  * expert's rows have a fixed order: the same inputs give the same bits. */
 zb_status zb_moe_forward(const zb_moe* m, const int32_t* offsets, const void* X, const void* W1,
                          const void* W2, const void* b1, const void* b2, void* H_save, void* A_save,

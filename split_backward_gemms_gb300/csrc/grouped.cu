@@ -500,7 +500,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 // the time in which the MMAs fill the two accumulators anew.  W of 16384 rows,
 // 16 experts, h 1024, f 4096: 235 us unpaced, 219 at 1500 cycles, 212 at 2000
 // to 2500, 230 at 3500; of 24570 rows, 64 experts (6 blocks each): 394, 374 at
-// 1500, 401 at 2000.
+// 1500, 401 at 2000.  (Measured before the clearing of partial blocks, with which
+// the first is 232 from a cold L2, 11 us more.)
 constexpr int W_SEG = 8;  // blocks of 64 rows
 constexpr int W_PACE = 250, W_PACE_MOST = 2200;
 // Warp 0 copies, warp 1 issues MMAs, warps 2 and 3 clear rows; warps 4-11 sum
