@@ -215,11 +215,15 @@ def _ptr(x):
 
 def _current_stream():
     """The current torch stream's handle when torch's CUDA is initialised, else None."""
-    torch = sys.modules.get("torch")
-    if torch is None or not torch.cuda.is_initialized():
+    cuda = getattr(sys.modules.get("torch"), "cuda", None)
+    if cuda is None or not cuda.is_initialized():
         return None
-    # the raw handle: small kernels take less time than making a Stream object
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) or None
+    try:
+        # the raw handle: small kernels take less time than making a Stream object
+        c = sys.modules["torch"]._C
+        return c._cuda_getCurrentRawStream(c._cuda_getDevice()) or None
+    except AttributeError:  # private names, which a torch need not have
+        return cuda.current_stream().cuda_stream or None
 
 
 def _stream(s):
