@@ -365,15 +365,21 @@ __global__ void __launch_bounds__(256)
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
-        if (top == -INFINITY) top = 0.0f;  // a row with nothing left: every weight is 0
+        unsigned live = 0u;  // a bit an element: not -inf
 #pragma unroll
         for (int v = 0; v < VPL; ++v) {
+            live |= (z[v] != -INFINITY ? 1u : 0u) << v;
             z[v] = expf(z[v] - top);
             total += z[v];
         }
         total = warp_sum(total);
+        // Logits of -inf get zeros whatever total and inner are: a NaN or an
+        // infinity times the weight of 0 would be NaN.
 #pragma unroll
-        for (int v = 0; v < VPL; ++v) dz[v] = total == 0.0f ? 0.0f : -(z[v] / total) * inner;
+        for (int v = 0; v < VPL; ++v) {
+            const float d = -(z[v] / total) * inner;
+            dz[v] = (live >> v) & 1u ? d : 0.0f;
+        }
     }
     for (int j = 0; j < topk; ++j) {
         const int ej = __shfl_sync(FULL, e, j);

@@ -134,6 +134,36 @@ def test_route_backward(zb, T, E, k, renorm, dtype):
     near(dz, ref, step + (E + 2 * k + 16) * 2.0 ** -23 * size)
 
 
+@pytest.mark.parametrize("E", [7, 40, 100, 256])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_route_backward_masked_logits_get_no_gradient(zb, E, dtype, renorm):
+    """Logits of -inf get zeros whatever the rest of their row holds."""
+    k = 3
+    z = np.random.default_rng(E).normal(size=(7, E)) * 2
+    z[:, 1::3] = -INF
+    z[3, 0], z[4, 0] = NAN, INF
+    z[5] = -INF
+    r, lg, out = _route(zb, z, k, renorm, dtype)
+    dgn = np.random.default_rng(5).normal(size=(7, k))
+    dgn[1, 1], dgn[2, 0], dgn[5, 0] = NAN, INF, NAN
+    dg = dev(dgn, torch.float32)
+    dz = torch.full((7, E), NAN, dtype=dtype, device="cuda")
+    zb.zb_moe_route_backward(r, lg, out["expert"], out["gates"], dg, dz)
+    sync(zb)
+    got, masked = f64(dz), np.isneginf(f64(lg))
+    assert (got[masked] == 0).all()
+    chosen = np.zeros((7, E), bool)
+    for t, e in np.argwhere(out["expert"].cpu().numpy() >= 0):
+        chosen[t, int(out["expert"][t, e])] = True
+    # what is not finite reaches every logit that has a weight
+    for t in (1, 2, 3, 4):
+        assert not np.isfinite(got[t][chosen[t] if renorm else ~masked[t]]).any()
+    ref = om.route_backward(f64(lg)[[0, 6]], out["expert"].cpu().numpy()[[0, 6]], dgn.astype(np.float32)[[0, 6]], renorm)
+    step = 2.0 ** -8 * np.abs(ref) if dtype == torch.bfloat16 else 0.0
+    near(dz[[0, 6]], ref, step + (E + 2 * k + 16) * 2.0 ** -23 * np.abs(dgn[[0, 6]]).sum(1, keepdims=True))
+
+
 # --------------------------------------------------------------------- rows
 @pytest.mark.parametrize("T,E,k,w", [(1, 1, 1, 8), (3, 4, 2, 1032), (65, 8, 3, 520), (130, 32, 8, 2056),
                                      (257, 16, 2, 4104), (40, 64, 32, 136)])
