@@ -579,8 +579,10 @@ zb_status zb_post_validated_adamw(int32_t P, const double* const* stage_state,
  * Row buffers hold `rows` rows (T k, or any bound on offsets[E]); those at and
  * past offsets[E] are neither read (their values change nothing) nor written.
  * `offsets` is E + 1 ascending int32 on the device, from 0 to at most rows
- * (others give unspecified results, but no access leaves the buffers).  rows
- * and tokens may be 0 (row buffers may then be NULL). */
+ * (others give unspecified results, but no access leaves the buffers); the
+ * passes and products that read it take it from any 4-byte boundary (a row of
+ * several microbatches' offsets), as dispatch and combine take row_of and gates.
+ * rows and tokens may be 0 (row buffers may then be NULL). */
 
 /* 1 <= topk <= experts <= 256, topk <= 32, 0 <= tokens, tokens topk <= 2^30. */
 typedef struct zb_router {

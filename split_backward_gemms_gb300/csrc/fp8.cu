@@ -799,8 +799,6 @@ __global__ void __launch_bounds__(Fp8Epi<EPI, CG, MX>::THREADS, 1)
 }
 
 // ---------------------------------------------------------------- host side
-bool off4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
-
 zb_status launched(const char* who) {
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return zb::fail(ZB_ERR_CUDA, std::string(who) + " launch: " + cudaGetErrorString(e));
@@ -910,9 +908,9 @@ extern "C" zb_status zb_fp8_matmul(const zb_fp8_gemm* g, const int32_t* offsets,
         return zb::fail(ZB_ERR_INVALID_ARG, "zb_fp8_matmul: required pointer is NULL");
     if (bias && g->epilogue == ZB_FP8_GELU_GRAD)
         return zb::fail(ZB_ERR_INVALID_ARG, "zb_fp8_matmul: the GeLU' epilogue takes no bias");
-    if (off16(offsets) || off16(Xq) || off4(xs) || off16(Wq) || off4(ws) || off16(bias) || off16(H) || off16(out0) ||
+    if (off4(offsets) || off16(Xq) || off4(xs) || off16(Wq) || off4(ws) || off16(bias) || off16(H) || off16(out0) ||
         off16(out1))
-        return zb::fail(ZB_ERR_ALIGN, "zb_fp8_matmul: pointers must be 16-byte aligned (scales: 4)");
+        return zb::fail(ZB_ERR_ALIGN, "zb_fp8_matmul: pointers must be 16-byte aligned (offsets, scales: 4)");
     // tiles of 256 rows on pairs when they fill the SMs, else 128 (counts as if
     // the rows were spread evenly)
     const int64_t used = std::min<int64_t>(g->experts, g->M);

@@ -1132,9 +1132,9 @@ extern "C" zb_status zb_moe_forward(const zb_moe* m, const int32_t* offsets, con
     if (!offsets || !X || !W1 || !Y || (mlp && (!W2 || !H_save || !A_save)))
         return zb::fail(ZB_ERR_INVALID_ARG, "zb_moe_forward: required pointer is NULL");
     if (m->has_bias && (!b1 || (mlp && !b2))) return zb::fail(ZB_ERR_INVALID_ARG, "zb_moe_forward: bias pointer is NULL");
-    if (off16(offsets) || off16(X) || off16(W1) || off16(W2) || off16(b1) || off16(b2) || off16(H_save) ||
+    if (off4(offsets) || off16(X) || off16(W1) || off16(W2) || off16(b1) || off16(b2) || off16(H_save) ||
         off16(A_save) || off16(Y))
-        return zb::fail(ZB_ERR_ALIGN, "zb_moe_forward: pointers must be 16-byte aligned");
+        return zb::fail(ZB_ERR_ALIGN, "zb_moe_forward: pointers must be 16-byte aligned (offsets: 4)");
     const void* bias1 = m->has_bias ? b1 : nullptr;
     if (!mlp) {
         s = rows_product(*m, offsets, X, W1, false, m->f, m->h, bias1, nullptr, zb::EPI_STORE_BF16, Y, nullptr, stream);
@@ -1159,8 +1159,8 @@ extern "C" zb_status zb_moe_backward_input(const zb_moe* m, const int32_t* offse
     const bool mlp = m->act != ZB_ACT_NONE;
     if (!offsets || !dY || !W1 || !dX || (mlp && (!W2 || !H_save || !dH_out)))
         return zb::fail(ZB_ERR_INVALID_ARG, "zb_moe_backward_input: required pointer is NULL");
-    if (off16(offsets) || off16(dY) || off16(W1) || off16(W2) || off16(H_save) || off16(dH_out) || off16(dX))
-        return zb::fail(ZB_ERR_ALIGN, "zb_moe_backward_input: pointers must be 16-byte aligned");
+    if (off4(offsets) || off16(dY) || off16(W1) || off16(W2) || off16(H_save) || off16(dH_out) || off16(dX))
+        return zb::fail(ZB_ERR_ALIGN, "zb_moe_backward_input: pointers must be 16-byte aligned (offsets: 4)");
     if (!mlp) {
         s = rows_product(*m, offsets, dY, W1, true, m->h, m->f, nullptr, nullptr, zb::EPI_STORE_BF16, dX, nullptr, stream);
     } else {
@@ -1189,9 +1189,9 @@ extern "C" zb_status zb_moe_backward_weight(const zb_moe* m, const int32_t* offs
         return zb::fail(ZB_ERR_INVALID_ARG, "zb_moe_backward_weight: required pointer is NULL");
     if (m->has_bias && (!db1 || (mlp && !db2)))
         return zb::fail(ZB_ERR_INVALID_ARG, "zb_moe_backward_weight: bias-gradient pointer is NULL");
-    if (off16(offsets) || off16(X) || off16(A_save) || off16(dH) || off16(dY) || off16(dW1) || off16(dW2) ||
+    if (off4(offsets) || off16(X) || off16(A_save) || off16(dH) || off16(dY) || off16(dW1) || off16(dW2) ||
         off16(db1) || off16(db2))
-        return zb::fail(ZB_ERR_ALIGN, "zb_moe_backward_weight: pointers must be 16-byte aligned");
+        return zb::fail(ZB_ERR_ALIGN, "zb_moe_backward_weight: pointers must be 16-byte aligned (offsets: 4)");
     if (!workspace || ws_bytes < zb_moe_workspace_bytes(m))
         return zb::fail(ZB_ERR_WORKSPACE, "zb_moe_backward_weight: workspace missing or too small: need " +
                                               std::to_string(zb_moe_workspace_bytes(m)) + " bytes");

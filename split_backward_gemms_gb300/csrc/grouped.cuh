@@ -64,6 +64,7 @@ __device__ __forceinline__ void load_offsets(int* off, const int* offsets, int e
 
 // ---------------------------------------------------------------- host side
 bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+bool off4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 
 // 3-D map of a stack of `count` matrices [outer, inner], dense, of elements of
 // `es` bytes; 128-byte swizzle.

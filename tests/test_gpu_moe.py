@@ -313,6 +313,35 @@ def test_experts_weight_gradient(zb, case, accumulate):
                 near(t[e], ref, (hi - lo + 1) * 2.0 ** -23 * mag)
 
 
+def test_offsets_at_any_word(zb):
+    """Offsets of several microbatches in one tensor: the second one's are read
+    from a 4-byte boundary."""
+    counts, h, f = [37, 0, 90, 21], 144, 208
+    m, off, offd, s, _ = _setup(zb, counts, h, f, "erf", True, 0, 12)
+    R, E = sum(counts), len(counts)
+    both = i32(np.stack([np.zeros(E + 1), off]))  # rows of 5 words
+    assert both[1].data_ptr() % 16
+    runs = []
+    for o in (offd, both[1]):
+        H, A, Y, dH, dX = empty_bf16(R, f), empty_bf16(R, f), empty_bf16(R, h), empty_bf16(R, f), empty_bf16(R, h)
+        grads = [empty_f32(E, h, f), empty_f32(E, f, h), empty_f32(E, f), empty_f32(E, h)]
+        n = zb.zb_moe_workspace_bytes(m)
+        ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+        zb.zb_moe_forward(m, o, s["X"], s["W1"], s["W2"], s["b1"], s["b2"], H, A, Y)
+        zb.zb_moe_backward_input(m, o, s["dY"], s["W1"], s["W2"], H, dH, dX)
+        zb.zb_moe_backward_weight(m, o, s["X"], A, dH, s["dY"], *grads, 0, ws, n)
+        Xq, Xs = torch.zeros(R, h, dtype=torch.uint8, device="cuda"), empty_f32(R, 2)
+        Wq, Ws = torch.zeros(E, f, h, dtype=torch.uint8, device="cuda"), empty_f32(E, 2, 2)
+        Z = empty_bf16(R, f)
+        zb.zb_fp8_quantize_rows(R, h, s["X"], Xq, Xs)
+        zb.zb_fp8_quantize_weight(E, h, f, s["W1"], None, None, Wq, Ws)
+        zb.zb_fp8_matmul(zb.make_fp8_matmul(R, f, h, E), o, Xq, Xs, Wq, Ws, None, Z, None)
+        sync(zb)
+        runs.append([H, A, Y, dH, dX, Z] + grads)
+    for a, b in zip(*runs):
+        assert torch.equal(a, b) and not torch.isnan(a).any()
+
+
 def test_experts_do_not_touch_each_other(zb):
     """NaN and infinities in one expert's weights or rows stay in its own results."""
     counts, h, f = [37, 0, 90, 21], 136, 200
