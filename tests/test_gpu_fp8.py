@@ -163,6 +163,112 @@ def test_matmul(zb, case, scales):
     assert torch.isnan(o0[live:]).all()
 
 
+# Scales that differ from block to block, and enough blocks of K or tiles to take
+# the hand-over of scales (16 blocks of K a batch, two batches in shared memory,
+# eight groups of four blocks in tensor memory) more than once round.
+LONG = [
+    # counts (None: no offsets), N, K, epilogue
+    (70, 136, 2064, "store"),                # 17 blocks: a second, partial batch
+    (70, 136, 2304, "grad"),
+    ([5, 0, 129, 40], 264, 4096, "gelu"),    # 32: two whole batches, scales in 16-byte loads
+    (200, 264, 4224, "store"),               # 33: a slot used again within a tile, a ninth group
+    ([3, 140], 136, 4224, "grad"),
+    (130, 136, 4608, "store"),               # 36, in 16-byte loads
+    (300, 264, 6160, "grad"),                # 49: four batches
+    ([9, 31, 3, 0, 70, 1, 17, 2] * 11, 520, 2064, "store"),      # CTA pairs, three tiles a pair and more
+    ([9, 31, 3, 0, 70, 1, 17, 2] * 11, 520, 2064, "grad"),
+    ([2, 5, 0, 3, 1, 7, 4, 2] * 32, 776, 144, "store"),          # pairs, eleven tiles each: groups go round
+    ([2, 5, 0, 3, 1, 7, 4, 2] * 32, 776, 144, "gelu"),
+    ([257, 255, 256] * 25, 136, 400, "store"),                   # single CTAs, some with a second tile
+    ([257, 255, 256] * 25, 136, 2064, "grad"),
+]
+
+
+def _steps(rng, rows, cols, rb, lo, hi):
+    """2^lo .. 2^hi for each block of rb x 128."""
+    e = rng.integers(lo, hi + 1, size=(-(-rows // rb), -(-cols // 128)))
+    return np.exp2(np.repeat(np.repeat(e, rb, axis=0), 128, axis=1)[:rows, :cols].astype(np.float64))
+
+
+@pytest.mark.parametrize("scales", ["powers", "any"])
+@pytest.mark.parametrize("case", range(len(LONG)))
+def test_matmul_of_many_blocks(zb, case, scales):
+    counts, N, K, epi = LONG[case]
+    rng = np.random.default_rng(100 + case)
+    dense = isinstance(counts, int)
+    cl = [counts] if dense else counts
+    E, M = len(cl), sum(cl)
+    off = np.concatenate([[0], np.cumsum(cl)])
+    kb, nb, Np = -(-K // 128), -(-N // 128), -(-N // 16) * 16
+    Xq, Xs = e4(M, K), empty_f32(M, kb)
+    zb.zb_fp8_quantize_rows(M, K, dev(rng.normal(size=(M, K)) * _steps(rng, M, K, 1, -6, 6)), Xq, Xs)
+    QT, ST = e4(E, Np, K), empty_f32(E, nb, kb)
+    W = np.zeros((E, K, Np), np.float32)
+    for e in range(E):
+        W[e, :, :N] = rng.standard_normal((K, N), dtype=np.float32) * _steps(rng, K, N, 128, -6, 6)
+    zb.zb_fp8_quantize_weight(E, K, Np, dev(W), None, None, QT, ST)
+    del W
+    sync(zb)
+    Wq = QT.view(torch.uint8)[:, :N].contiguous().view(E4)
+    if scales == "any":
+        Xs = Xs * (0.5 + torch.rand_like(Xs))
+        ST = ST * (0.5 + torch.rand_like(ST))
+    H = dev(rng.normal(size=(M, N)))
+    o0, o1 = empty_bf16(M, N), empty_bf16(M, N)
+    g = zb.make_fp8_matmul(M, N, K, E, dict(store=zb.ZB_FP8_STORE, gelu=zb.ZB_FP8_GELU, grad=zb.ZB_FP8_GELU_GRAD)[epi],
+                           zb.ZB_ACT_GELU_ERF, zb.ZB_FP8_SCALE_ANY if scales == "any" else zb.ZB_FP8_SCALE_POW2)
+    zb.zb_fp8_matmul(g, None if dense else i32(off), Xq, Xs, Wq, ST, H if epi == "grad" else None, o0,
+                     o1 if epi == "gelu" else None)
+    sync(zb)
+    xv = values(Xq) * om.spread_scales(f64(Xs), M, K, 1)
+    ref, mag = np.zeros((M, N)), np.zeros((M, N))
+    for e, a, b in om.spans(off):
+        if b > a:
+            wv = (values(Wq[e]) * om.spread_scales(f64(ST[e]), N, K, 128)).T
+            ref[a:b], mag[a:b] = xv[a:b] @ wv, np.abs(xv[a:b]) @ np.abs(wv)
+    err = (K + kb) * 2.0 ** -23 * mag
+    if epi == "grad":
+        h = f64(H)
+        gp = ref * om.gelu_prime(h, "gelu_erf")
+        near(o0, gp, 2.0 ** -8 * np.abs(gp) + 1.2 * err + 1e-6 * (1 + np.abs(h)) * np.abs(ref))
+    else:
+        near(o0, ref, 2.0 ** -8 * np.abs(ref) + err)
+    if epi == "gelu":
+        ga = om.gelu(ref, "gelu_erf")
+        near(o1, ga, 2.0 ** -8 * np.abs(ga) + 1.2 * err + 1e-6 * np.abs(ref))
+
+
+@pytest.mark.parametrize("scales", ["powers", "any"])
+@pytest.mark.parametrize("M,N,K", [(70, 136, 400), (300, 2056, 400)])
+def test_matmul_of_extreme_scales(zb, M, N, K, scales):
+    """Blocks whose scales lie near either end of their range, the products in
+    range: rows of 2^-126 (subnormal values) to 2^100 against weights of the
+    inverse, another exponent for every block of K."""
+    rng = np.random.default_rng(M)
+    kb, nb, Np = -(-K // 128), -(-N // 128), -(-N // 16) * 16
+    ex = np.array([-128, 100, -60, 3])[:kb]  # of the values; scales are 2^-126 and about 2^-6 of them
+    of_k = np.exp2(np.repeat(ex, 128)[:K].astype(np.float64))
+    X = rng.normal(size=(M, K)) * of_k
+    W = np.zeros((1, K, Np))
+    W[0, :, :N] = rng.normal(size=(K, N)) / of_k[:, None] * np.where(np.repeat(ex, 128)[:K, None] < -100, 2.0 ** -4, 1.0)
+    Xq, Xs, QT, ST = e4(M, K), empty_f32(M, kb), e4(1, Np, K), empty_f32(1, nb, kb)
+    zb.zb_fp8_quantize_rows(M, K, dev(X), Xq, Xs)
+    zb.zb_fp8_quantize_weight(1, K, Np, dev(W), None, None, QT, ST)
+    sync(zb)
+    assert (f64(Xs)[:, 0] == 2.0 ** -126).all() and f64(Xs)[:, 1].min() > 2.0 ** 90
+    Wq = QT.view(torch.uint8)[:, :N].contiguous().view(E4)
+    if scales == "any":
+        Xs = Xs * (1.0 + torch.rand_like(Xs))
+    out = empty_bf16(M, N)
+    zb.zb_fp8_matmul(zb.make_fp8_matmul(M, N, K, scales=zb.ZB_FP8_SCALE_ANY if scales == "any" else zb.ZB_FP8_SCALE_POW2),
+                     None, Xq, Xs, Wq, ST, None, out, None)
+    sync(zb)
+    xv, wv = values(Xq) * om.spread_scales(f64(Xs), M, K, 1), values(Wq[0]) * om.spread_scales(f64(ST[0]), N, K, 128)
+    ref, mag = xv @ wv.T, np.abs(xv) @ np.abs(wv).T
+    assert (np.abs(xv[:, :128]) @ np.abs(wv[:, :128]).T).min() > 0.0  # the subnormal block counts
+    near(out, ref, 2.0 ** -8 * np.abs(ref) + (K + kb) * 2.0 ** -23 * mag)
+
+
 def test_matmul_scale_of_nan_reaches_its_row_only(zb):
     M, N, K = 40, 136, 256
     X = torch.ones(M, K, dtype=torch.bfloat16, device="cuda")
