@@ -637,10 +637,12 @@ zb_status zb_moe_combine_backward(int64_t tokens, int32_t topk, int64_t width, c
                                   const void* Yp, const int32_t* row_of, const float* gates, void* dYp,
                                   float* dgates, void* stream);
 
-/* E expert blocks of zb_block's mathematics on the rows of each.  Weights are
+/* E expert blocks of zb_block's mathematics on the rows of each.  As there, Y is
+ * the product of the stored (bf16) A and dX that of the stored dH.  Weights are
  * W1[E,h,f], W2[E,f,h], b1[E,f], b2[E,h] in bf16, gradients the same shapes in
  * fp32; X, Y, dY, dX are [rows,h] and H, A, dH [rows,f] in bf16.  h and f are
- * multiples of 8, 1 <= experts <= 256, 0 <= rows <= 2^30.  ZB_ACT_NONE: the
+ * multiples of 8 (of 16 where the same block also runs through the 8-bit
+ * quantisers), 1 <= experts <= 256, 0 <= rows <= 2^30.  ZB_ACT_NONE: the
  * single linear map Y_e = X_e W1[e] with Y, dY [rows,f] (W2, H, A, dH unused). */
 typedef struct zb_moe {
     int64_t rows, h, f;
@@ -700,7 +702,9 @@ typedef enum zb_fp8_epilogue {
 
 /* Powers of two, as the quantisers make them, are applied by the tensor cores
  * (of another positive scale only the power of two below it would count);
- * other fp32 scales, block by block, on the way to fp32 sums (slower). */
+ * other fp32 scales, block by block, on the way to fp32 sums (slower): there a
+ * row's and a weight's scale are multiplied in fp32 first, so that product has to
+ * lie in fp32's normal range. */
 typedef enum zb_fp8_scales { ZB_FP8_SCALE_POW2 = 0, ZB_FP8_SCALE_ANY = 1 } zb_fp8_scales;
 
 /* D[M,N] = X W_e^T by expert: row r of expert e has

@@ -198,7 +198,9 @@ struct Fp8Cfg {
 // with 64 columns each, four to a scheduler to hide the latency of GeLU's special
 // functions, of H and of the stores (with 8: GeLU' of 16 experts, 8190 rows, K
 // 1040, N 4104 92 us against 79); else 8, whose threads hold 128 sums and 32
-// loaded values.
+// loaded values.  640 threads leave 96 registers each at launch, which the scale
+// and epilogue roles' code overruns: 24 bytes a thread are spilled in the plain
+// form, 36 to 44 with GeLU, 60 with GeLU' (none without MX).
 // GeLU' keeps a warp's values of H in its staging boxes (copied while the product
 // runs) and stores from them; the others store through one box, or two.
 constexpr uint32_t FP8_BOX = 32 * 64;  // 32 rows x 32 columns of bf16
@@ -218,6 +220,11 @@ static_assert(128 * 64 + 512 * 104 <= 640 * 96 && 128 * 72 + 256 * 216 <= 384 * 
 // of row i the scale of operand row i + 32 r in block k.  Four groups are loaded
 // and handed over at once: with one, the loads' latency and the cluster-scope
 // release (about 2000 cycles) took longer than the group's MMAs.
+// A batch's slot is released by the commit after its last block.  The columns in
+// TMEM, eight groups in turn, need no release.  A group is copied in for block n
+// (counted over all tiles) after the wait for block n - 1's stage; that stage was
+// filled once the MMAs of block n - 1 - STAGES were complete, n - 6 at the earliest.
+// The group it replaces, eight before, was last read by block n - 8 or an earlier one.
 constexpr int MX_GROUPS = 4;      // groups in a batch
 constexpr int MX_SLOTS = 2;       // batches in shared memory
 constexpr uint32_t MX_TMEM = 256;  // first TMEM column of the scales, 16 a group

@@ -486,22 +486,33 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 // (MN-major: a row of 64 values is a line of 128 bytes, whatever the swizzle).
 //
 // The tensor core cuts off low bits as it accumulates, so the error of one
-// long accumulator grows with its length (1.4e-6 of the result after ~1024
-// rows, where plain fp32 sums are 3e-7 off).  So an accumulator takes W_SEG
+// long accumulator grows with its length (1.0e-6 of the result after 1024 rows,
+// 2.6e-6 after 2500, 1.9e-5 after 16384).  So an accumulator takes W_SEG
 // blocks of rows only; the 8 epilogue warps (32 lanes x 128 columns each) add
 // the partial sums in registers, rounding to nearest, while the MMAs of the
 // next segment fill the other accumulator.  The fp32 tile goes out through 32 x
 // 32 staging boxes, added in place by TMA reduce-adds when accumulating (one
 // add per element: no order to vary).
 //
+// W_SEG trades error for time, since the epilogue reads an accumulator once a
+// segment.  Error of experts of 512 to 16384 rows, and microseconds of W of 16384
+// rows, 16 experts, h 1024, f 4096 (overwriting, accumulating) and of 8 experts, h
+// 2048, f 8192 (the same):
+//   W_SEG 4   2.3e-7 to 2.7e-7   255, 287   763, 791
+//   W_SEG 6   3.1e-7 to 3.7e-7   230, 279   701, 756
+//   W_SEG 8   4.6e-7 to 4.8e-7   226, 279   679, 753
+// where a library product in fp32 is 1.6e-7 to 4.4e-7 off.  8 is the choice: an
+// eleventh less time than 4 for twice its error, which is still a fifth of that of
+// the dense block's W (2.4e-6).
+//
 // The stores share the copy unit with the next tile's loads and, issued at once,
 // queue before them.  So a tile's four chunks a warp go out W_PACE cycles times
 // its blocks of rows apart (at most W_PACE_MOST), which spreads them over about
 // the time in which the MMAs fill the two accumulators anew.  W of 16384 rows,
-// 16 experts, h 1024, f 4096: 235 us unpaced, 219 at 1500 cycles, 212 at 2000
-// to 2500, 230 at 3500; of 24570 rows, 64 experts (6 blocks each): 394, 374 at
-// 1500, 401 at 2000.  (Measured before the clearing of partial blocks, with which
-// the first is 232 from a cold L2, 11 us more.)
+// 16 experts, h 1024, f 4096: 249 us unpaced, 247 at 1000 cycles at most, 232 at
+// 1500, 226 at 2200, 234 at 3500 (of 400 a block); of 24570 rows, 64 experts (6
+// blocks each): 413, 406, 391, 386, 435.  Accumulating, the first is 308, 306, 296,
+// 279 and 267: the reduce-adds take longer than stores and would bear a slower pace.
 constexpr int W_SEG = 8;  // blocks of 64 rows
 constexpr int W_PACE = 250, W_PACE_MOST = 2200;
 // Warp 0 copies, warp 1 issues MMAs, warps 2 and 3 clear rows; warps 4-11 sum
@@ -1090,6 +1101,11 @@ zb_status wgrad(const zb_moe& m, const int32_t* offsets, const WProduct* p, int 
     a.err = err;
     tiles1 *= m.experts;
     tiles2 *= m.experts;
+    // CTA pairs copy half as many bytes of B a row.  With at least as many tiles as
+    // pairs of SMs they are faster: 96 tiles (16384 rows, 3 experts, h = f = 1024) 68 us
+    // against 89 with single CTAs, 512 tiles (16 experts, f 4096) 226 against 261, the
+    // same with narrow matrices (8 experts, 512 x 1024: 23).  They are with 64 tiles
+    // too (4096 rows, 2 experts, 1024 x 1024: 25 against 30); fewer were not measured.
     return tiles2 >= sm_count() / 2 ? launch_wgrad<2>(mi, mo, a, tiles2, stream)
                                      : launch_wgrad<1>(mi, mo, a, tiles1, stream);
 }

@@ -313,6 +313,30 @@ def test_experts_weight_gradient(zb, case, accumulate):
                 near(t[e], ref, (hi - lo + 1) * 2.0 ** -23 * mag)
 
 
+@pytest.mark.parametrize("counts,h,f", [([2500], 264, 520), ([5001, 64, 700], 136, 256)])
+def test_experts_weight_gradient_of_long_experts(zb, counts, h, f):
+    """W's sums are cut into accumulators of 512 rows.  Each of an accumulator's
+    512 / 16 adds cuts off half a step of the partial sum on average, 0.72 2^-24
+    of its size; partial sums of independent terms grow as the root of their
+    number, so the cuts come to 0.72 2^-24 (2/3) (512 / 16) of the result, and
+    the s accumulators' own fp32 sum adds at most 2^-24 sqrt(s).  (One accumulator
+    over 2500 rows would be 2.6e-6 off.)"""
+    m, off, offd, s, _ = _setup(zb, counts, h, f, "erf", False, 0, 31)
+    R, E = sum(counts), len(counts)
+    rng = np.random.default_rng(32)
+    A, dH = dev(rng.normal(size=(R, f))), dev(rng.normal(size=(R, f)))
+    dW1, dW2 = empty_f32(E, h, f), empty_f32(E, f, h)
+    n = zb.zb_moe_workspace_bytes(m)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    zb.zb_moe_backward_weight(m, offd, s["X"], A, dH, s["dY"], dW1, dW2, None, None, 0, ws, n)
+    sync(zb)
+    for e, lo, hi in om.spans(off):
+        tol = 2.0 ** -24 * (0.72 * 2 / 3 * 32 + (-(-(hi - lo) // 512)) ** 0.5)
+        for t, a, b in ((dW1, s["X"], dH), (dW2, A, s["dY"])):
+            ref = f64(a)[lo:hi].T @ f64(b)[lo:hi]
+            assert np.linalg.norm(f64(t[e]) - ref) < tol * np.linalg.norm(ref)
+
+
 def test_offsets_at_any_word(zb):
     """Offsets of several microbatches in one tensor: the second one's are read
     from a 4-byte boundary."""
