@@ -725,6 +725,118 @@ zb_status zb_fp8_matmul(const zb_fp8_gemm* g, const int32_t* offsets, const void
                         void* out1, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* Around the block: linear maps with an epilogue, layer norm, embedding      */
+/* ------------------------------------------------------------------------ */
+/* What a pipeline stage runs beside its block, with the same split backward.  A
+ * pre-norm residual block is
+ *     N = LN(R),  A = GeLU(N W1 + b1),  R' = A W2 + b2 + R
+ * (zb_layernorm_forward, two zb_linear_product), and the first stage makes R by
+ * zb_embedding_forward.  Its B is dH = (dR' W2^T) GeLU'(H), dN = dH W1^T
+ * (zb_linear_product, transposed) and zb_layernorm_backward_input, which adds
+ * dR' to what came through the norm.  Its W is deferrable: the maps' weights by
+ * zb_backward_weight (ZB_ACT_NONE), zb_layernorm_backward_weight and, on the
+ * first stage, whose embedding has no B, zb_embedding_backward.
+ *
+ * `dtype` is that of the residual stream (R, R' and their gradients): bf16 or
+ * fp32.  Weights, biases and the operands of products are bf16, sums and the
+ * gradients of weights fp32.  M, rows and tokens may be 0 (their buffers may then
+ * be NULL; a weight's gradient is zeros, or unchanged with `accumulate`). */
+
+typedef enum zb_linear_epilogue {
+    ZB_LINEAR_STORE = 0,     /* out0 = D (+ bias) (+ R), in `dtype`              */
+    ZB_LINEAR_GELU = 1,      /* H = D (+ bias): out0 = H (NULL: not kept),
+                                out1 = GeLU(H) (+ R)                             */
+    ZB_LINEAR_GELU_GRAD = 2  /* out0 = D * GeLU'(H) (+ R)                        */
+} zb_linear_epilogue;
+
+/* D[M,N] = X[M,K] W[K,N], or X W^T with W[N,K] (transposed = 1).  N and K are
+ * multiples of 8, M, N and K at most 2^30.  The strides are those of rows, in
+ * elements: multiples of 8, at least the row's width, at most 2^30; 0 means the
+ * row's width.  X (ldx), W (ldw), R (ldr), H (ldh) and the outputs (ldo) may so
+ * be slices of wider buffers. */
+typedef struct zb_linear {
+    int64_t M, N, K;
+    int64_t ldx, ldw, ldr, ldh, ldo;
+    int32_t transposed;
+    int32_t epilogue;  /* zb_linear_epilogue                                     */
+    int32_t act;       /* ZB_ACT_GELU_ERF or ZB_ACT_GELU_TANH (GeLU epilogues)   */
+    int32_t dtype;     /* zb_dtype of R and of STORE's output; the GeLU epilogues
+                          take ZB_DT_BF16 only (else ZB_ERR_DTYPE)               */
+} zb_linear;
+
+/* bias is bf16 [N] (NULL: none; not with GELU_GRAD), R [M,N] (NULL: none), H
+ * bf16 [M,N] (read by GELU_GRAD alone).  Everything is added to the fp32 sums,
+ * and rounded once.  The output may be R itself (the same address and stride);
+ * outputs otherwise overlap nothing that is read.  bf16 outputs sum K as
+ * zb_forward does; for fp32 outputs the partial sums of at most 512 products
+ * (more only where K / 512 of them do not fit) are added in registers, since
+ * one long accumulator loses low bits. */
+zb_status zb_linear_product(const zb_linear* g, const void* X, const void* W, const void* bias,
+                            const void* R, const void* H, void* out0, void* out1, void* stream);
+
+/* Layer norm of rows of `width` values (a multiple of 8, at most 32768):
+ *   mean = sum x / width,  rstd = (sum (x - mean)^2 / width + eps)^-1/2,
+ *   y = gamma (x - mean) rstd + beta. */
+typedef struct zb_layernorm {
+    int64_t rows;
+    int64_t width;
+    float eps;      /* > 0                                                      */
+    int32_t dtype;  /* zb_dtype of X, dR and dX                                  */
+} zb_layernorm;
+
+/* F.  X in `dtype`, gamma and beta bf16 [width] (beta NULL: none), Y bf16; mean
+ * and rstd fp32 [rows], kept for B and W (both NULL: not kept). */
+zb_status zb_layernorm_forward(const zb_layernorm* n, const void* X, const void* gamma, const void* beta,
+                               void* Y, float* mean, float* rstd, void* stream);
+
+/* B.  With xh = (x - mean) rstd and u = gamma dy (dY bf16):
+ *   dX = rstd (u - mean(u) - xh mean(u xh)) (+ dR), in `dtype`.
+ * dR (NULL: none) is the gradient that came along the residual; dX may be dR
+ * itself.  dX16, if not NULL, receives the same values in bf16 (the operand of
+ * the next products where the stream is fp32). */
+zb_status zb_layernorm_backward_input(const zb_layernorm* n, const void* dY, const void* X, const void* gamma,
+                                      const float* mean, const float* rstd, const void* dR, void* dX,
+                                      void* dX16, void* stream);
+
+/* W.  dgamma (+)= sum over the rows of dy xh, dbeta (+)= sum of dy (fp32
+ * [width]; dbeta NULL: not wanted), added to what is there when `accumulate`.
+ * The order of the sums is fixed. */
+zb_status zb_layernorm_backward_weight(const zb_layernorm* n, const void* dY, const void* X, const float* mean,
+                                       const float* rstd, float* dgamma, float* dbeta, int accumulate,
+                                       void* stream);
+
+/* Rows of a table E[vocab, width] (bf16; width a multiple of 8, at most 2^20;
+ * tokens and vocab at most 2^30) by id (int32). */
+typedef struct zb_embedding {
+    int64_t tokens;
+    int64_t vocab;
+    int64_t width;
+    float scale;
+    int32_t dtype;  /* zb_dtype of Y and dY                                      */
+} zb_embedding;
+
+/* F: Y[t, :] = scale E[ids[t], :].  An id outside [0, vocab) (padding) gives
+ * zeros, and has no gradient. */
+zb_status zb_embedding_forward(const zb_embedding* e, const int32_t* ids, const void* E, void* Y, void* stream);
+
+/* The tokens in ascending order of (id, token), those with an id outside [0,
+ * vocab) behind all others: order[i] is the i-th token, sorted_id[i] its id (-1
+ * outside).  Workspace: zb_embedding_workspace_bytes, 256-byte aligned. */
+size_t zb_embedding_workspace_bytes(const zb_embedding* e);
+zb_status zb_embedding_sort(const zb_embedding* e, const int32_t* ids, int32_t* order, int32_t* sorted_id,
+                            void* workspace, size_t ws_bytes, void* stream);
+
+/* W: dE[v, :] (+)= scale * sum of dY[t, :] over the tokens of id v, fp32
+ * [vocab, width], from zb_embedding_sort's results.  accumulate = 0 writes every
+ * row (zeros where an id has no token), accumulate = 1 adds to the rows of the
+ * ids that occur and leaves the others alone.  The order of the sums is fixed
+ * (32 tokens at a time).  An `order` or `sorted_id` that the sort has not made
+ * gives unspecified sums, but no access leaves the buffers. */
+zb_status zb_embedding_backward(const zb_embedding* e, const int32_t* order, const int32_t* sorted_id,
+                                const void* dY, float* dE, int accumulate, void* workspace, size_t ws_bytes,
+                                void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Status                                                                   */
 /* ------------------------------------------------------------------------ */
 

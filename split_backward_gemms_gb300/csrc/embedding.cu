@@ -1,0 +1,486 @@
+// embedding.cu — rows of a table by id: the lookup (F of a pipeline's first
+// stage) and the table's gradient (its W; there is no B) from the tokens in the
+// order of their ids.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <string>
+
+#include "ptx.cuh"
+#include "zb_internal.h"
+
+namespace {
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// ---------------------------------------------------------------- lookup
+// A warp copies up to 32 x LOOK_U pieces of 8 values of one token's row.
+constexpr int LOOK_U = 4;
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+    zb_embedding_forward_kernel(const int* __restrict__ ids, const uint4* __restrict__ E, T* __restrict__ Y,
+                                long long tokens, long long vocab, int w8, int segs, float scale) {
+    const long long item = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const long long t = item / segs;
+    if (t >= tokens) return;
+    const int at = static_cast<int>(item - t * segs) * 32 * LOOK_U + (threadIdx.x & 31);
+    const int id = ids[t];
+    const bool on = id >= 0 && id < vocab;
+    const uint4* src = E + static_cast<long long>(on ? id : 0) * w8;
+    uint4 q[LOOK_U];
+#pragma unroll
+    for (int u = 0; u < LOOK_U; ++u) {
+        q[u] = make_uint4(0, 0, 0, 0);
+        if (on && at + 32 * u < w8) q[u] = src[at + 32 * u];
+    }
+#pragma unroll
+    for (int u = 0; u < LOOK_U; ++u) {
+        const int k = at + 32 * u;
+        if (k >= w8) break;
+        const uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = on ? __uint_as_float(w[i] << 16) * scale : 0.0f;
+            v[2 * i + 1] = on ? __uint_as_float(w[i] & 0xffff0000u) * scale : 0.0f;
+        }
+        T* y = Y + (t * w8 + k) * 8;
+        if constexpr (sizeof(T) == 2) {
+            *reinterpret_cast<uint4*>(y) =
+                make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+        } else {
+            reinterpret_cast<float4*>(y)[0] = make_float4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<float4*>(y)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- sort
+// Keys are ids, `vocab` standing for every id outside the table.
+__device__ __forceinline__ uint32_t key_of(int id, uint32_t vocab) {
+    return static_cast<uint32_t>(id) < vocab ? static_cast<uint32_t>(id) : vocab;
+}
+__device__ __forceinline__ int id_of(uint32_t key, uint32_t vocab) { return key < vocab ? static_cast<int>(key) : -1; }
+
+// A stable radix sort by one cluster of 8 blocks, digits from the lowest up.  A
+// block owns an eighth of the tokens and a warp a contiguous part of them, so
+// that a digit's tokens are placed in the order (block, warp, token): each warp
+// counts its digits, the counts are summed over warps and blocks (through
+// distributed shared memory) into the first place of each warp's tokens of each
+// digit, and the warp places its tokens by them.
+constexpr int SORT_BLOCKS = 8;
+constexpr int SORT_THREADS = 1024;
+constexpr int SORT_WARPS = SORT_THREADS / 32;
+constexpr int SORT_BITS = 10;  // of a digit, at most
+constexpr size_t sort_smem(int bits) { return (static_cast<size_t>(SORT_WARPS + 1) << bits) * 4; }
+
+struct SortArgs {
+    const int* ids;
+    int tokens, bits, passes;  // bits of a digit
+    uint32_t vocab;
+    uint32_t *keys[2], *vals[2];
+    int *order, *sorted_id;
+};
+
+__global__ void __cluster_dims__(SORT_BLOCKS, 1, 1) __launch_bounds__(SORT_THREADS)
+    zb_embedding_sort_kernel(const SortArgs a) {
+    extern __shared__ uint32_t sort_shared[];
+    __shared__ uint32_t warp_total[SORT_WARPS];
+    const int digits = 1 << a.bits;
+    uint32_t* hist = sort_shared;                        // [warp][digit]
+    uint32_t* total = sort_shared + SORT_WARPS * digits;  // [digit]: the block's
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = threadIdx.x;
+    const uint32_t rank = zbp::cluster_ctarank();
+    const long long n = a.tokens;
+    const int part = static_cast<int>(rank) * SORT_WARPS + warp;
+    const int lo = static_cast<int>(n * part / (SORT_BLOCKS * SORT_WARPS));
+    const int hi = static_cast<int>(n * (part + 1) / (SORT_BLOCKS * SORT_WARPS));
+    uint32_t* mine = hist + warp * digits;
+    for (int pass = 0; pass < a.passes; ++pass) {
+        const uint32_t* src_key = a.keys[(pass + 1) & 1];
+        const uint32_t* src_val = a.vals[(pass + 1) & 1];
+        const int shift = pass * a.bits;
+        auto key_at = [&](int i) { return pass == 0 ? key_of(a.ids[i], a.vocab) : __ldcg(src_key + i); };
+        auto digit_of = [&](uint32_t k) { return (k >> shift) & static_cast<uint32_t>(digits - 1); };
+        for (int d = lane; d < digits; d += 32) mine[d] = 0;
+        __syncwarp();
+        for (int i = lo + lane; i < hi; i += 32) atomicAdd(&mine[digit_of(key_at(i))], 1u);
+        __syncthreads();
+        // each warp's count becomes the number of such tokens in the warps before it
+        uint32_t here = 0;
+        if (t < digits) {
+            for (int w = 0; w < SORT_WARPS; ++w) {
+                const uint32_t c = hist[w * digits + t];
+                hist[w * digits + t] = here;
+                here += c;
+            }
+            total[t] = here;
+        }
+        zbp::cluster_sync();
+        // the digit's tokens in the blocks before this one, and in all
+        uint32_t before = 0, all = 0;
+        if (t < digits) {
+            const uint32_t at = zbp::smem_u32(&total[t]);
+#pragma unroll
+            for (int b = 0; b < SORT_BLOCKS; ++b) {
+                uint32_t c;
+                asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(c) : "r"(zbp::mapa_shared(at, b)) : "memory");
+                if (b < static_cast<int>(rank)) before += c;
+                all += c;
+            }
+        }
+        uint32_t sum = all;  // over the digits up to this one
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t u = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += u;
+        }
+        if (lane == 31) warp_total[warp] = sum;
+        zbp::cluster_sync();  // also: every block has read the totals
+        for (int w = 0; w < warp; ++w) sum += warp_total[w];
+        if (t < digits) total[t] = sum - all + before;
+        __syncthreads();
+        const bool last = pass + 1 == a.passes;
+        for (int i0 = lo; i0 < hi; i0 += 32) {
+            const int i = i0 + lane;
+            const bool on = i < hi;
+            const uint32_t key = on ? key_at(i) : 0u;
+            const uint32_t d = on ? digit_of(key) : ~0u;
+            const uint32_t peers = __match_any_sync(0xffffffffu, d);
+            const int before_me = __popc(peers & ((1u << lane) - 1u));
+            uint32_t place = 0;
+            if (on) place = total[d] + mine[d] + static_cast<uint32_t>(before_me);
+            __syncwarp();
+            if (on && before_me == 0) mine[d] += static_cast<uint32_t>(__popc(peers));
+            __syncwarp();
+            if (on) {
+                const uint32_t val = pass == 0 ? static_cast<uint32_t>(i) : __ldcg(src_val + i);
+                if (last) {
+                    a.order[place] = static_cast<int>(val);
+                    a.sorted_id[place] = id_of(key, a.vocab);
+                } else {
+                    a.keys[pass & 1][place] = key;
+                    a.vals[pass & 1][place] = val;
+                }
+            }
+        }
+        zbp::cluster_sync();  // the next pass reads what the others placed; no one's shared memory is read any more
+    }
+}
+
+// Few tokens: a token's place is the number of tokens that go before it.  One
+// block, every key in shared memory.
+constexpr int RANK_TOKENS = 1024;
+
+__global__ void __launch_bounds__(RANK_TOKENS)
+    zb_embedding_rank_kernel(const int* __restrict__ ids, int tokens, uint32_t vocab, int* __restrict__ order,
+                             int* __restrict__ sorted_id) {
+    __shared__ __align__(16) uint32_t keys[RANK_TOKENS];
+    const int t = threadIdx.x;
+    const int n4 = (tokens + 3) / 4;
+    const uint32_t key = t < tokens ? key_of(ids[t], vocab) : ~0u;  // past the end: behind every key
+    if (t < 4 * n4) keys[t] = key;
+    __syncthreads();
+    if (t >= tokens) return;
+    int place = 0;
+    for (int j = 0; j < n4; ++j) {
+        const uint4 k = reinterpret_cast<const uint4*>(keys)[j];
+        const uint32_t v[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) place += v[i] < key || (v[i] == key && 4 * j + i < t);
+    }
+    order[place] = t;
+    sorted_id[place] = id_of(key, vocab);
+}
+
+// ---------------------------------------------------------------- gradient
+// The sorted tokens are cut into pieces of PIECE.  A block sums a piece's runs of
+// equal ids, a thread 4 columns.  A run that lies within its piece goes straight
+// to the table's gradient; what a run has in a piece that it shares with another
+// piece goes to the workspace (a row for the run that came in from the left, one
+// for the run that goes on to the right), and a second kernel adds such a run's
+// parts in order.  Without accumulation blocks of their own write zeros to the
+// rows of the ids that do not occur.
+constexpr int PIECE = 32;
+constexpr int GRAD_THREADS = 256;
+constexpr int ZERO_ROWS = GRAD_THREADS / 32;
+
+struct GradArgs {
+    const int* order;
+    const int* sorted_id;
+    const void* dY;
+    float* dE;
+    float4* part;  // [pieces][2][w4]
+    int tokens, pieces, w4, col_blocks;
+    uint32_t vocab;
+    int accumulate;
+    float scale;
+};
+
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+    const uint2 q = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xffff0000u), __uint_as_float(q.y << 16),
+                       __uint_as_float(q.y & 0xffff0000u));
+}
+__device__ __forceinline__ void add4(float4& a, const float4& b) {
+    a.x += b.x;
+    a.y += b.y;
+    a.z += b.z;
+    a.w += b.w;
+}
+__device__ __forceinline__ void finish(const GradArgs& a, int id, int c, const float4& s) {
+    float4* out = reinterpret_cast<float4*>(a.dE) + static_cast<long long>(id) * a.w4 + c;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (a.accumulate) v = *out;
+    v.x = fmaf(a.scale, s.x, v.x);
+    v.y = fmaf(a.scale, s.y, v.y);
+    v.z = fmaf(a.scale, s.z, v.z);
+    v.w = fmaf(a.scale, s.w, v.w);
+    *out = v;
+}
+
+// The warp's search for `id` among the sorted ids (as unsigned: -1 is the last).
+__device__ __forceinline__ bool occurs(const int* sorted_id, int n, uint32_t id) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, len = n;  // the first entry >= id lies in [lo, lo + len]
+    while (len > 0) {
+        const int step = (len + 31) / 32;
+        const int at = lo + (lane + 1) * step - 1;
+        const int end = lo + len;
+        const uint32_t v = at < end ? static_cast<uint32_t>(sorted_id[at]) : ~0u;
+        if (__any_sync(0xffffffffu, at < end && v == id)) return true;
+        const int less = __popc(__ballot_sync(0xffffffffu, at < end && v < id));
+        lo += less * step;
+        len = min(step - 1, end - lo);
+    }
+    return false;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(GRAD_THREADS) zb_embedding_backward_kernel(const GradArgs a, int zero_blocks) {
+    if (static_cast<int>(blockIdx.x) < zero_blocks) {
+        const long long row = static_cast<long long>(blockIdx.x) * ZERO_ROWS + (threadIdx.x >> 5);
+        if (row >= a.vocab) return;
+        if (occurs(a.sorted_id, a.tokens, static_cast<uint32_t>(row))) return;
+        float4* out = reinterpret_cast<float4*>(a.dE) + row * a.w4;
+        for (int c = threadIdx.x & 31; c < a.w4; c += 32) out[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        return;
+    }
+    __shared__ int id_s[PIECE + 2], tok_s[PIECE];
+    const int b = static_cast<int>(blockIdx.x) - zero_blocks;
+    const int piece = b / a.col_blocks;
+    const int c = (b - piece * a.col_blocks) * GRAD_THREADS + threadIdx.x;
+    const int first = piece * PIECE, n = min(PIECE, a.tokens - first);
+    if (threadIdx.x < PIECE + 2) {
+        const int i = first - 1 + static_cast<int>(threadIdx.x);
+        id_s[threadIdx.x] = i >= 0 && i < a.tokens ? a.sorted_id[i] : -1;
+        if (threadIdx.x < PIECE) {
+            const int tok = threadIdx.x < n ? a.order[first + threadIdx.x] : 0;
+            tok_s[threadIdx.x] = tok >= 0 && tok < a.tokens ? tok : 0;
+        }
+    }
+    __syncthreads();
+    if (c >= a.w4) return;
+    const T* dY = static_cast<const T*>(a.dY) + 4 * c;
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    bool from_left = id_s[0] == id_s[1];
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+        const int id = id_s[i + 1];
+        add4(sum, load4(dY + static_cast<long long>(tok_s[i]) * (4 * a.w4)));
+        const bool more = id_s[i + 2] == id;  // the run goes on
+        if (more && i + 1 < n) continue;
+        if (static_cast<uint32_t>(id) < a.vocab) {
+            if (from_left)
+                a.part[(2LL * piece) * a.w4 + c] = sum;
+            else if (more)
+                a.part[(2LL * piece + 1) * a.w4 + c] = sum;
+            else
+                finish(a, id, c, sum);
+        }
+        sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        from_left = false;
+    }
+}
+
+// Adds the parts of the run that starts in piece p and goes on after it.
+constexpr int JOIN_THREADS = 64;
+
+__global__ void __launch_bounds__(JOIN_THREADS) zb_embedding_join_kernel(const GradArgs a, int col_blocks) {
+    const int piece = blockIdx.x / col_blocks;
+    const int c = (blockIdx.x - piece * col_blocks) * JOIN_THREADS + threadIdx.x;
+    const int first = piece * PIECE, end = first + PIECE;  // not the last piece
+    const int id = a.sorted_id[end - 1];
+    if (static_cast<uint32_t>(id) >= a.vocab || a.sorted_id[end] != id) return;
+    // a run that came in from the left and fills the piece is joined by an earlier block
+    if (first > 0 && a.sorted_id[first] == id && a.sorted_id[first - 1] == id) return;
+    if (c >= a.w4) return;
+    float4 sum = a.part[(2LL * piece + 1) * a.w4 + c];
+    for (int p = piece + 1; p < a.pieces; ++p) {
+        add4(sum, a.part[2LL * p * a.w4 + c]);
+        const int next = (p + 1) * PIECE;
+        if (next >= a.tokens || a.sorted_id[next] != id || a.sorted_id[next - 1] != id) break;
+    }
+    finish(a, id, c, sum);
+}
+
+// ---------------------------------------------------------------- host side
+bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+bool off4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+zb_status check_embedding(const char* who, const zb_embedding* e) {
+    const std::string w = who;
+    if (!e) return zb::fail(ZB_ERR_INVALID_ARG, w + ": descriptor is NULL");
+    if (e->tokens < 0 || e->tokens > (1LL << 30)) return zb::fail(ZB_ERR_SHAPE, w + ": tokens must be in [0, 2^30]");
+    if (e->vocab < 1 || e->vocab > (1LL << 30)) return zb::fail(ZB_ERR_SHAPE, w + ": vocab must be in [1, 2^30]");
+    if (e->width < 1 || e->width > (1LL << 20)) return zb::fail(ZB_ERR_SHAPE, w + ": width must be in [1, 2^20]");
+    if (e->width % 8) return zb::fail(ZB_ERR_ALIGN, w + ": width must be a multiple of 8");
+    if (e->dtype != ZB_DT_BF16 && e->dtype != ZB_DT_F32) return zb::fail(ZB_ERR_DTYPE, w + ": unknown dtype");
+    return ZB_OK;
+}
+
+zb_status launched(const char* who) {
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return zb::fail(ZB_ERR_CUDA, std::string(who) + " launch: " + cudaGetErrorString(e));
+    zb::clear_error();
+    return ZB_OK;
+}
+
+zb_status done() {
+    zb::clear_error();
+    return ZB_OK;
+}
+
+size_t sort_bytes(const zb_embedding& e) { return e.tokens > RANK_TOKENS ? 16 * static_cast<size_t>(e.tokens) : 0; }
+size_t pieces_of(const zb_embedding& e) { return (static_cast<size_t>(e.tokens) + PIECE - 1) / PIECE; }
+
+zb_status check_workspace(const char* who, const zb_embedding* e, const void* workspace, size_t ws_bytes) {
+    const size_t need = zb_embedding_workspace_bytes(e);
+    if (need && (!workspace || ws_bytes < need))
+        return zb::fail(ZB_ERR_WORKSPACE, std::string(who) + ": workspace missing or too small: need " +
+                                              std::to_string(need) + " bytes");
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+        return zb::fail(ZB_ERR_ALIGN, std::string(who) + ": workspace must be 256-byte aligned");
+    return ZB_OK;
+}
+
+}  // namespace
+
+extern "C" zb_status zb_embedding_forward(const zb_embedding* e, const int32_t* ids, const void* E, void* Y,
+                                          void* stream) {
+    zb_status s = check_embedding("zb_embedding_forward", e);
+    if (s != ZB_OK) return s;
+    if (e->tokens == 0) return done();
+    if (!ids || !E || !Y) return zb::fail(ZB_ERR_INVALID_ARG, "zb_embedding_forward: required pointer is NULL");
+    if (off4(ids) || off16(E) || off16(Y))
+        return zb::fail(ZB_ERR_ALIGN, "zb_embedding_forward: pointers must be 16-byte aligned (ids: 4)");
+    const int w8 = static_cast<int>(e->width / 8);
+    const int segs = (w8 + 32 * LOOK_U - 1) / (32 * LOOK_U);
+    const long long blocks = (e->tokens * segs + 7) / 8;
+    if (blocks > 0x7fffffffLL) return zb::fail(ZB_ERR_SHAPE, "zb_embedding_forward: too many elements");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (e->dtype == ZB_DT_BF16)
+        zb_embedding_forward_kernel<<<static_cast<unsigned>(blocks), 256, 0, st>>>(
+            ids, static_cast<const uint4*>(E), static_cast<__nv_bfloat16*>(Y), e->tokens, e->vocab, w8, segs, e->scale);
+    else
+        zb_embedding_forward_kernel<<<static_cast<unsigned>(blocks), 256, 0, st>>>(
+            ids, static_cast<const uint4*>(E), static_cast<float*>(Y), e->tokens, e->vocab, w8, segs, e->scale);
+    return launched("zb_embedding_forward");
+}
+
+extern "C" size_t zb_embedding_workspace_bytes(const zb_embedding* e) {
+    if (check_embedding("zb_embedding_workspace_bytes", e) != ZB_OK) return 0;
+    // the sort's two copies of keys and tokens, or the gradient's parts of runs
+    const size_t parts = pieces_of(*e) > 1 ? pieces_of(*e) * 2 * static_cast<size_t>(e->width) * 4 : 0;
+    const size_t need = std::max(sort_bytes(*e), parts);
+    zb::clear_error();
+    return (need + 255) / 256 * 256;
+}
+
+extern "C" zb_status zb_embedding_sort(const zb_embedding* e, const int32_t* ids, int32_t* order, int32_t* sorted_id,
+                                       void* workspace, size_t ws_bytes, void* stream) {
+    zb_status s = check_embedding("zb_embedding_sort", e);
+    if (s != ZB_OK) return s;
+    if (e->tokens == 0) return done();
+    if (!ids || !order || !sorted_id) return zb::fail(ZB_ERR_INVALID_ARG, "zb_embedding_sort: required pointer is NULL");
+    if (off4(ids) || off4(order) || off4(sorted_id))
+        return zb::fail(ZB_ERR_ALIGN, "zb_embedding_sort: pointers must be 4-byte aligned");
+    s = check_workspace("zb_embedding_sort", e, workspace, ws_bytes);
+    if (s != ZB_OK) return s;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int n = static_cast<int>(e->tokens);
+    const uint32_t vocab = static_cast<uint32_t>(e->vocab);
+    if (n <= RANK_TOKENS) {
+        zb_embedding_rank_kernel<<<1, (n + 31) / 32 * 32, 0, st>>>(ids, n, vocab, order, sorted_id);
+        return launched("zb_embedding_sort");
+    }
+    int bits = 1;
+    while (vocab >> bits) ++bits;
+    SortArgs a;
+    a.ids = ids;
+    a.tokens = n;
+    a.passes = (bits + SORT_BITS - 1) / SORT_BITS;
+    a.bits = (bits + a.passes - 1) / a.passes;
+    a.vocab = vocab;
+    uint32_t* ws = static_cast<uint32_t*>(workspace);
+    for (int i = 0; i < 2; ++i) {
+        a.keys[i] = ws + static_cast<size_t>(2 * i) * n;
+        a.vals[i] = ws + static_cast<size_t>(2 * i + 1) * n;
+    }
+    a.order = order;
+    a.sorted_id = sorted_id;
+    const cudaError_t err = cudaFuncSetAttribute(zb_embedding_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 static_cast<int>(sort_smem(SORT_BITS)));
+    if (err != cudaSuccess)
+        return zb::fail(ZB_ERR_CUDA, std::string("zb_embedding_sort: cudaFuncSetAttribute: ") + cudaGetErrorString(err));
+    zb_embedding_sort_kernel<<<SORT_BLOCKS, SORT_THREADS, sort_smem(a.bits), st>>>(a);
+    return launched("zb_embedding_sort");
+}
+
+extern "C" zb_status zb_embedding_backward(const zb_embedding* e, const int32_t* order, const int32_t* sorted_id,
+                                           const void* dY, float* dE, int accumulate, void* workspace, size_t ws_bytes,
+                                           void* stream) {
+    zb_status s = check_embedding("zb_embedding_backward", e);
+    if (s != ZB_OK) return s;
+    if (!dE || (e->tokens > 0 && (!order || !sorted_id || !dY)))
+        return zb::fail(ZB_ERR_INVALID_ARG, "zb_embedding_backward: required pointer is NULL");
+    if (off4(order) || off4(sorted_id) || off16(dY) || off16(dE))
+        return zb::fail(ZB_ERR_ALIGN, "zb_embedding_backward: dY and dE must be 16-byte aligned (indices: 4)");
+    s = check_workspace("zb_embedding_backward", e, workspace, ws_bytes);
+    if (s != ZB_OK) return s;
+    GradArgs a;
+    a.order = order;
+    a.sorted_id = sorted_id;
+    a.dY = dY;
+    a.dE = dE;
+    a.part = static_cast<float4*>(workspace);
+    a.tokens = static_cast<int>(e->tokens);
+    a.pieces = static_cast<int>(pieces_of(*e));
+    a.w4 = static_cast<int>(e->width / 4);
+    a.col_blocks = (a.w4 + GRAD_THREADS - 1) / GRAD_THREADS;
+    a.vocab = static_cast<uint32_t>(e->vocab);
+    a.accumulate = accumulate != 0;
+    a.scale = e->scale;
+    const long long zero = accumulate ? 0 : (e->vocab + ZERO_ROWS - 1) / ZERO_ROWS;
+    const long long blocks = zero + static_cast<long long>(a.pieces) * a.col_blocks;
+    const int join_cols = (a.w4 + JOIN_THREADS - 1) / JOIN_THREADS;
+    const long long joins = static_cast<long long>(std::max(a.pieces - 1, 0)) * join_cols;
+    if (blocks > 0x7fffffffLL || joins > 0x7fffffffLL)
+        return zb::fail(ZB_ERR_SHAPE, "zb_embedding_backward: too many elements");
+    if (blocks == 0) return done();
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (e->dtype == ZB_DT_BF16)
+        zb_embedding_backward_kernel<__nv_bfloat16>
+            <<<static_cast<unsigned>(blocks), GRAD_THREADS, 0, st>>>(a, static_cast<int>(zero));
+    else
+        zb_embedding_backward_kernel<float>
+            <<<static_cast<unsigned>(blocks), GRAD_THREADS, 0, st>>>(a, static_cast<int>(zero));
+    if (joins > 0) zb_embedding_join_kernel<<<static_cast<unsigned>(joins), JOIN_THREADS, 0, st>>>(a, join_cols);
+    return launched("zb_embedding_backward");
+}

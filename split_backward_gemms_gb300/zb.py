@@ -42,6 +42,7 @@ ZB_ACT_GELU_ERF = 1
 ZB_ACT_GELU_TANH = 2
 ZB_FP8_STORE, ZB_FP8_GELU, ZB_FP8_GELU_GRAD = range(3)
 ZB_FP8_SCALE_POW2, ZB_FP8_SCALE_ANY = range(2)
+ZB_LINEAR_STORE, ZB_LINEAR_GELU, ZB_LINEAR_GELU_GRAD = range(3)
 ZB_BLOCK_NO_SPLIT_K = 1  # zb_block.flags: single passes never split K
 
 ZB_OP_F, ZB_OP_B, ZB_OP_W, ZB_OP_BW, ZB_OP_OPT = range(5)
@@ -126,6 +127,21 @@ class zb_fp8_gemm(C.Structure):
                 ("epilogue", C.c_int32), ("act", C.c_int32), ("scales", C.c_int32)]
 
 
+class zb_linear(C.Structure):
+    _fields_ = [("M", C.c_int64), ("N", C.c_int64), ("K", C.c_int64), ("ldx", C.c_int64), ("ldw", C.c_int64),
+                ("ldr", C.c_int64), ("ldh", C.c_int64), ("ldo", C.c_int64), ("transposed", C.c_int32),
+                ("epilogue", C.c_int32), ("act", C.c_int32), ("dtype", C.c_int32)]
+
+
+class zb_layernorm(C.Structure):
+    _fields_ = [("rows", C.c_int64), ("width", C.c_int64), ("eps", C.c_float), ("dtype", C.c_int32)]
+
+
+class zb_embedding(C.Structure):
+    _fields_ = [("tokens", C.c_int64), ("vocab", C.c_int64), ("width", C.c_int64), ("scale", C.c_float),
+                ("dtype", C.c_int32)]
+
+
 class ZBError(RuntimeError):
     def __init__(self, status: int, where: str, msg: str):
         super().__init__(f"{where}: {STATUS_NAMES.get(status, status)}: {msg}")
@@ -180,6 +196,13 @@ def _load():
         "zb_fp8_quantize_rows": [C.c_int64, C.c_int64, vp, vp, vp, vp],
         "zb_fp8_quantize_weight": [C.c_int32, C.c_int64, C.c_int64, vp, vp, vp, vp, vp, vp],
         "zb_fp8_matmul": [C.POINTER(zb_fp8_gemm)] + [vp] * 10,
+        "zb_linear_product": [C.POINTER(zb_linear)] + [vp] * 8,
+        "zb_layernorm_forward": [C.POINTER(zb_layernorm)] + [vp] * 7,
+        "zb_layernorm_backward_input": [C.POINTER(zb_layernorm)] + [vp] * 9,
+        "zb_layernorm_backward_weight": [C.POINTER(zb_layernorm)] + [vp] * 6 + [C.c_int, vp],
+        "zb_embedding_forward": [C.POINTER(zb_embedding)] + [vp] * 4,
+        "zb_embedding_sort": [C.POINTER(zb_embedding)] + [vp] * 4 + [sz, vp],
+        "zb_embedding_backward": [C.POINTER(zb_embedding)] + [vp] * 4 + [C.c_int, vp, sz, vp],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -189,7 +212,8 @@ def _load():
     lib.zb_last_error.restype = C.c_char_p
     lib.zb_grad_stats_scratch_bytes.argtypes = []
     lib.zb_grad_stats_scratch_bytes.restype = C.c_size_t
-    for name, desc in (("zb_moe_route_workspace_bytes", zb_router), ("zb_moe_workspace_bytes", zb_moe)):
+    for name, desc in (("zb_moe_route_workspace_bytes", zb_router), ("zb_moe_workspace_bytes", zb_moe),
+                       ("zb_embedding_workspace_bytes", zb_embedding)):
         getattr(lib, name).argtypes = [C.POINTER(desc)]
         getattr(lib, name).restype = C.c_size_t
     lib.zb_version.argtypes = []
@@ -578,6 +602,66 @@ def make_fp8_matmul(M: int, N: int, K: int, experts: int = 1, epilogue: int = ZB
 def zb_fp8_matmul(g, offsets, Xq, xs, Wq, ws, H, out0, out1, bias=None, stream=None):
     _check(LIB.zb_fp8_matmul(C.byref(g), _ptr(offsets), _ptr(Xq), _ptr(xs), _ptr(Wq), _ptr(ws), _ptr(bias),
                              _ptr(H), _ptr(out0), _ptr(out1), _stream(stream)), "zb_fp8_matmul")
+
+
+# ---------------------------------------------------------------- around the block
+def make_linear(M: int, N: int, K: int, transposed: bool = False, epilogue: int = ZB_LINEAR_STORE,
+                act: int = ZB_ACT_GELU_ERF, dtype: int = ZB_DT_BF16, ldx: int = 0, ldw: int = 0, ldr: int = 0,
+                ldh: int = 0, ldo: int = 0) -> zb_linear:
+    """Row strides of 0 mean dense rows; dtype is that of R and of STORE's output."""
+    return zb_linear(M, N, K, ldx, ldw, ldr, ldh, ldo, 1 if transposed else 0, epilogue, act, dtype)
+
+
+def zb_linear_product(g, X, W, bias, R, H, out0, out1, stream=None):
+    """X W (or X W^T) with bias, GeLU or GeLU' and residual in its epilogue."""
+    _check(LIB.zb_linear_product(C.byref(g), _ptr(X), _ptr(W), _ptr(bias), _ptr(R), _ptr(H), _ptr(out0),
+                                 _ptr(out1), _stream(stream)), "zb_linear_product")
+
+
+def make_layernorm(rows: int, width: int, dtype: int = ZB_DT_BF16, eps: float = 1e-5) -> zb_layernorm:
+    return zb_layernorm(rows, width, eps, dtype)
+
+
+def zb_layernorm_forward(n, X, gamma, beta, Y, mean, rstd, stream=None):
+    _check(LIB.zb_layernorm_forward(C.byref(n), _ptr(X), _ptr(gamma), _ptr(beta), _ptr(Y), _ptr(mean), _ptr(rstd),
+                                    _stream(stream)), "zb_layernorm_forward")
+
+
+def zb_layernorm_backward_input(n, dY, X, gamma, mean, rstd, dR, dX, dX16, stream=None):
+    """dX of the norm, plus the residual's gradient dR; dX16: the same in bf16."""
+    _check(LIB.zb_layernorm_backward_input(C.byref(n), _ptr(dY), _ptr(X), _ptr(gamma), _ptr(mean), _ptr(rstd),
+                                           _ptr(dR), _ptr(dX), _ptr(dX16), _stream(stream)),
+           "zb_layernorm_backward_input")
+
+
+def zb_layernorm_backward_weight(n, dY, X, mean, rstd, dgamma, dbeta, accumulate, stream=None):
+    _check(LIB.zb_layernorm_backward_weight(C.byref(n), _ptr(dY), _ptr(X), _ptr(mean), _ptr(rstd), _ptr(dgamma),
+                                            _ptr(dbeta), 1 if accumulate else 0, _stream(stream)),
+           "zb_layernorm_backward_weight")
+
+
+def make_embedding(tokens: int, vocab: int, width: int, dtype: int = ZB_DT_BF16, scale: float = 1.0) -> zb_embedding:
+    return zb_embedding(tokens, vocab, width, scale, dtype)
+
+
+def zb_embedding_workspace_bytes(e) -> int:
+    return LIB.zb_embedding_workspace_bytes(C.byref(e))
+
+
+def zb_embedding_forward(e, ids, E, Y, stream=None):
+    _check(LIB.zb_embedding_forward(C.byref(e), _ptr(ids), _ptr(E), _ptr(Y), _stream(stream)), "zb_embedding_forward")
+
+
+def zb_embedding_sort(e, ids, order, sorted_id, workspace, ws_bytes, stream=None):
+    """The tokens in ascending order of (id, token), ids outside the table last."""
+    _check(LIB.zb_embedding_sort(C.byref(e), _ptr(ids), _ptr(order), _ptr(sorted_id), _ptr(workspace), ws_bytes,
+                                 _stream(stream)), "zb_embedding_sort")
+
+
+def zb_embedding_backward(e, order, sorted_id, dY, dE, accumulate, workspace, ws_bytes, stream=None):
+    _check(LIB.zb_embedding_backward(C.byref(e), _ptr(order), _ptr(sorted_id), _ptr(dY), _ptr(dE),
+                                     1 if accumulate else 0, _ptr(workspace), ws_bytes, _stream(stream)),
+           "zb_embedding_backward")
 
 
 def zb_sync_status(stream=None):
