@@ -1,66 +1,820 @@
 // linear.cu — a linear map with its epilogue: D = X W (or X W^T) with bias,
-// GeLU or GeLU', and a residual.
+// GeLU or GeLU', and a residual (zb_linear_product).
+//
+// Two kernels, by the number of output tiles (see use_rows):
+//   zb_linear_tiles_kernel  persistent CTA pairs over 256 x 256 tiles, for
+//                           problems that fill the GPU with them;
+//   zb_linear_rows_kernel   one 128-column tile of few rows a cluster, whose
+//                           CTAs split K, for the others.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <atomic>
 #include <string>
 
-#include "gemm_core.cuh"
+#include "grouped.cuh"
 
 namespace {
 
+enum Form { STORE = 0, GELU = 1, GRAD = 2, STORE32 = 3 };
+
 struct LinearArgs {
-    const __nv_bfloat16 *X, *W, *bias, *H;
+    const __nv_bfloat16 *bias, *H;
     const void* R;
-    void *out0, *out1;
-    long long ldx, ldr, ldh, ldo, sk, sn;  // sk, sn: strides of W along K and N
-    int M, N, K, epilogue, tanh_form, f32;
+    void *out0, *out1;  // out1: GELU's output
+    long long ldr, ldh, ldo;
+    int M, N, K;
+    int save, tanh_form;
+    int hint_a, hint_b, hint_out;  // L2 priorities of the copies (choose_l2_hints)
+    int tiles_n, split;            // rows kernel: column tiles, CTAs along K
+    int stages;                    // rows kernel: of the ring
+    unsigned int* err;
 };
 
-// 64 x 64 outputs a block, 16 along K at a time, 4 x 4 a thread.
-__global__ void __launch_bounds__(256) zb_linear_simple_kernel(const LinearArgs a) {
-    __shared__ float xs[16][65], ws[16][65];
-    const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 64;
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    float acc[4][4] = {};
-    for (int k0 = 0; k0 < a.K; k0 += 16) {
-        for (int i = threadIdx.x; i < 64 * 16; i += 256) {
-            const int r = i / 16, k = i % 16;
-            xs[k][r] = m0 + r < a.M && k0 + k < a.K ? __bfloat162float(a.X[(m0 + r) * a.ldx + k0 + k]) : 0.0f;
-            ws[k][r] = n0 + r < a.N && k0 + k < a.K ? __bfloat162float(a.W[(k0 + k) * a.sk + (n0 + r) * a.sn]) : 0.0f;
+// GeLU of N values in place (an even number of them), in fp32.
+template <bool TANH, int N>
+__device__ __forceinline__ void gelu_values(float (&x)[N]) {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        if (TANH) {
+            x[2 * i] = gelu_t<true>(x[2 * i]);
+            x[2 * i + 1] = gelu_t<true>(x[2 * i + 1]);
+        } else {
+            const f32x2 X = pk2(x[2 * i], x[2 * i + 1]);
+            f32x2 PHI, E;
+            normal_cdf_and_exp2(X, PHI, E);
+            up2(mul2(X, PHI), x[2 * i], x[2 * i + 1]);
         }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < 16; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(xs[k][ty * 4 + i], ws[k][tx * 4 + j], acc[i][j]);
-        __syncthreads();
     }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const long long r = m0 + ty * 4 + i;
-            const int n = n0 + tx * 4 + j;
-            if (r >= a.M || n >= a.N) continue;
-            float d = acc[i][j] + (a.bias ? __bfloat162float(a.bias[n]) : 0.0f);
-            void* out = a.out0;
-            if (a.epilogue == ZB_LINEAR_GELU) {
-                if (a.out0) static_cast<__nv_bfloat16*>(a.out0)[r * a.ldo + n] = __float2bfloat16(d);
-                d = a.tanh_form ? gelu_t<true>(d) : gelu_t<false>(d);
-                out = a.out1;
-            } else if (a.epilogue == ZB_LINEAR_GELU_GRAD) {
-                const float h = __bfloat162float(a.H[r * a.ldh + n]);
-                d *= a.tanh_form ? gelu_grad_t<true>(h) : gelu_grad_t<false>(h);
-            }
-            if (a.f32) {
-                if (a.R) d += static_cast<const float*>(a.R)[r * a.ldr + n];
-                static_cast<float*>(out)[r * a.ldo + n] = d;
-            } else {
-                if (a.R) d += __bfloat162float(static_cast<const __nv_bfloat16*>(a.R)[r * a.ldr + n]);
-                static_cast<__nv_bfloat16*>(out)[r * a.ldo + n] = __float2bfloat16(d);
+}
+
+// ---------------------------------------------------------------- large problems
+// The roles of the dense kernel (gemm_tc.cu) on CTA pairs: warp 0 copies, warp
+// 1 of the even CTA issues 256 x 256 MMAs into one of two accumulators, warps
+// 2-9 drain (a TMEM lane is a row, a warp has 32 rows x 128 columns in chunks of
+// 32).  The residual comes by TMA into the staging box that the chunk's results
+// then leave from: a thread adds its row's values and writes the sums back to
+// where they lay.  So its bytes cost no registers and no waiting loads, and an
+// output that is the residual itself needs no care (each of its elements is read
+// and written by one warp, in this order).  H is loaded a chunk ahead.
+//
+// fp32 outputs (STORE32): the tensor core cuts off low bits as it adds, so the
+// accumulators take SEG blocks of K each and the epilogue adds them in registers,
+// rounding to nearest, as the experts' W does (grouped.cu has both sides' errors).
+template <int FORM>
+struct TileCfg {
+    static constexpr bool F32 = FORM == STORE32;
+    static constexpr int SEG = 8;                            // F32: blocks of 64 along K an accumulator takes
+    static constexpr int STAGES = 5;                         // of 32 KiB: 16 of X, 16 of W
+    static constexpr int BOXES = F32 ? 2 : 4;                // staging boxes a warp
+    static constexpr uint32_t BOX = F32 ? 32 * 128 : 32 * 64;  // 32 rows x 32 columns
+};
+constexpr int TILE_WARPS = 8;
+constexpr uint32_t T_STAGE = Cfg<2>::STAGE_BYTES;
+
+struct TileCtl {
+    uint64_t full[6], empty[6], tfull[2], tempty[2], drain;
+    uint64_t rbar[TILE_WARPS][4];  // a residual box has landed
+    uint32_t tmem_base;
+    int abort_flag;
+};
+template <int FORM>
+constexpr size_t tile_smem() {
+    return 1024 + TileCfg<FORM>::STAGES * T_STAGE + TILE_WARPS * TileCfg<FORM>::BOXES * TileCfg<FORM>::BOX + sizeof(TileCtl);
+}
+static_assert(tile_smem<STORE>() <= 232448 && tile_smem<STORE32>() <= 232448, "shared memory");
+
+template <int FORM, int W_MN>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    zb_linear_tiles_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                           const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmH,
+                           const __grid_constant__ CUtensorMap tmR, const LinearArgs args) {
+    using T = TileCfg<FORM>;
+    constexpr int STAGES = T::STAGES, SEG = T::SEG;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t* staging = smem + STAGES * T_STAGE;
+    TileCtl* ctl = reinterpret_cast<TileCtl*>(staging + TILE_WARPS * T::BOXES * T::BOX);
+
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t rank = zbp::cluster_ctarank();
+    const bool leader = rank == 0;
+    const int cluster = blockIdx.x / 2, clusters = gridDim.x / 2;
+    const int tiles_m = (args.M + 255) / 256, tiles_n = (args.N + BN - 1) / BN, num_tiles = tiles_m * tiles_n;
+    const int num_kb = (args.K + BK - 1) / BK;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            zbp::mbar_init(zbp::smem_u32(&ctl->full[s]), 1);
+            zbp::mbar_init(zbp::smem_u32(&ctl->empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            zbp::mbar_init(zbp::smem_u32(&ctl->tfull[b]), 1);
+            zbp::mbar_init(zbp::smem_u32(&ctl->tempty[b]), 2 * TILE_WARPS);
+        }
+        zbp::mbar_init(zbp::smem_u32(&ctl->drain), 1);
+        for (int w = 0; w < TILE_WARPS; ++w)
+            for (int b = 0; b < 4; ++b) zbp::mbar_init(zbp::smem_u32(&ctl->rbar[w][b]), 1);
+        ctl->abort_flag = 0;
+        zbp::fence_mbar_init();
+        zbp::tma_prefetch_desc(&tmX);
+        zbp::tma_prefetch_desc(&tmW);
+        zbp::tma_prefetch_desc(&tmO);
+        if (args.R) zbp::tma_prefetch_desc(&tmR);
+        if (FORM == GELU && args.save) zbp::tma_prefetch_desc(&tmH);
+    }
+    if (warp == 1) {
+        zbp::tmem_alloc_pair(zbp::smem_u32(&ctl->tmem_base), TMEM_COLS);
+        zbp::tmem_relinquish_pair();
+    }
+    zbp::tc_fence_before();
+    __syncthreads();
+    zbp::cluster_sync();
+    zbp::tc_fence_after();
+    const uint32_t tmem_base = ctl->tmem_base;
+    volatile int* abort_flag = &ctl->abort_flag;
+    zbp::grid_dependency_wait();
+    zbp::allow_dependent_launch();
+
+    if (warp == 0) {
+        // ---------------------------------------------------- TMA producer
+        const uint32_t full0 = zbp::smem_u32(&ctl->full[0]), empty0 = zbp::smem_u32(&ctl->empty[0]);
+        const uint32_t full0_lead = zbp::mapa_shared(full0, 0), sa0 = zbp::smem_u32(smem);
+        const uint64_t pol_x = zbp::l2_policy(args.hint_a), pol_w = zbp::l2_policy(args.hint_b);
+        uint32_t s = 0, sp = 1, it = 0;  // stage and the phase of its last release; stages filled
+        bool ok = true;
+        for (int tile = cluster; tile < num_tiles && ok; tile += clusters) {
+            int mb, nb;
+            tile_coords(tile, tiles_m, tiles_n, Cfg<2>::GROUP_M, mb, nb);
+            const int m0 = mb * 256 + static_cast<int>(rank) * BM;
+            const int n0 = nb * BN + static_cast<int>(rank) * 128;
+            for (int kb = 0; kb < num_kb; ++kb, ++it) {
+                if (!wait_bar<false>(empty0 + s * 8u, sp, abort_flag, args.err, ERR_WAIT_PRODUCER, WAIT_LIMIT_NS, true)) {
+                    ok = false;
+                    break;
+                }
+                if (zbp::elect_one()) {
+                    const uint32_t full = full0_lead + s * 8u, sa = sa0 + s * T_STAGE, sb = sa + A_BYTES;
+                    const int k0 = kb * BK;
+                    if (leader) zbp::mbar_arrive_expect_tx(full0 + s * 8u, 2 * T_STAGE);
+                    zbp::tma_load_2d_pair_hint(sa, &tmX, full, k0, m0, pol_x);
+                    if (W_MN) {
+                        zbp::tma_load_2d_pair_hint(sb, &tmW, full, n0, k0, pol_w);
+                        zbp::tma_load_2d_pair_hint(sb + MN_ATOM_BYTES, &tmW, full, n0 + 64, k0, pol_w);
+                    } else {
+                        zbp::tma_load_2d_pair_hint(sb, &tmW, full, k0, n0, pol_w);
+                    }
+                }
+                __syncwarp();
+                if (++s == STAGES) {
+                    s = 0;
+                    sp ^= 1u;
+                }
             }
         }
+        if (!ok && leader) {
+            // wait for the copies that were issued but may not have landed
+            const uint32_t first = it > STAGES ? it - STAGES : 0;
+            for (uint32_t i = first; i < it; ++i)
+                wait_bar<false>(full0 + (i % STAGES) * 8u, (i / STAGES) & 1u, abort_flag, args.err, ERR_WAIT_PRODUCER,
+                                DRAIN_LIMIT_NS, false);
+        }
+    } else if (warp == 1) {
+        if (leader) {
+            // ------------------------------------------------ MMA issuer
+            constexpr uint32_t idesc = zbp::idesc_bf16_f32(256, BN, 0, W_MN);
+            constexpr uint32_t W_STEP = W_MN ? 2048 >> 4 : 32 >> 4, hi = zbp::desc_hi(1024);
+            const uint32_t a0 = zbp::desc_lo(zbp::smem_u32(smem), 16);
+            const uint32_t b0 = zbp::desc_lo(zbp::smem_u32(smem) + A_BYTES, W_MN ? MN_ATOM_BYTES : 16);
+            const uint32_t full0 = zbp::smem_u32(&ctl->full[0]), empty0 = zbp::smem_u32(&ctl->empty[0]);
+            uint32_t s = 0, sp = 0, local = 0;  // stage and its phase; accumulators filled
+            bool ok = true;
+            for (int tile = cluster; tile < num_tiles && ok; tile += clusters) {
+                for (int kb0 = 0; kb0 < num_kb && ok; kb0 += T::F32 ? SEG : num_kb) {
+                    const uint32_t buf = local & 1u, tr = local >> 1;
+                    ++local;
+                    if (!wait_bar<false>(zbp::smem_u32(&ctl->tempty[buf]), (tr & 1u) ^ 1u, abort_flag, args.err,
+                                         ERR_WAIT_MMA, WAIT_LIMIT_NS, true)) {
+                        ok = false;
+                        break;
+                    }
+                    zbp::tc_fence_after();
+                    const uint32_t d_tmem = tmem_base + buf * ACC_COLS;
+                    const int kb1 = T::F32 ? min(kb0 + SEG, num_kb) : num_kb;
+                    for (int kb = kb0; kb < kb1; ++kb) {
+                        if (!wait_bar<false>(full0 + s * 8u, sp, abort_flag, args.err, ERR_WAIT_MMA, WAIT_LIMIT_NS, true)) {
+                            ok = false;
+                            break;
+                        }
+                        zbp::tc_fence_after();
+                        if (zbp::elect_one()) {
+                            const uint32_t off = s * (T_STAGE >> 4);
+                            zbp::mma4_f16_pair<2, W_STEP>(d_tmem, a0 + off, hi, b0 + off, hi, idesc, kb != kb0);
+                            zbp::tc_commit_pair_multicast(empty0 + s * 8u, 0x3);
+                            if (kb + 1 == kb1) zbp::tc_commit_pair_multicast(zbp::smem_u32(&ctl->tfull[buf]), 0x3);
+                        }
+                        __syncwarp();
+                        if (++s == STAGES) {
+                            s = 0;
+                            sp ^= 1u;
+                        }
+                    }
+                }
+            }
+            // every MMA issued here completes before TMEM is released
+            if (zbp::elect_one()) zbp::tc_commit_pair(zbp::smem_u32(&ctl->drain));
+            __syncwarp();
+            wait_bar<false>(zbp::smem_u32(&ctl->drain), 0, abort_flag, args.err, ERR_WAIT_MMA, DRAIN_LIMIT_NS, false);
+        }
+    } else {
+        // ---------------------------------------------------- epilogue
+        constexpr int CH = 4;  // chunks of 32 columns a warp
+        const int ew = warp - 2, q = warp & 3, c_lo = (ew >> 2) * 128;
+        const uint32_t stg0 = zbp::smem_u32(staging) + static_cast<uint32_t>(ew) * T::BOXES * T::BOX;
+        const uint32_t rbar0 = zbp::smem_u32(&ctl->rbar[ew][0]);
+        const uint64_t pol_out = zbp::l2_policy(args.hint_out);
+        const bool res = args.R != nullptr;
+        const int per = FORM == GELU && args.save ? 2 : 1;  // boxes a chunk leaves by
+        // chunks whose residual is asked for ahead: the box must have been read
+        // out by the store that left from it
+        const int ahead = T::BOXES / per / 2;
+        uint32_t local = 0;
+        uint32_t g = 0;                  // boxes used so far
+        uint32_t asked = 0, phases = 0;  // a bit a box: residual on its way or landed; phase of its barrier
+        bool ok = true;
+        for (int tile = cluster; tile < num_tiles && ok; tile += clusters) {
+            int mb, nb;
+            tile_coords(tile, tiles_m, tiles_n, Cfg<2>::GROUP_M, mb, nb);
+            const int row0 = mb * 256 + static_cast<int>(rank) * BM + q * 32, row = row0 + lane;
+            const int n0 = nb * BN + c_lo;  // first column of this warp
+            const bool rows_live = row0 < args.M;
+            const int chunks = rows_live ? min(CH, max(0, (args.N - n0 + 31) / 32)) : 0;
+            const uint32_t g0 = g;
+            auto ask = [&](int c) {  // residual of chunk c into the box its results will leave by
+                const uint32_t b = (g0 + static_cast<uint32_t>(c * per + per - 1)) % T::BOXES;
+                if (lane == 0) {
+                    zbp::mbar_arrive_expect_tx(rbar0 + b * 8u, T::BOX);
+                    zbp::tma_load_2d(stg0 + b * T::BOX, &tmR, rbar0 + b * 8u, n0 + c * 32, row0);
+                }
+                asked |= 1u << b;
+            };
+            if (res && chunks > 0) {
+                // the boxes used in the last chunk may still be read, those before not
+                if (lane == 0) {
+                    if (ahead > 1)
+                        zbp::bulk_wait_read<2>();
+                    else
+                        zbp::bulk_wait_read<0>();
+                }
+                __syncwarp();
+                for (int c = 0; c < min(ahead, chunks); ++c) ask(c);
+                const int ncols = min(128, args.N - n0);
+                if (row < args.M)
+                    zbp::prefetch_l2(static_cast<const uint8_t*>(args.R) +
+                                         (static_cast<long long>(row) * args.ldr + n0) * (T::F32 ? 4 : 2),
+                                     static_cast<uint32_t>(ncols) * (T::F32 ? 4u : 2u));
+            }
+            uint32_t h_next[16];
+            auto load_h = [&](int col0) {
+                const __nv_bfloat16* hp = args.H + static_cast<long long>(row) * args.ldh + col0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                    if (row < args.M && col0 + 8 * i < args.N) v = *reinterpret_cast<const uint4*>(hp + 8 * i);
+                    h_next[4 * i] = v.x;
+                    h_next[4 * i + 1] = v.y;
+                    h_next[4 * i + 2] = v.z;
+                    h_next[4 * i + 3] = v.w;
+                }
+            };
+            if (FORM == GRAD && chunks > 0) {
+                if (row < args.M)
+                    zbp::prefetch_l2(args.H + static_cast<long long>(row) * args.ldh + n0,
+                                     static_cast<uint32_t>(min(128, args.N - n0)) * 2u);
+                load_h(n0);
+            }
+            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(c_lo);
+            float acc[T::F32 ? CH : 1][32];
+            uint32_t buf = 0;
+            // the accumulators' parts (bf16 outputs have one, read chunk by chunk below)
+            for (int kb0 = 0; kb0 < num_kb; kb0 += T::F32 ? SEG : num_kb) {
+                buf = local & 1u;
+                const uint32_t tr = local >> 1;
+                ++local;
+                if (!wait_bar<false>(zbp::smem_u32(&ctl->tfull[buf]), tr & 1u, abort_flag, args.err, ERR_WAIT_EPI,
+                                    WAIT_LIMIT_NS, true)) {
+                    ok = false;
+                    break;
+                }
+                zbp::tc_fence_after();
+                if constexpr (T::F32) {
+#pragma unroll
+                    for (int c = 0; c < CH; ++c) {
+                        uint32_t v[32];
+                        zbp::tmem_ld_32x32b_x32(taddr + buf * ACC_COLS + c * 32, v);
+                        zbp::tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            acc[c][i] = kb0 == 0 ? __uint_as_float(v[i]) : acc[c][i] + __uint_as_float(v[i]);
+                    }
+                    zbp::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) zbp::mbar_arrive_remote(zbp::mapa_shared(zbp::smem_u32(&ctl->tempty[buf]), 0));
+                }
+            }
+            if (!ok) break;
+            auto box_of = [&](uint32_t use) { return stg0 + (use % T::BOXES) * T::BOX; };
+            auto chunk = [&](int c, float (&x)[32]) {
+                const int col0 = n0 + c * 32;
+                if (res && c + ahead < chunks) {
+                    // the box that chunk's results will leave by was used `BOXES` boxes before
+                    if (lane == 0) {
+                        if (ahead > 1)
+                            zbp::bulk_wait_read<1>();
+                        else
+                            zbp::bulk_wait_read<0>();
+                    }
+                    __syncwarp();
+                    ask(c + ahead);
+                }
+                if (args.bias && FORM != GRAD) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (col0 + i * 8 >= args.N) break;
+                        const uint4 b = *reinterpret_cast<const uint4*>(args.bias + col0 + i * 8);
+                        const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 f2 = unpack_bf16x2(bw[j]);
+                            x[i * 8 + 2 * j] += f2.x;
+                            x[i * 8 + 2 * j + 1] += f2.y;
+                        }
+                    }
+                }
+                uint32_t w[16];
+                if (FORM == GELU && per == 2) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+                    const uint32_t stg = box_of(g++);
+                    if (lane == 0) zbp::bulk_wait_read<T::BOXES - 1>();
+                    __syncwarp();
+                    stage_row64(stg, lane, w);
+                    staging_release<false>(&tmH, stg, lane, col0, row0, pol_out);
+                }
+                if (FORM == GELU) {
+                    if (args.tanh_form)
+                        gelu_values<true, 32>(x);
+                    else
+                        gelu_values<false, 32>(x);
+                }
+                const uint32_t b = g % T::BOXES, stg = box_of(g);
+                ++g;
+                if (res) {
+                    if (!wait_bar<false>(rbar0 + b * 8u, (phases >> b) & 1u, abort_flag, args.err, ERR_WAIT_EPI,
+                                        WAIT_LIMIT_NS, true)) {
+                        ok = false;
+                        return;
+                    }
+                    phases ^= 1u << b;
+                    asked &= ~(1u << b);
+                    if (T::F32) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float4 r = zbp::ld_shared_v4(stg + static_cast<uint32_t>(lane * 128 + ((k ^ (lane & 7)) << 4)));
+                            x[4 * k] += r.x;
+                            x[4 * k + 1] += r.y;
+                            x[4 * k + 2] += r.z;
+                            x[4 * k + 3] += r.w;
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float4 r =
+                                zbp::ld_shared_v4(stg + static_cast<uint32_t>(lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)));
+                            const float4 rr[1] = {r};
+                            const uint32_t* rw = reinterpret_cast<const uint32_t*>(rr);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const float2 f2 = unpack_bf16x2(rw[j]);
+                                x[8 * k + 2 * j] += f2.x;
+                                x[8 * k + 2 * j + 1] += f2.y;
+                            }
+                        }
+                    }
+                } else {
+                    if (lane == 0) zbp::bulk_wait_read<T::BOXES - 1>();
+                    __syncwarp();
+                }
+                if constexpr (T::F32) {
+                    uint32_t o[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(x[i]);
+                    stage_row(stg, lane, o);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+                    stage_row64(stg, lane, w);
+                }
+                staging_release<false>(&tmO, stg, lane, col0, row0, pol_out);
+            };
+            if constexpr (T::F32) {
+#pragma unroll
+                for (int c = 0; c < CH; ++c)
+                    if (c < chunks && ok) chunk(c, acc[c]);
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < chunks && ok; ++c) {
+                    uint32_t hw[16];
+                    if (FORM == GRAD) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) hw[i] = h_next[i];
+                        if (c + 1 < chunks) load_h(n0 + c * 32 + 32);
+                    }
+                    uint32_t v[32];
+                    zbp::tmem_ld_32x32b_x32(taddr + buf * ACC_COLS + c * 32, v);
+                    zbp::tmem_ld_wait();
+                    float x[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(v[i]);
+                    if (FORM == GRAD) {
+                        if (args.tanh_form)
+                            gelu_grad_mul<true, 32>(x, hw);
+                        else
+                            gelu_grad_mul<false, 32>(x, hw);
+                    }
+                    chunk(c, x);
+                }
+                zbp::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) zbp::mbar_arrive_remote(zbp::mapa_shared(zbp::smem_u32(&ctl->tempty[buf]), 0));
+            }
+            // the boxes of chunks outside the matrix: empty groups, so that groups count boxes
+            for (int c = chunks; c < CH; ++c)
+                for (int i = 0; i < per; ++i, ++g)
+                    if (lane == 0) zbp::bulk_commit();
+        }
+        // residuals asked for and not used (after an abort)
+        for (uint32_t b = 0; b < static_cast<uint32_t>(T::BOXES); ++b)
+            if ((asked >> b) & 1u)
+                wait_bar<false>(rbar0 + b * 8u, (phases >> b) & 1u, abort_flag, args.err, ERR_WAIT_EPI, DRAIN_LIMIT_NS, false);
+        // the staging boxes must not be released while a bulk store reads them
+        if (lane == 0) zbp::bulk_wait<0>();
+        __syncwarp();
+    }
+
+    __syncthreads();
+    zbp::cluster_sync();  // no remote arrivals or copies remain
+    if (warp == 1) {
+        zbp::tc_fence_after();
+        zbp::tmem_dealloc_pair(tmem_base, TMEM_COLS);
+    }
+}
+
+// ---------------------------------------------------------------- few tiles
+// One tile of ROWS rows x 128 columns a cluster of `split` CTAs, which share its K
+// range.  The product is transposed (as in grouped.cu): the weight's columns are
+// the MMA's M side, the rows its N side, so a few rows cost little more than
+// streaming the weight, and the split lets as many SMs stream it as there are.
+// Each CTA leaves its fp32 partial tile in its own shared memory (its ring, idle
+// by then), [row][column]; after a cluster barrier CTA r adds the partials of the
+// r-th part of the rows through distributed shared memory, in the order of the
+// CTAs (so the same inputs give the same bits), applies the epilogue and stores.
+//
+// At least R_SMEM of shared memory are asked for whatever the ring needs, so that
+// an SM holds one CTA: two CTAs of different clusters on an SM could each wait for
+// the other's tensor memory while their own clusters wait for them.
+//
+// fp32 outputs: an accumulator takes SEG blocks of K, as above; here each part has
+// tensor memory of its own (as far as it reaches: 512 columns / ROWS).
+constexpr int R_THREADS = NUM_THREADS;
+constexpr int R_STAGES = 10;
+constexpr int R_MIN_KB = 2;  // blocks of K a CTA, at least
+constexpr uint32_t R_SMEM = 120 * 1024;
+constexpr uint32_t R_W_BYTES = 128 * BK * 2;
+constexpr uint32_t rows_stage(int rows) { return R_W_BYTES + static_cast<uint32_t>(rows) * BK * 2; }
+
+struct RowsCtl {
+    uint64_t full[R_STAGES], empty[R_STAGES], tfull, drain;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+// The epilogue of 4 consecutive columns of a row (all inside the matrix).
+template <int FORM>
+__device__ __forceinline__ void finish4(const LinearArgs& a, long long row, int col, float (&x)[4]) {
+    auto four = [](const __nv_bfloat16* p, float (&v)[4]) {
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        const float2 lo = unpack_bf16x2(u.x), hi = unpack_bf16x2(u.y);
+        v[0] = lo.x;
+        v[1] = lo.y;
+        v[2] = hi.x;
+        v[3] = hi.y;
+    };
+    auto put = [](void* p, long long at, const float (&v)[4]) {
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p) + at) =
+            make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    };
+    if (FORM != GRAD && a.bias) {
+        float b[4];
+        four(a.bias + col, b);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] += b[i];
+    }
+    if (FORM == GELU) {
+        if (a.save) put(a.out0, row * a.ldo + col, x);
+        if (a.tanh_form)
+            gelu_values<true, 4>(x);
+        else
+            gelu_values<false, 4>(x);
+    }
+    if (FORM == GRAD) {
+        const uint2 u = *reinterpret_cast<const uint2*>(a.H + row * a.ldh + col);
+        const uint32_t h[2] = {u.x, u.y};
+        if (a.tanh_form)
+            gelu_grad_mul<true, 4>(x, h);
+        else
+            gelu_grad_mul<false, 4>(x, h);
+    }
+    if (FORM == STORE32) {
+        if (a.R) {
+            const float4 r = *reinterpret_cast<const float4*>(static_cast<const float*>(a.R) + row * a.ldr + col);
+            x[0] += r.x;
+            x[1] += r.y;
+            x[2] += r.z;
+            x[3] += r.w;
+        }
+        *reinterpret_cast<float4*>(static_cast<float*>(a.out0) + row * a.ldo + col) = make_float4(x[0], x[1], x[2], x[3]);
+    } else {
+        if (a.R) {
+            float r[4];
+            four(static_cast<const __nv_bfloat16*>(a.R) + row * a.ldr + col, r);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] += r[i];
+        }
+        put(FORM == GELU ? a.out1 : a.out0, row * a.ldo + col, x);
+    }
+}
+
+template <int FORM, int W_MN, int ROWS>
+__global__ void __launch_bounds__(R_THREADS, 1)
+    zb_linear_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                          const LinearArgs args) {
+    constexpr uint32_t STAGE = rows_stage(ROWS);
+    constexpr int SEG = 8, PARTS = FORM == STORE32 ? 512 / ROWS : 1;  // accumulators, at most
+    constexpr uint32_t TMEM = PARTS * ROWS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    __shared__ RowsCtl ctl_shared;
+    RowsCtl* ctl = &ctl_shared;
+
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int split = args.split, stages = args.stages;
+    const int rank = split > 1 ? static_cast<int>(zbp::cluster_ctarank()) : 0;
+    const int tile = blockIdx.x / split;
+    const int mb = tile / args.tiles_n, n0 = (tile - mb * args.tiles_n) * 128;
+    const int m0 = mb * ROWS, live = min(ROWS, args.M - m0);
+    const int num_kb_all = (args.K + BK - 1) / BK;
+    const int kb0 = static_cast<int>(static_cast<long long>(num_kb_all) * rank / split);
+    const int num_kb = static_cast<int>(static_cast<long long>(num_kb_all) * (rank + 1) / split) - kb0;
+    // accumulators, and blocks of K in each
+    const int parts = min(PARTS, (num_kb + SEG - 1) / SEG), seg = (num_kb + parts - 1) / parts;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) {
+            zbp::mbar_init(zbp::smem_u32(&ctl->full[s]), 1);
+            zbp::mbar_init(zbp::smem_u32(&ctl->empty[s]), 1);
+        }
+        zbp::mbar_init(zbp::smem_u32(&ctl->tfull), 1);
+        zbp::mbar_init(zbp::smem_u32(&ctl->drain), 1);
+        ctl->abort_flag = 0;
+        zbp::fence_mbar_init();
+        zbp::tma_prefetch_desc(&tmX);
+        zbp::tma_prefetch_desc(&tmW);
+    }
+    if (warp == 1) {
+        zbp::tmem_alloc(zbp::smem_u32(&ctl->tmem_base), TMEM);
+        zbp::tmem_relinquish();
+    }
+    zbp::tc_fence_before();
+    __syncthreads();
+    zbp::tc_fence_after();
+    const uint32_t tmem_base = ctl->tmem_base;
+    volatile int* abort_flag = &ctl->abort_flag;
+    zbp::grid_dependency_wait();
+    zbp::allow_dependent_launch();
+
+    const uint32_t ring = zbp::smem_u32(smem);
+    const uint32_t full0 = zbp::smem_u32(&ctl->full[0]), empty0 = zbp::smem_u32(&ctl->empty[0]);
+    if (warp == 0) {
+        // ---------------------------------------------------- TMA producer
+        int s = 0;
+        uint32_t sp = 1, it = 0;
+        bool ok = true;
+        for (int kb = 0; kb < num_kb; ++kb, ++it) {
+            if (!wait_bar<false>(empty0 + static_cast<uint32_t>(s) * 8u, sp, abort_flag, args.err, ERR_WAIT_PRODUCER,
+                                WAIT_LIMIT_NS, true)) {
+                ok = false;
+                break;
+            }
+            if (zbp::elect_one()) {
+                const uint32_t full = full0 + static_cast<uint32_t>(s) * 8u;
+                const uint32_t sa = ring + static_cast<uint32_t>(s) * STAGE, sb = sa + R_W_BYTES;
+                const int k0 = (kb0 + kb) * BK;
+                zbp::mbar_arrive_expect_tx(full, STAGE);
+                if (W_MN) {
+                    zbp::tma_load_2d(sa, &tmW, full, n0, k0);
+                    zbp::tma_load_2d(sa + MN_ATOM_BYTES, &tmW, full, n0 + 64, k0);
+                } else {
+                    zbp::tma_load_2d(sa, &tmW, full, k0, n0);
+                }
+                zbp::tma_load_2d(sb, &tmX, full, k0, m0);
+            }
+            __syncwarp();
+            if (++s == stages) {
+                s = 0;
+                sp ^= 1u;
+            }
+        }
+        if (!ok) {
+            // wait for the copies that were issued but may not have landed
+            const uint32_t n = static_cast<uint32_t>(stages), first = it > n ? it - n : 0;
+            for (uint32_t i = first; i < it; ++i)
+                wait_bar<false>(full0 + (i % n) * 8u, (i / n) & 1u, abort_flag, args.err, ERR_WAIT_PRODUCER,
+                                DRAIN_LIMIT_NS, false);
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------------- MMA issuer
+        constexpr uint32_t idesc = zbp::idesc_bf16_f32(128, ROWS, W_MN, 0);
+        constexpr uint32_t W_STEP = W_MN ? 2048 >> 4 : 32 >> 4, hi = zbp::desc_hi(1024);
+        const uint32_t a0 = zbp::desc_lo(ring, W_MN ? MN_ATOM_BYTES : 16), b0 = zbp::desc_lo(ring + R_W_BYTES, 16);
+        int s = 0;
+        uint32_t sp = 0, d_tmem = tmem_base;
+        int in_part = 0;
+        for (int kb = 0; kb < num_kb; ++kb) {
+            if (!wait_bar<false>(full0 + static_cast<uint32_t>(s) * 8u, sp, abort_flag, args.err, ERR_WAIT_MMA,
+                                WAIT_LIMIT_NS, true))
+                break;
+            zbp::tc_fence_after();
+            if (zbp::elect_one()) {
+                const uint32_t off = static_cast<uint32_t>(s) * (STAGE >> 4);
+                zbp::mma4_f16<W_STEP, 2>(d_tmem, a0 + off, hi, b0 + off, hi, idesc, in_part != 0);
+                zbp::tc_commit(empty0 + static_cast<uint32_t>(s) * 8u);
+                if (kb + 1 == num_kb) zbp::tc_commit(zbp::smem_u32(&ctl->tfull));
+            }
+            __syncwarp();
+            if (++in_part == seg) {
+                in_part = 0;
+                d_tmem += ROWS;
+            }
+            if (++s == stages) {
+                s = 0;
+                sp ^= 1u;
+            }
+        }
+        // every MMA issued here completes before TMEM is released
+        if (zbp::elect_one()) zbp::tc_commit(zbp::smem_u32(&ctl->drain));
+        __syncwarp();
+        wait_bar<false>(zbp::smem_u32(&ctl->drain), 0, abort_flag, args.err, ERR_WAIT_MMA, DRAIN_LIMIT_NS, false);
+    } else {
+        // ---------------------------------------------------- partial tile to shared memory
+        const int q = warp & 3, hf = (warp - 2) >> 2;
+        if (wait_bar<false>(zbp::smem_u32(&ctl->tfull), 0, abort_flag, args.err, ERR_WAIT_EPI, WAIT_LIMIT_NS, true)) {
+            zbp::tc_fence_after();
+            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+#pragma unroll 1
+            for (int c = hf; c < ROWS / 32 && c * 32 < live; c += 2) {
+                float x[32];
+#pragma unroll 1
+                for (int p = 0; p < parts; ++p) {
+                    uint32_t v[32];
+                    zbp::tmem_ld_32x32b_x32(taddr + p * ROWS + c * 32, v);
+                    zbp::tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) x[i] = p == 0 ? __uint_as_float(v[i]) : x[i] + __uint_as_float(v[i]);
+                }
+                float* to = reinterpret_cast<float*>(smem) + c * 32 * 128 + q * 32 + lane;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) to[i * 128] = x[i];
+            }
+            zbp::tc_fence_before();
+        }
+        __syncwarp();
+    }
+
+    __syncthreads();
+    if (split > 1) zbp::cluster_sync();  // every partial is written
+    if (!*abort_flag) {
+        const int lo = live * rank / split, items = (live * (rank + 1) / split - lo) * 32;
+        for (int i = threadIdx.x; i < items; i += R_THREADS) {
+            const int r = lo + (i >> 5), c = (i & 31) * 4;
+            if (n0 + c >= args.N) continue;
+            const uint32_t at = ring + static_cast<uint32_t>(r * 512 + c * 4);
+            float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (split == 1) {
+                const float4 p = zbp::ld_shared_v4(at);
+                x[0] = p.x;
+                x[1] = p.y;
+                x[2] = p.z;
+                x[3] = p.w;
+            } else {
+                float4 p[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k < split) p[k] = zbp::ld_shared_cluster_v4(zbp::mapa_shared(at, static_cast<uint32_t>(k)));
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k < split) {
+                        x[0] += p[k].x;
+                        x[1] += p[k].y;
+                        x[2] += p[k].z;
+                        x[3] += p[k].w;
+                    }
+            }
+            finish4<FORM>(args, m0 + r, n0 + c, x);
+        }
+    }
+    __syncthreads();
+    if (split > 1) zbp::cluster_sync();  // no CTA leaves while another may still read its partial
+    if (warp == 1) {
+        zbp::tc_fence_after();
+        zbp::tmem_dealloc(tmem_base, TMEM);
+    }
+}
+
+// ---------------------------------------------------------------- host side
+template <int FORM, int W_MN>
+zb_status launch_tiles(const CUtensorMap& x, const CUtensorMap& w, const CUtensorMap& o, const CUtensorMap& h,
+                       const CUtensorMap& r, const LinearArgs& a, void* stream) {
+    static std::atomic<int> cache[64];
+    auto kern = zb_linear_tiles_kernel<FORM, W_MN>;
+    int ctas = 0;
+    const zb_status s = full_grid(kern, cache, tile_smem<FORM>(), NUM_THREADS, 2, &ctas);
+    if (s != ZB_OK) return s;
+    const long long tiles = (static_cast<long long>(a.M) + 255) / 256 * ((a.N + BN - 1) / BN);
+    LaunchCfg cfg(static_cast<int>(std::min<long long>(2 * tiles, ctas)), NUM_THREADS, tile_smem<FORM>(), 2, stream);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg.cfg, kern, x, w, o, h, r, a);
+    if (e != cudaSuccess)
+        return zb::fail(ZB_ERR_CUDA, std::string("zb_linear_product launch: ") + cudaGetErrorString(e));
+    return ZB_OK;
+}
+
+constexpr size_t rows_smem(int rows, int stages) {
+    const size_t ring = static_cast<size_t>(stages) * rows_stage(rows), tile = static_cast<size_t>(rows) * 512;
+    return std::max<size_t>(R_SMEM, 1024 + std::max(ring, tile));
+}
+
+template <int FORM, int W_MN, int ROWS>
+zb_status launch_rows(const CUtensorMap& x, const CUtensorMap& w, LinearArgs a, void* stream) {
+    auto kern = zb_linear_rows_kernel<FORM, W_MN, ROWS>;
+    constexpr int MOST = std::min(R_STAGES, static_cast<int>((220 * 1024) / rows_stage(ROWS)));
+    // co-resident clusters of 1, 2, 4 and 8 CTAs, per device
+    static std::atomic<int> cache[64][4];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+        return zb::fail(ZB_ERR_CUDA, "zb_linear_product: cudaGetDevice failed");
+    if (!cache[dev][0].load(std::memory_order_acquire)) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(rows_smem(ROWS, MOST)));
+        if (e != cudaSuccess)
+            return zb::fail(ZB_ERR_CUDA, std::string("cudaFuncSetAttribute: ") + cudaGetErrorString(e));
+        for (int i = 3; i >= 0; --i) {
+            int n = sm_count();
+            if (i > 0) {
+                cudaLaunchConfig_t cfg = {};
+                cfg.gridDim = dim3(1024);
+                cfg.blockDim = dim3(R_THREADS);
+                cfg.dynamicSmemBytes = rows_smem(ROWS, MOST);
+                cudaLaunchAttribute attr;
+                attr.id = cudaLaunchAttributeClusterDimension;
+                attr.val.clusterDim.x = 1u << i;
+                attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+                cfg.attrs = &attr;
+                cfg.numAttrs = 1;
+                if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+                    cudaGetLastError();
+                    n = 0;  // no clusters of this size
+                }
+            }
+            if (i == 0 && n <= 0) return zb::fail(ZB_ERR_CUDA, "cannot query the SM count");
+            cache[dev][i].store(n, std::memory_order_release);
+        }
+    }
+    const long long tiles = (static_cast<long long>(a.M) + ROWS - 1) / ROWS * ((a.N + 127) / 128);
+    const int num_kb = (a.K + BK - 1) / BK;
+    // as many CTAs along K as are resident at once, with at least R_MIN_KB blocks each
+    int split = 1;
+    for (int i = 1; i <= 3; ++i)
+        if (cache[dev][i].load(std::memory_order_relaxed) >= tiles && num_kb >= R_MIN_KB << i) split = 1 << i;
+    a.tiles_n = (a.N + 127) / 128;
+    a.split = split;
+    a.stages = std::min(MOST, (num_kb + split - 1) / split);
+    LaunchCfg cfg(static_cast<int>(tiles * split), R_THREADS, rows_smem(ROWS, a.stages), split, stream);
+    cfg.cfg.numAttrs = split > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg.cfg, kern, x, w, a);
+    if (e != cudaSuccess)
+        return zb::fail(ZB_ERR_CUDA, std::string("zb_linear_product launch: ") + cudaGetErrorString(e));
+    return ZB_OK;
 }
 
 bool mis16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
@@ -69,6 +823,45 @@ bool mis16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; 
 bool stride(int64_t* ld, int64_t width) {
     if (*ld == 0) *ld = width;
     return *ld >= width && *ld <= (1LL << 30);
+}
+
+// The rows kernel where 128 x 128 tiles fit on the SMs at once.
+bool use_rows(int64_t M, int64_t N) { return (M + 127) / 128 * ((N + 127) / 128) <= sm_count(); }
+
+template <int FORM, int W_MN>
+zb_status product(const zb_linear& g, int64_t ldx, int64_t ldw, const void* X, const void* W, LinearArgs a,
+                  void* stream) {
+    std::string why;
+    CUtensorMap x, w, o, h, r;
+    const bool rows = use_rows(g.M, g.N);
+    const uint32_t x_rows = !rows ? 128 : g.M <= 32 ? 32 : g.M <= 64 ? 64 : 128;
+    bool ok = make_map(&x, X, false, g.K, g.M, ldx, BK, x_rows, &why) &&
+              (W_MN ? make_map(&w, W, false, g.N, g.K, ldw, 64, BK, &why)
+                    : make_map(&w, W, false, g.K, g.N, ldw, BK, 128, &why));
+    if (!ok) return zb::fail(ZB_ERR_CUDA, why);
+    if (rows) {
+        if (x_rows == 32) return launch_rows<FORM, W_MN, 32>(x, w, a, stream);
+        if (x_rows == 64) return launch_rows<FORM, W_MN, 64>(x, w, a, stream);
+        return launch_rows<FORM, W_MN, 128>(x, w, a, stream);
+    }
+    constexpr bool f32 = FORM == STORE32;
+    constexpr CUtensorMapSwizzle sw = f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    ok = make_map(&o, FORM == GELU ? a.out1 : a.out0, f32, g.N, g.M, a.ldo, 32, 32, &why, sw);
+    h = r = o;
+    if (ok && FORM == GELU && a.save) ok = make_map(&h, a.out0, false, g.N, g.M, a.ldo, 32, 32, &why, sw);
+    if (ok && a.R) ok = make_map(&r, a.R, f32, g.N, g.M, a.ldr, 32, 32, &why, sw);
+    if (!ok) return zb::fail(ZB_ERR_CUDA, why);
+    zb::GemmBf16 gm;
+    gm.Mg = g.M;
+    gm.Ng = g.N;
+    gm.Kg = g.K;
+    gm.epi = f32 ? zb::EPI_F32 : zb::EPI_STORE_BF16;
+    EpiArgs ea;
+    choose_l2_hints(gm, 2, &ea);
+    a.hint_a = ea.hint_a;
+    a.hint_b = ea.hint_b;
+    a.hint_out = ea.hint_out;
+    return launch_tiles<FORM, W_MN>(x, w, o, h, r, a, stream);
 }
 
 }  // namespace
@@ -102,33 +895,36 @@ extern "C" zb_status zb_linear_product(const zb_linear* g, const void* X, const 
         return zb::fail(ZB_ERR_INVALID_ARG, "zb_linear_product: required pointer is NULL");
     if (mis16(X) || mis16(W) || mis16(bias) || mis16(R) || mis16(H) || mis16(out0) || mis16(out1))
         return zb::fail(ZB_ERR_ALIGN, "zb_linear_product: pointers must be 16-byte aligned");
-    LinearArgs a;
-    a.X = static_cast<const __nv_bfloat16*>(X);
-    a.W = static_cast<const __nv_bfloat16*>(W);
+    unsigned int* err = zb::device_error_word();
+    if (!err) return ZB_ERR_CUDA;
+    LinearArgs a = {};
     a.bias = static_cast<const __nv_bfloat16*>(bias);
     a.H = static_cast<const __nv_bfloat16*>(H);
     a.R = R;
     a.out0 = out0;
     a.out1 = out1;
-    a.ldx = ldx;
     a.ldr = ldr;
     a.ldh = ldh;
     a.ldo = ldo;
-    a.sk = g->transposed ? 1 : ldw;
-    a.sn = g->transposed ? ldw : 1;
     a.M = static_cast<int>(g->M);
     a.N = static_cast<int>(g->N);
     a.K = static_cast<int>(g->K);
-    a.epilogue = g->epilogue;
+    a.save = gelu && out0 != nullptr;
     a.tanh_form = g->act == ZB_ACT_GELU_TANH;
-    a.f32 = g->dtype == ZB_DT_F32;
-    const int64_t by = (g->M + 63) / 64;
-    if (by > 65535) return zb::fail(ZB_ERR_SHAPE, "zb_linear_product: M too large");
-    zb_linear_simple_kernel<<<dim3(static_cast<unsigned>((g->N + 63) / 64), static_cast<unsigned>(by)), 256, 0,
-                              static_cast<cudaStream_t>(stream)>>>(a);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess)
-        return zb::fail(ZB_ERR_CUDA, std::string("zb_linear_product launch: ") + cudaGetErrorString(e));
-    zb::clear_error();
-    return ZB_OK;
+    a.err = err;
+    auto go = [&](auto form) {
+        constexpr int F = form();
+        return g->transposed ? product<F, 0>(*g, ldx, ldw, X, W, a, stream) : product<F, 1>(*g, ldx, ldw, X, W, a, stream);
+    };
+    zb_status s;
+    if (g->dtype == ZB_DT_F32)
+        s = go(std::integral_constant<int, STORE32>());
+    else if (gelu)
+        s = go(std::integral_constant<int, GELU>());
+    else if (grad)
+        s = go(std::integral_constant<int, GRAD>());
+    else
+        s = go(std::integral_constant<int, STORE>());
+    if (s == ZB_OK) zb::clear_error();
+    return s;
 }
