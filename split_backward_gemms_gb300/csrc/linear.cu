@@ -69,7 +69,12 @@ struct TileCfg {
     static constexpr int STAGES = 5;                         // of 32 KiB: 16 of X, 16 of W
     static constexpr int BOXES = F32 ? 2 : 4;                // staging boxes a warp
     static constexpr uint32_t BOX = F32 ? 32 * 128 : 32 * 64;  // 32 rows x 32 columns
+    // F32's 128 sums a thread need the registers that warps 0-3 (2 and 3 idle) give up
+    static constexpr int THREADS = F32 ? 384 : NUM_THREADS;
+    static constexpr int FIRST = F32 ? 4 : 2;  // first epilogue warp
 };
+constexpr int REGS_LOW = 40, REGS_HIGH = 232;
+static_assert(128 * REGS_LOW + 256 * REGS_HIGH <= 384 * 168, "register split");
 constexpr int TILE_WARPS = 8;
 constexpr uint32_t T_STAGE = Cfg<2>::STAGE_BYTES;
 
@@ -86,7 +91,7 @@ constexpr size_t tile_smem() {
 static_assert(tile_smem<STORE>() <= 232448 && tile_smem<STORE32>() <= 232448, "shared memory");
 
 template <int FORM, int W_MN>
-__global__ void __launch_bounds__(NUM_THREADS, 1)
+__global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
     zb_linear_tiles_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                            const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmH,
                            const __grid_constant__ CUtensorMap tmR, const LinearArgs args) {
@@ -122,7 +127,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         zbp::tma_prefetch_desc(&tmW);
         zbp::tma_prefetch_desc(&tmO);
         if (args.R) zbp::tma_prefetch_desc(&tmR);
-        if (FORM == GELU && args.save) zbp::tma_prefetch_desc(&tmH);
+        if (FORM == GRAD || (FORM == GELU && args.save)) zbp::tma_prefetch_desc(&tmH);
     }
     if (warp == 1) {
         zbp::tmem_alloc_pair(zbp::smem_u32(&ctl->tmem_base), TMEM_COLS);
@@ -137,6 +142,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     zbp::grid_dependency_wait();
     zbp::allow_dependent_launch();
 
+    if (T::F32 && warp < T::FIRST) zbp::regs_dec<REGS_LOW>();
     if (warp == 0) {
         // ---------------------------------------------------- TMA producer
         const uint32_t full0 = zbp::smem_u32(&ctl->full[0]), empty0 = zbp::smem_u32(&ctl->empty[0]);
@@ -227,77 +233,64 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             __syncwarp();
             wait_bar<false>(zbp::smem_u32(&ctl->drain), 0, abort_flag, args.err, ERR_WAIT_MMA, DRAIN_LIMIT_NS, false);
         }
-    } else {
+    } else if (warp >= T::FIRST) {
         // ---------------------------------------------------- epilogue
+        if (T::F32) zbp::regs_inc<REGS_HIGH>();
         constexpr int CH = 4;  // chunks of 32 columns a warp
-        const int ew = warp - 2, q = warp & 3, c_lo = (ew >> 2) * 128;
+        const int ew = warp - T::FIRST, q = warp & 3, c_lo = (ew >> 2) * 128;
         const uint32_t stg0 = zbp::smem_u32(staging) + static_cast<uint32_t>(ew) * T::BOXES * T::BOX;
         const uint32_t rbar0 = zbp::smem_u32(&ctl->rbar[ew][0]);
-        const uint64_t pol_out = zbp::l2_policy(args.hint_out);
-        const bool res = args.R != nullptr;
-        const int per = FORM == GELU && args.save ? 2 : 1;  // boxes a chunk leaves by
-        // chunks whose residual is asked for ahead: the box must have been read
-        // out by the store that left from it
-        const int ahead = T::BOXES / per / 2;
-        uint32_t local = 0;
-        uint32_t g = 0;                  // boxes used so far
-        uint32_t asked = 0, phases = 0;  // a bit a box: residual on its way or landed; phase of its barrier
-        bool ok = true;
-        for (int tile = cluster; tile < num_tiles && ok; tile += clusters) {
+        const uint64_t pol_out = zbp::l2_policy(args.hint_out), pol_once = zbp::l2_policy(1);
+        const bool res = args.R != nullptr, save = FORM == GELU && args.save;
+        // boxes of a chunk: H's (read by GRAD, written by GELU where it is kept),
+        // then the residual's, which the results leave from; without a residual
+        // GRAD's leave from H's
+        const int per = (save || (FORM == GRAD && res)) ? 2 : 1;
+        const bool inputs = res || FORM == GRAD;
+        const uint32_t ring = static_cast<uint32_t>(T::BOXES / per);  // chunks whose boxes there are
+        const uint32_t depth = ring / 2;                             // chunks asked for ahead
+        const uint32_t in_bytes = (FORM == GRAD ? T::BOX : 0u) + (res ? T::BOX : 0u);
+        auto boxes_of = [&](uint32_t j) { return stg0 + (j % ring) * static_cast<uint32_t>(per) * T::BOX; };
+        auto place = [&](int tile, int& row0, int& n0) {  // a tile's first row and column of this warp; its live chunks
             int mb, nb;
             tile_coords(tile, tiles_m, tiles_n, Cfg<2>::GROUP_M, mb, nb);
-            const int row0 = mb * 256 + static_cast<int>(rank) * BM + q * 32, row = row0 + lane;
-            const int n0 = nb * BN + c_lo;  // first column of this warp
-            const bool rows_live = row0 < args.M;
-            const int chunks = rows_live ? min(CH, max(0, (args.N - n0 + 31) / 32)) : 0;
-            const uint32_t g0 = g;
-            auto ask = [&](int c) {  // residual of chunk c into the box its results will leave by
-                const uint32_t b = (g0 + static_cast<uint32_t>(c * per + per - 1)) % T::BOXES;
-                if (lane == 0) {
-                    zbp::mbar_arrive_expect_tx(rbar0 + b * 8u, T::BOX);
-                    zbp::tma_load_2d(stg0 + b * T::BOX, &tmR, rbar0 + b * 8u, n0 + c * 32, row0);
-                }
-                asked |= 1u << b;
-            };
-            if (res && chunks > 0) {
-                // the boxes used in the last chunk may still be read, those before not
-                if (lane == 0) {
-                    if (ahead > 1)
-                        zbp::bulk_wait_read<2>();
-                    else
-                        zbp::bulk_wait_read<0>();
-                }
-                __syncwarp();
-                for (int c = 0; c < min(ahead, chunks); ++c) ask(c);
-                const int ncols = min(128, args.N - n0);
-                if (row < args.M)
-                    zbp::prefetch_l2(static_cast<const uint8_t*>(args.R) +
-                                         (static_cast<long long>(row) * args.ldr + n0) * (T::F32 ? 4 : 2),
-                                     static_cast<uint32_t>(ncols) * (T::F32 ? 4u : 2u));
+            row0 = mb * 256 + static_cast<int>(rank) * BM + q * 32;
+            n0 = nb * BN + c_lo;
+            return row0 < args.M ? min(CH, max(0, (args.N - n0 + 31) / 32)) : 0;
+        };
+        // the inputs of the next chunk (over the tiles) that has not been asked for
+        int a_tile = cluster - clusters, a_c = 0, a_chunks = 0, a_row0 = 0, a_n0 = 0;
+        uint32_t asked = 0, used = 0;  // chunks asked for, chunks stored
+        auto ask = [&]() {
+            while (a_c >= a_chunks) {
+                if (a_tile >= num_tiles) return;
+                a_tile += clusters;
+                if (a_tile >= num_tiles) return;
+                a_c = 0;
+                a_chunks = place(a_tile, a_row0, a_n0);
             }
-            uint32_t h_next[16];
-            auto load_h = [&](int col0) {
-                const __nv_bfloat16* hp = args.H + static_cast<long long>(row) * args.ldh + col0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (row < args.M && col0 + 8 * i < args.N) v = *reinterpret_cast<const uint4*>(hp + 8 * i);
-                    h_next[4 * i] = v.x;
-                    h_next[4 * i + 1] = v.y;
-                    h_next[4 * i + 2] = v.z;
-                    h_next[4 * i + 3] = v.w;
-                }
-            };
-            if (FORM == GRAD && chunks > 0) {
-                if (row < args.M)
-                    zbp::prefetch_l2(args.H + static_cast<long long>(row) * args.ldh + n0,
-                                     static_cast<uint32_t>(min(128, args.N - n0)) * 2u);
-                load_h(n0);
+            if (lane == 0) {
+                const uint32_t bar = rbar0 + (asked % ring) * 8u, at = boxes_of(asked);
+                zbp::mbar_arrive_expect_tx(bar, in_bytes);
+                if (FORM == GRAD) zbp::tma_load_2d_hint(at, &tmH, bar, a_n0 + a_c * 32, a_row0, pol_once);
+                if (res)
+                    zbp::tma_load_2d_hint(at + (FORM == GRAD ? T::BOX : 0u) + (save ? T::BOX : 0u), &tmR, bar,
+                                          a_n0 + a_c * 32, a_row0, pol_once);
             }
+            ++a_c;
+            ++asked;
+        };
+        if (inputs)
+            for (uint32_t k = 0; k < depth; ++k) ask();
+        uint32_t local = 0;
+        bool ok = true;
+        for (int tile = cluster; tile < num_tiles && ok; tile += clusters) {
+            int row0, n0;
+            const int chunks = place(tile, row0, n0);
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(c_lo);
             float acc[T::F32 ? CH : 1][32];
             uint32_t buf = 0;
-            // the accumulators' parts (bf16 outputs have one, read chunk by chunk below)
+            // fp32 outputs add the accumulators' parts; the others have one, read chunk by chunk below
             for (int kb0 = 0; kb0 < num_kb; kb0 += T::F32 ? SEG : num_kb) {
                 buf = local & 1u;
                 const uint32_t tr = local >> 1;
@@ -324,21 +317,31 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 }
             }
             if (!ok) break;
-            auto box_of = [&](uint32_t use) { return stg0 + (use % T::BOXES) * T::BOX; };
+            // this lane's 16-byte part k of its row in a box
+            auto at64 = [&](uint32_t box, int k) { return box + static_cast<uint32_t>(lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)); };
             auto chunk = [&](int c, float (&x)[32]) {
                 const int col0 = n0 + c * 32;
-                if (res && c + ahead < chunks) {
-                    // the box that chunk's results will leave by was used `BOXES` boxes before
-                    if (lane == 0) {
-                        if (ahead > 1)
-                            zbp::bulk_wait_read<1>();
-                        else
-                            zbp::bulk_wait_read<0>();
-                    }
-                    __syncwarp();
-                    ask(c + ahead);
+                const uint32_t box0 = boxes_of(used), box = box0 + static_cast<uint32_t>(per - 1) * T::BOX;
+                uint32_t w[16];
+                if (inputs && !wait_bar<false>(rbar0 + (used % ring) * 8u, (used / ring) & 1u, abort_flag, args.err,
+                                              ERR_WAIT_EPI, WAIT_LIMIT_NS, true)) {
+                    ok = false;
+                    return;
                 }
-                if (args.bias && FORM != GRAD) {
+                if (FORM == GRAD) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float4 h = zbp::ld_shared_v4(at64(box0, k));
+                        w[4 * k] = __float_as_uint(h.x);
+                        w[4 * k + 1] = __float_as_uint(h.y);
+                        w[4 * k + 2] = __float_as_uint(h.z);
+                        w[4 * k + 3] = __float_as_uint(h.w);
+                    }
+                    if (args.tanh_form)
+                        gelu_grad_mul<true, 32>(x, w);
+                    else
+                        gelu_grad_mul<false, 32>(x, w);
+                } else if (args.bias) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         if (col0 + i * 8 >= args.N) break;
@@ -352,15 +355,30 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         }
                     }
                 }
-                uint32_t w[16];
-                if (FORM == GELU && per == 2) {
+                // the boxes of the chunk `depth` ahead were stored from ring - depth chunks ago
+                if (inputs) {
+                    if (lane == 0) {
+                        if (T::BOXES == 4 && per == 1)
+                            zbp::bulk_wait_read<1>();
+                        else
+                            zbp::bulk_wait_read<0>();
+                    }
+                    __syncwarp();
+                    ask();
+                } else {
+                    if (lane == 0) {
+                        if (save)
+                            zbp::bulk_wait_read<2>();
+                        else
+                            zbp::bulk_wait_read<T::BOXES - 1>();
+                    }
+                    __syncwarp();
+                }
+                if (save) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-                    const uint32_t stg = box_of(g++);
-                    if (lane == 0) zbp::bulk_wait_read<T::BOXES - 1>();
-                    __syncwarp();
-                    stage_row64(stg, lane, w);
-                    staging_release<false>(&tmH, stg, lane, col0, row0, pol_out);
+                    stage_row64(box0, lane, w);
+                    staging_release<false>(&tmH, box0, lane, col0, row0, pol_out);
                 }
                 if (FORM == GELU) {
                     if (args.tanh_form)
@@ -368,20 +386,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     else
                         gelu_values<false, 32>(x);
                 }
-                const uint32_t b = g % T::BOXES, stg = box_of(g);
-                ++g;
                 if (res) {
-                    if (!wait_bar<false>(rbar0 + b * 8u, (phases >> b) & 1u, abort_flag, args.err, ERR_WAIT_EPI,
-                                        WAIT_LIMIT_NS, true)) {
-                        ok = false;
-                        return;
-                    }
-                    phases ^= 1u << b;
-                    asked &= ~(1u << b);
                     if (T::F32) {
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
-                            const float4 r = zbp::ld_shared_v4(stg + static_cast<uint32_t>(lane * 128 + ((k ^ (lane & 7)) << 4)));
+                            const float4 r = zbp::ld_shared_v4(box + static_cast<uint32_t>(lane * 128 + ((k ^ (lane & 7)) << 4)));
                             x[4 * k] += r.x;
                             x[4 * k + 1] += r.y;
                             x[4 * k + 2] += r.z;
@@ -390,10 +399,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     } else {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const float4 r =
-                                zbp::ld_shared_v4(stg + static_cast<uint32_t>(lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)));
-                            const float4 rr[1] = {r};
-                            const uint32_t* rw = reinterpret_cast<const uint32_t*>(rr);
+                            const float4 r = zbp::ld_shared_v4(at64(box, k));
+                            const uint32_t rw[4] = {__float_as_uint(r.x), __float_as_uint(r.y), __float_as_uint(r.z),
+                                                    __float_as_uint(r.w)};
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
                                 const float2 f2 = unpack_bf16x2(rw[j]);
@@ -402,21 +410,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                             }
                         }
                     }
-                } else {
-                    if (lane == 0) zbp::bulk_wait_read<T::BOXES - 1>();
-                    __syncwarp();
                 }
                 if constexpr (T::F32) {
                     uint32_t o[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(x[i]);
-                    stage_row(stg, lane, o);
+                    stage_row(box, lane, o);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-                    stage_row64(stg, lane, w);
+                    stage_row64(box, lane, w);
                 }
-                staging_release<false>(&tmO, stg, lane, col0, row0, pol_out);
+                staging_release<false>(&tmO, box, lane, col0, row0, pol_out);
+                ++used;
             };
             if constexpr (T::F32) {
 #pragma unroll
@@ -425,39 +431,23 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             } else {
 #pragma unroll 1
                 for (int c = 0; c < chunks && ok; ++c) {
-                    uint32_t hw[16];
-                    if (FORM == GRAD) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) hw[i] = h_next[i];
-                        if (c + 1 < chunks) load_h(n0 + c * 32 + 32);
-                    }
                     uint32_t v[32];
                     zbp::tmem_ld_32x32b_x32(taddr + buf * ACC_COLS + c * 32, v);
                     zbp::tmem_ld_wait();
                     float x[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(v[i]);
-                    if (FORM == GRAD) {
-                        if (args.tanh_form)
-                            gelu_grad_mul<true, 32>(x, hw);
-                        else
-                            gelu_grad_mul<false, 32>(x, hw);
-                    }
                     chunk(c, x);
                 }
                 zbp::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) zbp::mbar_arrive_remote(zbp::mapa_shared(zbp::smem_u32(&ctl->tempty[buf]), 0));
             }
-            // the boxes of chunks outside the matrix: empty groups, so that groups count boxes
-            for (int c = chunks; c < CH; ++c)
-                for (int i = 0; i < per; ++i, ++g)
-                    if (lane == 0) zbp::bulk_commit();
         }
-        // residuals asked for and not used (after an abort)
-        for (uint32_t b = 0; b < static_cast<uint32_t>(T::BOXES); ++b)
-            if ((asked >> b) & 1u)
-                wait_bar<false>(rbar0 + b * 8u, (phases >> b) & 1u, abort_flag, args.err, ERR_WAIT_EPI, DRAIN_LIMIT_NS, false);
+        // inputs asked for and not used (after an abort)
+        for (; inputs && used < asked; ++used)
+            wait_bar<false>(rbar0 + (used % ring) * 8u, (used / ring) & 1u, abort_flag, args.err, ERR_WAIT_EPI,
+                            DRAIN_LIMIT_NS, false);
         // the staging boxes must not be released while a bulk store reads them
         if (lane == 0) zbp::bulk_wait<0>();
         __syncwarp();
@@ -749,10 +739,10 @@ zb_status launch_tiles(const CUtensorMap& x, const CUtensorMap& w, const CUtenso
     static std::atomic<int> cache[64];
     auto kern = zb_linear_tiles_kernel<FORM, W_MN>;
     int ctas = 0;
-    const zb_status s = full_grid(kern, cache, tile_smem<FORM>(), NUM_THREADS, 2, &ctas);
+    const zb_status s = full_grid(kern, cache, tile_smem<FORM>(), TileCfg<FORM>::THREADS, 2, &ctas);
     if (s != ZB_OK) return s;
     const long long tiles = (static_cast<long long>(a.M) + 255) / 256 * ((a.N + BN - 1) / BN);
-    LaunchCfg cfg(static_cast<int>(std::min<long long>(2 * tiles, ctas)), NUM_THREADS, tile_smem<FORM>(), 2, stream);
+    LaunchCfg cfg(static_cast<int>(std::min<long long>(2 * tiles, ctas)), TileCfg<FORM>::THREADS, tile_smem<FORM>(), 2, stream);
     const cudaError_t e = cudaLaunchKernelEx(&cfg.cfg, kern, x, w, o, h, r, a);
     if (e != cudaSuccess)
         return zb::fail(ZB_ERR_CUDA, std::string("zb_linear_product launch: ") + cudaGetErrorString(e));
@@ -849,6 +839,7 @@ zb_status product(const zb_linear& g, int64_t ldx, int64_t ldw, const void* X, c
     ok = make_map(&o, FORM == GELU ? a.out1 : a.out0, f32, g.N, g.M, a.ldo, 32, 32, &why, sw);
     h = r = o;
     if (ok && FORM == GELU && a.save) ok = make_map(&h, a.out0, false, g.N, g.M, a.ldo, 32, 32, &why, sw);
+    if (ok && FORM == GRAD) ok = make_map(&h, a.H, false, g.N, g.M, a.ldh, 32, 32, &why, sw);
     if (ok && a.R) ok = make_map(&r, a.R, f32, g.N, g.M, a.ldr, 32, 32, &why, sw);
     if (!ok) return zb::fail(ZB_ERR_CUDA, why);
     zb::GemmBf16 gm;
