@@ -32,21 +32,91 @@ struct LinearArgs {
     unsigned int* err;
 };
 
+// GeLU and GeLU' of pairs, with few instructions: at K = 1024 a tile's epilogue
+// takes longer than its MMAs.  With a = |x| and q = Phi(-a) = e t (a1 + t (a2 +
+// ...)) / 2, e = exp(-a^2 / 2), t = 1 / (1 + p a / sqrt 2) (Abramowitz & Stegun
+// 7.1.26, as in gemm_core.cuh):
+//   GeLU(x)  = max(x, 0) - a q
+//   GeLU'(x) = 1/2 + sign(x) (1/2 - g),  g = q - a phi(a)
+// The .ftz forms of ex2 and rcp are single instructions (the others also scale
+// subnormal numbers, which neither e's place in these sums nor a denominator of at
+// least 1 needs): 4096 x 4096, K 1024 with GeLU executes GELU_INSTR.
+__device__ __forceinline__ float ex2_ftz(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float rcp_ftz(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ f32x2 both(float v) { return pk2(v, v); }
+
+// a, e and 2 q / e of the pair (x0, x1).
+__device__ __forceinline__ void tail_pair(float x0, float x1, f32x2& A, f32x2& E, f32x2& Q) {
+    using C = AS71_26;
+    A = pk2(fabsf(x0), fabsf(x1));
+    const f32x2 X = pk2(x0, x1);
+    float v0, v1;
+    up2(mul2(mul2(X, X), both(-0.7213475204444817f)), v0, v1);  // exp(v) = 2^(v / ln 2)
+    E = pk2(ex2_ftz(v0), ex2_ftz(v1));
+    constexpr float pz = C::p * 0.7071067811865476f;
+    up2(fma2(A, both(pz), both(1.0f)), v0, v1);
+    const f32x2 T = pk2(rcp_ftz(v0), rcp_ftz(v1));
+    f32x2 P = fma2(T, both(C::a5), both(C::a4));
+    P = fma2(T, P, both(C::a3));
+    P = fma2(T, P, both(C::a2));
+    P = fma2(T, P, both(C::a1));
+    Q = mul2(T, P);
+}
+
 // GeLU of N values in place (an even number of them), in fp32.
 template <bool TANH, int N>
 __device__ __forceinline__ void gelu_values(float (&x)[N]) {
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
+    for (int i = 0; i < N; i += 2) {
         if (TANH) {
-            x[2 * i] = gelu_t<true>(x[2 * i]);
-            x[2 * i + 1] = gelu_t<true>(x[2 * i + 1]);
+            x[i] = gelu_t<true>(x[i]);
+            x[i + 1] = gelu_t<true>(x[i + 1]);
         } else {
-            const f32x2 X = pk2(x[2 * i], x[2 * i + 1]);
-            f32x2 PHI, E;
-            normal_cdf_and_exp2(X, PHI, E);
-            up2(mul2(X, PHI), x[2 * i], x[2 * i + 1]);
+            f32x2 A, E, Q;
+            tail_pair(x[i], x[i + 1], A, E, Q);
+            const f32x2 relu = pk2(fmaxf(x[i], 0.0f), fmaxf(x[i + 1], 0.0f));
+            up2(fma2(mul2(A, E), mul2(Q, both(-0.5f)), relu), x[i], x[i + 1]);
         }
     }
+}
+
+// x *= GeLU'(h) for N values (h: pairs of bf16).
+template <bool TANH, int N>
+__device__ __forceinline__ void gelu_grad_values(float (&x)[N], const uint32_t (&h)[N / 2]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const float h0 = __uint_as_float(h[i / 2] << 16), h1 = __uint_as_float(h[i / 2] & 0xffff0000u);
+        if (TANH) {
+            x[i] *= gelu_grad_t<true>(h0);
+            x[i + 1] *= gelu_grad_t<true>(h1);
+        } else {
+            f32x2 A, E, Q;
+            tail_pair(h0, h1, A, E, Q);
+            // 1/2 - g = 1/2 - e (Q / 2 - a / sqrt(2 pi))
+            const f32x2 U = fma2(Q, both(-0.5f), mul2(A, both(0.3989422804014327f)));
+            float g0, g1;
+            up2(fma2(E, U, both(0.5f)), g0, g1);
+            const f32x2 G = add2(pk2(copysignf(g0, h0), copysignf(g1, h1)), both(0.5f));
+            up2(mul2(pk2(x[i], x[i + 1]), G), x[i], x[i + 1]);
+        }
+    }
+}
+
+// x += r for 8 values of bf16.
+__device__ __forceinline__ void add_bf16(float* x, const float4& r) {
+    const uint32_t w[4] = {__float_as_uint(r.x), __float_as_uint(r.y), __float_as_uint(r.z), __float_as_uint(r.w)};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        up2(add2(pk2(x[2 * j], x[2 * j + 1]), pk2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u))),
+            x[2 * j], x[2 * j + 1]);
 }
 
 // ---------------------------------------------------------------- large problems
@@ -247,10 +317,11 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
         // GRAD's leave from H's
         const int per = (save || (FORM == GRAD && res)) ? 2 : 1;
         const bool inputs = res || FORM == GRAD;
-        const uint32_t ring = static_cast<uint32_t>(T::BOXES / per);  // chunks whose boxes there are
-        const uint32_t depth = ring / 2;                             // chunks asked for ahead
+        // chunks whose boxes there are (a power of two), and chunks asked for ahead
+        const uint32_t ring = static_cast<uint32_t>(per == 2 ? T::BOXES / 2 : T::BOXES), depth = ring / 2;
+        const uint32_t turn = ring - 1, log_ring = ring == 4 ? 2u : ring == 2 ? 1u : 0u;
         const uint32_t in_bytes = (FORM == GRAD ? T::BOX : 0u) + (res ? T::BOX : 0u);
-        auto boxes_of = [&](uint32_t j) { return stg0 + (j % ring) * static_cast<uint32_t>(per) * T::BOX; };
+        auto boxes_of = [&](uint32_t j) { return stg0 + (j & turn) * static_cast<uint32_t>(per) * T::BOX; };
         auto place = [&](int tile, int& row0, int& n0) {  // a tile's first row and column of this warp; its live chunks
             int mb, nb;
             tile_coords(tile, tiles_m, tiles_n, Cfg<2>::GROUP_M, mb, nb);
@@ -270,7 +341,7 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
                 a_chunks = place(a_tile, a_row0, a_n0);
             }
             if (lane == 0) {
-                const uint32_t bar = rbar0 + (asked % ring) * 8u, at = boxes_of(asked);
+                const uint32_t bar = rbar0 + (asked & turn) * 8u, at = boxes_of(asked);
                 zbp::mbar_arrive_expect_tx(bar, in_bytes);
                 if (FORM == GRAD) zbp::tma_load_2d_hint(at, &tmH, bar, a_n0 + a_c * 32, a_row0, pol_once);
                 if (res)
@@ -323,7 +394,7 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
                 const int col0 = n0 + c * 32;
                 const uint32_t box0 = boxes_of(used), box = box0 + static_cast<uint32_t>(per - 1) * T::BOX;
                 uint32_t w[16];
-                if (inputs && !wait_bar<false>(rbar0 + (used % ring) * 8u, (used / ring) & 1u, abort_flag, args.err,
+                if (inputs && !wait_bar<false>(rbar0 + (used & turn) * 8u, (used >> log_ring) & 1u, abort_flag, args.err,
                                               ERR_WAIT_EPI, WAIT_LIMIT_NS, true)) {
                     ok = false;
                     return;
@@ -338,21 +409,14 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
                         w[4 * k + 3] = __float_as_uint(h.w);
                     }
                     if (args.tanh_form)
-                        gelu_grad_mul<true, 32>(x, w);
+                        gelu_grad_values<true, 32>(x, w);
                     else
-                        gelu_grad_mul<false, 32>(x, w);
+                        gelu_grad_values<false, 32>(x, w);
                 } else if (args.bias) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         if (col0 + i * 8 >= args.N) break;
-                        const uint4 b = *reinterpret_cast<const uint4*>(args.bias + col0 + i * 8);
-                        const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float2 f2 = unpack_bf16x2(bw[j]);
-                            x[i * 8 + 2 * j] += f2.x;
-                            x[i * 8 + 2 * j + 1] += f2.y;
-                        }
+                        add_bf16(x + i * 8, *reinterpret_cast<const float4*>(args.bias + col0 + i * 8));
                     }
                 }
                 // the boxes of the chunk `depth` ahead were stored from ring - depth chunks ago
@@ -399,15 +463,7 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
                     } else {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const float4 r = zbp::ld_shared_v4(at64(box, k));
-                            const uint32_t rw[4] = {__float_as_uint(r.x), __float_as_uint(r.y), __float_as_uint(r.z),
-                                                    __float_as_uint(r.w)};
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const float2 f2 = unpack_bf16x2(rw[j]);
-                                x[8 * k + 2 * j] += f2.x;
-                                x[8 * k + 2 * j + 1] += f2.y;
-                            }
+                            add_bf16(x + 8 * k, zbp::ld_shared_v4(at64(box, k)));
                         }
                     }
                 }
@@ -446,7 +502,7 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
         }
         // inputs asked for and not used (after an abort)
         for (; inputs && used < asked; ++used)
-            wait_bar<false>(rbar0 + (used % ring) * 8u, (used / ring) & 1u, abort_flag, args.err, ERR_WAIT_EPI,
+            wait_bar<false>(rbar0 + (used & turn) * 8u, (used >> log_ring) & 1u, abort_flag, args.err, ERR_WAIT_EPI,
                             DRAIN_LIMIT_NS, false);
         // the staging boxes must not be released while a bulk store reads them
         if (lane == 0) zbp::bulk_wait<0>();
@@ -522,9 +578,9 @@ __device__ __forceinline__ void finish4(const LinearArgs& a, long long row, int 
         const uint2 u = *reinterpret_cast<const uint2*>(a.H + row * a.ldh + col);
         const uint32_t h[2] = {u.x, u.y};
         if (a.tanh_form)
-            gelu_grad_mul<true, 4>(x, h);
+            gelu_grad_values<true, 4>(x, h);
         else
-            gelu_grad_mul<false, 4>(x, h);
+            gelu_grad_values<false, 4>(x, h);
     }
     if (FORM == STORE32) {
         if (a.R) {
