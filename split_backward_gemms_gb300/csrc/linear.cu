@@ -15,6 +15,11 @@
 
 #include "grouped.cuh"
 
+#ifndef ZB_GS
+#define ZB_GS 4
+#define ZB_FS 4
+#define ZB_SS 5
+#endif
 namespace {
 
 enum Form { STORE = 0, GELU = 1, GRAD = 2, STORE32 = 3 };
@@ -136,8 +141,8 @@ template <int FORM>
 struct TileCfg {
     static constexpr bool F32 = FORM == STORE32;
     static constexpr int SEG = 8;                            // F32: blocks of 64 along K an accumulator takes
-    static constexpr int STAGES = 5;                         // of 32 KiB: 16 of X, 16 of W
-    static constexpr int BOXES = F32 ? 2 : 4;                // staging boxes a warp
+    static constexpr int STAGES = FORM == GRAD ? ZB_GS : F32 ? ZB_FS : ZB_SS;  // of 32 KiB: 16 of X, 16 of W
+    static constexpr int BOXES = (7 - STAGES) * (F32 ? 1 : 2);                // staging boxes a warp
     static constexpr uint32_t BOX = F32 ? 32 * 128 : 32 * 64;  // 32 rows x 32 columns
     // F32's 128 sums a thread need the registers that warps 0-3 (2 and 3 idle) give up
     static constexpr int THREADS = F32 ? 384 : NUM_THREADS;
@@ -150,7 +155,7 @@ constexpr uint32_t T_STAGE = Cfg<2>::STAGE_BYTES;
 
 struct TileCtl {
     uint64_t full[6], empty[6], tfull[2], tempty[2], drain;
-    uint64_t rbar[TILE_WARPS][4];  // a residual box has landed
+    uint64_t rbar[TILE_WARPS][8];  // a residual box has landed
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -190,7 +195,7 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
         }
         zbp::mbar_init(zbp::smem_u32(&ctl->drain), 1);
         for (int w = 0; w < TILE_WARPS; ++w)
-            for (int b = 0; b < 4; ++b) zbp::mbar_init(zbp::smem_u32(&ctl->rbar[w][b]), 1);
+            for (int b = 0; b < T::BOXES; ++b) zbp::mbar_init(zbp::smem_u32(&ctl->rbar[w][b]), 1);
         ctl->abort_flag = 0;
         zbp::fence_mbar_init();
         zbp::tma_prefetch_desc(&tmX);
@@ -317,11 +322,10 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
         // GRAD's leave from H's
         const int per = (save || (FORM == GRAD && res)) ? 2 : 1;
         const bool inputs = res || FORM == GRAD;
-        // chunks whose boxes there are (a power of two), and chunks asked for ahead
-        const uint32_t ring = static_cast<uint32_t>(per == 2 ? T::BOXES / 2 : T::BOXES), depth = ring / 2;
-        const uint32_t turn = ring - 1, log_ring = ring == 4 ? 2u : ring == 2 ? 1u : 0u;
+        // chunks whose boxes there are; all but one of them are asked for ahead
+        const uint32_t ring = static_cast<uint32_t>(per == 2 ? T::BOXES / 2 : T::BOXES);
         const uint32_t in_bytes = (FORM == GRAD ? T::BOX : 0u) + (res ? T::BOX : 0u);
-        auto boxes_of = [&](uint32_t j) { return stg0 + (j & turn) * static_cast<uint32_t>(per) * T::BOX; };
+        auto boxes_of = [&](uint32_t slot) { return stg0 + slot * static_cast<uint32_t>(per) * T::BOX; };
         auto place = [&](int tile, int& row0, int& n0) {  // a tile's first row and column of this warp; its live chunks
             int mb, nb;
             tile_coords(tile, tiles_m, tiles_n, Cfg<2>::GROUP_M, mb, nb);
@@ -331,7 +335,8 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
         };
         // the inputs of the next chunk (over the tiles) that has not been asked for
         int a_tile = cluster - clusters, a_c = 0, a_chunks = 0, a_row0 = 0, a_n0 = 0;
-        uint32_t asked = 0, used = 0;  // chunks asked for, chunks stored
+        uint32_t asked = 0, used = 0;            // chunks asked for, chunks stored
+        uint32_t a_slot = 0, slot = 0, turn = 0;  // their places in the ring; parity of the ring's turn
         auto ask = [&]() {
             while (a_c >= a_chunks) {
                 if (a_tile >= num_tiles) return;
@@ -341,7 +346,7 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
                 a_chunks = place(a_tile, a_row0, a_n0);
             }
             if (lane == 0) {
-                const uint32_t bar = rbar0 + (asked & turn) * 8u, at = boxes_of(asked);
+                const uint32_t bar = rbar0 + a_slot * 8u, at = boxes_of(a_slot);
                 zbp::mbar_arrive_expect_tx(bar, in_bytes);
                 if (FORM == GRAD) zbp::tma_load_2d_hint(at, &tmH, bar, a_n0 + a_c * 32, a_row0, pol_once);
                 if (res)
@@ -350,9 +355,10 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
             }
             ++a_c;
             ++asked;
+            a_slot = a_slot + 1 == ring ? 0 : a_slot + 1;
         };
         if (inputs)
-            for (uint32_t k = 0; k < depth; ++k) ask();
+            for (uint32_t k = 0; k + 1 < ring; ++k) ask();
         uint32_t local = 0;
         bool ok = true;
         for (int tile = cluster; tile < num_tiles && ok; tile += clusters) {
@@ -392,9 +398,9 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
             auto at64 = [&](uint32_t box, int k) { return box + static_cast<uint32_t>(lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)); };
             auto chunk = [&](int c, float (&x)[32]) {
                 const int col0 = n0 + c * 32;
-                const uint32_t box0 = boxes_of(used), box = box0 + static_cast<uint32_t>(per - 1) * T::BOX;
+                const uint32_t box0 = boxes_of(slot), box = box0 + static_cast<uint32_t>(per - 1) * T::BOX;
                 uint32_t w[16];
-                if (inputs && !wait_bar<false>(rbar0 + (used & turn) * 8u, (used >> log_ring) & 1u, abort_flag, args.err,
+                if (inputs && !wait_bar<false>(rbar0 + slot * 8u, turn, abort_flag, args.err,
                                               ERR_WAIT_EPI, WAIT_LIMIT_NS, true)) {
                     ok = false;
                     return;
@@ -419,20 +425,16 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
                         add_bf16(x + i * 8, *reinterpret_cast<const float4*>(args.bias + col0 + i * 8));
                     }
                 }
-                // the boxes of the chunk `depth` ahead were stored from ring - depth chunks ago
+                // the last chunk's boxes are the next to be asked for: its stores, well
+                // under way by now, must have read them
                 if (inputs) {
-                    if (lane == 0) {
-                        if (T::BOXES == 4 && per == 1)
-                            zbp::bulk_wait_read<1>();
-                        else
-                            zbp::bulk_wait_read<0>();
-                    }
+                    if (lane == 0) zbp::bulk_wait_read<0>();
                     __syncwarp();
                     ask();
                 } else {
                     if (lane == 0) {
                         if (save)
-                            zbp::bulk_wait_read<2>();
+                            zbp::bulk_wait_read<(T::BOXES / 2 - 1) * 2>();
                         else
                             zbp::bulk_wait_read<T::BOXES - 1>();
                     }
@@ -479,6 +481,10 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
                 }
                 staging_release<false>(&tmO, box, lane, col0, row0, pol_out);
                 ++used;
+                if (++slot == ring) {
+                    slot = 0;
+                    turn ^= 1u;
+                }
             };
             if constexpr (T::F32) {
 #pragma unroll
@@ -501,9 +507,13 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
             }
         }
         // inputs asked for and not used (after an abort)
-        for (; inputs && used < asked; ++used)
-            wait_bar<false>(rbar0 + (used & turn) * 8u, (used >> log_ring) & 1u, abort_flag, args.err, ERR_WAIT_EPI,
-                            DRAIN_LIMIT_NS, false);
+        for (; inputs && used < asked; ++used) {
+            wait_bar<false>(rbar0 + slot * 8u, turn, abort_flag, args.err, ERR_WAIT_EPI, DRAIN_LIMIT_NS, false);
+            if (++slot == ring) {
+                slot = 0;
+                turn ^= 1u;
+            }
+        }
         // the staging boxes must not be released while a bulk store reads them
         if (lane == 0) zbp::bulk_wait<0>();
         __syncwarp();
