@@ -15,11 +15,6 @@
 
 #include "grouped.cuh"
 
-#ifndef ZB_GS
-#define ZB_GS 4
-#define ZB_FS 4
-#define ZB_SS 5
-#endif
 namespace {
 
 enum Form { STORE = 0, GELU = 1, GRAD = 2, STORE32 = 3 };
@@ -32,6 +27,7 @@ struct LinearArgs {
     int M, N, K;
     int save, tanh_form;
     int hint_a, hint_b, hint_out;  // L2 priorities of the copies (choose_l2_hints)
+    int tile_n;                    // tiles kernel: columns of a tile, a multiple of 32
     int tiles_n, split;            // rows kernel: column tiles, CTAs along K
     int stages;                    // rows kernel: of the ring
     unsigned int* err;
@@ -61,14 +57,17 @@ __device__ __forceinline__ f32x2 both(float v) { return pk2(v, v); }
 // a, e and 2 q / e of the pair (x0, x1).
 __device__ __forceinline__ void tail_pair(float x0, float x1, f32x2& A, f32x2& E, f32x2& Q) {
     using C = AS71_26;
-    A = pk2(fabsf(x0), fabsf(x1));
+    // e is 0 from 14 on; a finite a keeps an infinity out of its neighbour's t and of a e
+    const float a0 = fminf(fabsf(x0), 32.0f), a1 = fminf(fabsf(x1), 32.0f);
+    A = pk2(a0, a1);
     const f32x2 X = pk2(x0, x1);
     float v0, v1;
     up2(mul2(mul2(X, X), both(-0.7213475204444817f)), v0, v1);  // exp(v) = 2^(v / ln 2)
     E = pk2(ex2_ftz(v0), ex2_ftz(v1));
     constexpr float pz = C::p * 0.7071067811865476f;
     up2(fma2(A, both(pz), both(1.0f)), v0, v1);
-    const f32x2 T = pk2(rcp_ftz(v0), rcp_ftz(v1));
+    // one reciprocal for both: 1 / v0 = v1 / (v0 v1)
+    const f32x2 T = mul2(both(rcp_ftz(v0 * v1)), pk2(v1, v0));
     f32x2 P = fma2(T, both(C::a5), both(C::a4));
     P = fma2(T, P, both(C::a3));
     P = fma2(T, P, both(C::a2));
@@ -140,48 +139,44 @@ __device__ __forceinline__ void add_bf16(float* x, const float4& r) {
 template <int FORM>
 struct TileCfg {
     static constexpr bool F32 = FORM == STORE32;
-    static constexpr int SEG = 8;                            // F32: blocks of 64 along K an accumulator takes
-    static constexpr int STAGES = FORM == GRAD ? ZB_GS : F32 ? ZB_FS : ZB_SS;  // of 32 KiB: 16 of X, 16 of W
-    static constexpr int BOXES = (7 - STAGES) * (F32 ? 1 : 2);                // staging boxes a warp
-    static constexpr uint32_t BOX = F32 ? 32 * 128 : 32 * 64;  // 32 rows x 32 columns
-    // F32's 128 sums a thread need the registers that warps 0-3 (2 and 3 idle) give up
-    static constexpr int THREADS = F32 ? 384 : NUM_THREADS;
-    static constexpr int FIRST = F32 ? 4 : 2;  // first epilogue warp
+    static constexpr int COLS = F32 ? 16 : 32;  // of a box: 32 rows of 64 bytes
 };
-constexpr int REGS_LOW = 40, REGS_HIGH = 232;
-static_assert(128 * REGS_LOW + 256 * REGS_HIGH <= 384 * 168, "register split");
-constexpr int TILE_WARPS = 8;
+constexpr int SEG = 8;            // fp32 outputs: blocks of 64 along K an accumulator takes
+constexpr int TILE_STAGES = 5;    // of the ring: 16 KiB of X and of W
+constexpr int TILE_WARPS = 8;     // of the epilogue
+constexpr int WARP_COLS = 128;    // columns of a warp
+constexpr uint32_t TILE_BOXES = 4;  // staging boxes a warp
+constexpr uint32_t T_BOX = 32 * 64;
 constexpr uint32_t T_STAGE = Cfg<2>::STAGE_BYTES;
 
 struct TileCtl {
-    uint64_t full[6], empty[6], tfull[2], tempty[2], drain;
-    uint64_t rbar[TILE_WARPS][8];  // a residual box has landed
+    uint64_t full[TILE_STAGES], empty[TILE_STAGES], tfull[2], tempty[2], drain;
+    uint64_t rbar[TILE_WARPS][TILE_BOXES];  // a residual box has landed
     uint32_t tmem_base;
     int abort_flag;
 };
-template <int FORM>
-constexpr size_t tile_smem() {
-    return 1024 + TileCfg<FORM>::STAGES * T_STAGE + TILE_WARPS * TileCfg<FORM>::BOXES * TileCfg<FORM>::BOX + sizeof(TileCtl);
-}
-static_assert(tile_smem<STORE>() <= 232448 && tile_smem<STORE32>() <= 232448, "shared memory");
+constexpr size_t TILE_SMEM = 1024 + TILE_STAGES * T_STAGE + TILE_WARPS * TILE_BOXES * T_BOX + sizeof(TileCtl);
+static_assert(TILE_SMEM <= 232448, "shared memory");
 
 template <int FORM, int W_MN>
-__global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
+__global__ void __launch_bounds__(NUM_THREADS, 1)
     zb_linear_tiles_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                            const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmH,
                            const __grid_constant__ CUtensorMap tmR, const LinearArgs args) {
     using T = TileCfg<FORM>;
-    constexpr int STAGES = T::STAGES, SEG = T::SEG;
+    constexpr int STAGES = TILE_STAGES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t* staging = smem + STAGES * T_STAGE;
-    TileCtl* ctl = reinterpret_cast<TileCtl*>(staging + TILE_WARPS * T::BOXES * T::BOX);
+    TileCtl* ctl = reinterpret_cast<TileCtl*>(staging + TILE_WARPS * TILE_BOXES * T_BOX);
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = zbp::cluster_ctarank();
     const bool leader = rank == 0;
     const int cluster = blockIdx.x / 2, clusters = gridDim.x / 2;
-    const int tiles_m = (args.M + 255) / 256, tiles_n = (args.N + BN - 1) / BN, num_tiles = tiles_m * tiles_n;
+    const int tile_n = W_MN ? BN : args.tile_n;
+    const int tiles_m = (args.M + 255) / 256, tiles_n = (args.N + tile_n - 1) / tile_n, num_tiles = tiles_m * tiles_n;
+    const uint32_t w_bytes = static_cast<uint32_t>(tile_n / 2) * BK * 2u;  // of a stage in one CTA
     const int num_kb = (args.K + BK - 1) / BK;
 
     if (threadIdx.x == 0) {
@@ -195,7 +190,7 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
         }
         zbp::mbar_init(zbp::smem_u32(&ctl->drain), 1);
         for (int w = 0; w < TILE_WARPS; ++w)
-            for (int b = 0; b < T::BOXES; ++b) zbp::mbar_init(zbp::smem_u32(&ctl->rbar[w][b]), 1);
+            for (int b = 0; b < static_cast<int>(TILE_BOXES); ++b) zbp::mbar_init(zbp::smem_u32(&ctl->rbar[w][b]), 1);
         ctl->abort_flag = 0;
         zbp::fence_mbar_init();
         zbp::tma_prefetch_desc(&tmX);
@@ -217,7 +212,6 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
     zbp::grid_dependency_wait();
     zbp::allow_dependent_launch();
 
-    if (T::F32 && warp < T::FIRST) zbp::regs_dec<REGS_LOW>();
     if (warp == 0) {
         // ---------------------------------------------------- TMA producer
         const uint32_t full0 = zbp::smem_u32(&ctl->full[0]), empty0 = zbp::smem_u32(&ctl->empty[0]);
@@ -229,7 +223,7 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
             int mb, nb;
             tile_coords(tile, tiles_m, tiles_n, Cfg<2>::GROUP_M, mb, nb);
             const int m0 = mb * 256 + static_cast<int>(rank) * BM;
-            const int n0 = nb * BN + static_cast<int>(rank) * 128;
+            const int n0 = nb * tile_n + static_cast<int>(rank) * (tile_n / 2);
             for (int kb = 0; kb < num_kb; ++kb, ++it) {
                 if (!wait_bar<false>(empty0 + s * 8u, sp, abort_flag, args.err, ERR_WAIT_PRODUCER, WAIT_LIMIT_NS, true)) {
                     ok = false;
@@ -238,7 +232,7 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
                 if (zbp::elect_one()) {
                     const uint32_t full = full0_lead + s * 8u, sa = sa0 + s * T_STAGE, sb = sa + A_BYTES;
                     const int k0 = kb * BK;
-                    if (leader) zbp::mbar_arrive_expect_tx(full0 + s * 8u, 2 * T_STAGE);
+                    if (leader) zbp::mbar_arrive_expect_tx(full0 + s * 8u, 2 * (A_BYTES + w_bytes));
                     zbp::tma_load_2d_pair_hint(sa, &tmX, full, k0, m0, pol_x);
                     if (W_MN) {
                         zbp::tma_load_2d_pair_hint(sb, &tmW, full, n0, k0, pol_w);
@@ -264,7 +258,7 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
     } else if (warp == 1) {
         if (leader) {
             // ------------------------------------------------ MMA issuer
-            constexpr uint32_t idesc = zbp::idesc_bf16_f32(256, BN, 0, W_MN);
+            const uint32_t idesc = zbp::idesc_bf16_f32(256, static_cast<uint32_t>(tile_n), 0, W_MN);
             constexpr uint32_t W_STEP = W_MN ? 2048 >> 4 : 32 >> 4, hi = zbp::desc_hi(1024);
             const uint32_t a0 = zbp::desc_lo(zbp::smem_u32(smem), 16);
             const uint32_t b0 = zbp::desc_lo(zbp::smem_u32(smem) + A_BYTES, W_MN ? MN_ATOM_BYTES : 16);
@@ -308,30 +302,29 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
             __syncwarp();
             wait_bar<false>(zbp::smem_u32(&ctl->drain), 0, abort_flag, args.err, ERR_WAIT_MMA, DRAIN_LIMIT_NS, false);
         }
-    } else if (warp >= T::FIRST) {
+    } else {
         // ---------------------------------------------------- epilogue
-        if (T::F32) zbp::regs_inc<REGS_HIGH>();
-        constexpr int CH = 4;  // chunks of 32 columns a warp
-        const int ew = warp - T::FIRST, q = warp & 3, c_lo = (ew >> 2) * 128;
-        const uint32_t stg0 = zbp::smem_u32(staging) + static_cast<uint32_t>(ew) * T::BOXES * T::BOX;
+        constexpr int CH = WARP_COLS / T::COLS;  // chunks of a warp's columns
+        const int ew = warp - 2, q = warp & 3, c_lo = (ew >> 2) * WARP_COLS;
+        const uint32_t stg0 = zbp::smem_u32(staging) + static_cast<uint32_t>(ew) * TILE_BOXES * T_BOX;
         const uint32_t rbar0 = zbp::smem_u32(&ctl->rbar[ew][0]);
         const uint64_t pol_out = zbp::l2_policy(args.hint_out), pol_once = zbp::l2_policy(1);
         const bool res = args.R != nullptr, save = FORM == GELU && args.save;
         // boxes of a chunk: H's (read by GRAD, written by GELU where it is kept),
         // then the residual's, which the results leave from; without a residual
         // GRAD's leave from H's
-        const int per = (save || (FORM == GRAD && res)) ? 2 : 1;
+        const uint32_t per = (save || (FORM == GRAD && res)) ? 2 : 1;
         const bool inputs = res || FORM == GRAD;
-        // chunks whose boxes there are; all but one of them are asked for ahead
-        const uint32_t ring = static_cast<uint32_t>(per == 2 ? T::BOXES / 2 : T::BOXES);
-        const uint32_t in_bytes = (FORM == GRAD ? T::BOX : 0u) + (res ? T::BOX : 0u);
-        auto boxes_of = [&](uint32_t slot) { return stg0 + slot * static_cast<uint32_t>(per) * T::BOX; };
+        const uint32_t in_bytes = (FORM == GRAD ? T_BOX : 0u) + (res ? T_BOX : 0u);
+        const uint32_t ring = per == 2 ? TILE_BOXES / 2 : TILE_BOXES;  // chunks whose boxes there are
+        auto boxes_of = [&](uint32_t slot) { return stg0 + slot * per * T_BOX; };
         auto place = [&](int tile, int& row0, int& n0) {  // a tile's first row and column of this warp; its live chunks
             int mb, nb;
             tile_coords(tile, tiles_m, tiles_n, Cfg<2>::GROUP_M, mb, nb);
             row0 = mb * 256 + static_cast<int>(rank) * BM + q * 32;
-            n0 = nb * BN + c_lo;
-            return row0 < args.M ? min(CH, max(0, (args.N - n0 + 31) / 32)) : 0;
+            n0 = nb * tile_n + c_lo;
+            const int cols = min(args.N - n0, tile_n - c_lo);
+            return row0 < args.M ? min(CH, max(0, (cols + T::COLS - 1) / T::COLS)) : 0;
         };
         // the inputs of the next chunk (over the tiles) that has not been asked for
         int a_tile = cluster - clusters, a_c = 0, a_chunks = 0, a_row0 = 0, a_n0 = 0;
@@ -347,27 +340,36 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
             }
             if (lane == 0) {
                 const uint32_t bar = rbar0 + a_slot * 8u, at = boxes_of(a_slot);
+                const int x = a_n0 + a_c * T::COLS;
                 zbp::mbar_arrive_expect_tx(bar, in_bytes);
-                if (FORM == GRAD) zbp::tma_load_2d_hint(at, &tmH, bar, a_n0 + a_c * 32, a_row0, pol_once);
-                if (res)
-                    zbp::tma_load_2d_hint(at + (FORM == GRAD ? T::BOX : 0u) + (save ? T::BOX : 0u), &tmR, bar,
-                                          a_n0 + a_c * 32, a_row0, pol_once);
+                if (FORM == GRAD) zbp::tma_load_2d_hint(at, &tmH, bar, x, a_row0, pol_once);
+                if (res) zbp::tma_load_2d_hint(at + (per - 1) * T_BOX, &tmR, bar, x, a_row0, pol_once);
             }
             ++a_c;
             ++asked;
             a_slot = a_slot + 1 == ring ? 0 : a_slot + 1;
         };
+        bool owed = false;  // the last chunk's boxes have not been asked for again
+        // once the stores so far have read their boxes
+        auto ask_on = [&]() {
+            if (lane == 0) zbp::bulk_wait_read<0>();
+            __syncwarp();
+            ask();
+            owed = false;
+        };
         if (inputs)
-            for (uint32_t k = 0; k + 1 < ring; ++k) ask();
+            for (uint32_t k = 0; k < ring; ++k) ask();
+        // this lane's 16-byte part k of its row in a box
+        auto part = [&](uint32_t box, int k) { return box + static_cast<uint32_t>(lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)); };
         uint32_t local = 0;
         bool ok = true;
         for (int tile = cluster; tile < num_tiles && ok; tile += clusters) {
             int row0, n0;
             const int chunks = place(tile, row0, n0);
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(c_lo);
-            float acc[T::F32 ? CH : 1][32];
+            float acc[T::F32 ? CH : 1][16];
             uint32_t buf = 0;
-            // fp32 outputs add the accumulators' parts; the others have one, read chunk by chunk below
+            // fp32 outputs add the accumulators' parts; the others have one, read piece by piece below
             for (int kb0 = 0; kb0 < num_kb; kb0 += T::F32 ? SEG : num_kb) {
                 buf = local & 1u;
                 const uint32_t tr = local >> 1;
@@ -381,11 +383,11 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
                 if constexpr (T::F32) {
 #pragma unroll
                     for (int c = 0; c < CH; ++c) {
-                        uint32_t v[32];
-                        zbp::tmem_ld_32x32b_x32(taddr + buf * ACC_COLS + c * 32, v);
+                        uint32_t v[16];
+                        zbp::tmem_ld_32x32b_x16(taddr + buf * ACC_COLS + c * 16, v);
                         zbp::tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
+                        for (int i = 0; i < 16; ++i)
                             acc[c][i] = kb0 == 0 ? __uint_as_float(v[i]) : acc[c][i] + __uint_as_float(v[i]);
                     }
                     zbp::tc_fence_before();
@@ -394,92 +396,102 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
                 }
             }
             if (!ok) break;
-            // this lane's 16-byte part k of its row in a box
-            auto at64 = [&](uint32_t box, int k) { return box + static_cast<uint32_t>(lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)); };
-            auto chunk = [&](int c, float (&x)[32]) {
-                const int col0 = n0 + c * 32;
-                const uint32_t box0 = boxes_of(slot), box = box0 + static_cast<uint32_t>(per - 1) * T::BOX;
-                uint32_t w[16];
-                if (inputs && !wait_bar<false>(rbar0 + slot * 8u, turn, abort_flag, args.err,
-                                              ERR_WAIT_EPI, WAIT_LIMIT_NS, true)) {
-                    ok = false;
-                    return;
-                }
+            // 16 columns from col, the p-th of their boxes
+            auto piece = [&](int p, int col, uint32_t box0, uint32_t box, float (&x)[16]) {
                 if (FORM == GRAD) {
+                    uint32_t w[8];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float4 h = zbp::ld_shared_v4(at64(box0, k));
+                    for (int k = 0; k < 2; ++k) {
+                        const float4 h = zbp::ld_shared_v4(part(box0, 2 * p + k));
                         w[4 * k] = __float_as_uint(h.x);
                         w[4 * k + 1] = __float_as_uint(h.y);
                         w[4 * k + 2] = __float_as_uint(h.z);
                         w[4 * k + 3] = __float_as_uint(h.w);
                     }
                     if (args.tanh_form)
-                        gelu_grad_values<true, 32>(x, w);
+                        gelu_grad_values<true, 16>(x, w);
                     else
-                        gelu_grad_values<false, 32>(x, w);
+                        gelu_grad_values<false, 16>(x, w);
                 } else if (args.bias) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (col0 + i * 8 >= args.N) break;
-                        add_bf16(x + i * 8, *reinterpret_cast<const float4*>(args.bias + col0 + i * 8));
-                    }
+                    for (int i = 0; i < 2; ++i)
+                        if (col + i * 8 < args.N)
+                            add_bf16(x + i * 8, *reinterpret_cast<const float4*>(args.bias + col + i * 8));
                 }
-                // the last chunk's boxes are the next to be asked for: its stores, well
-                // under way by now, must have read them
-                if (inputs) {
-                    if (lane == 0) zbp::bulk_wait_read<0>();
-                    __syncwarp();
-                    ask();
-                } else {
-                    if (lane == 0) {
-                        if (save)
-                            zbp::bulk_wait_read<(T::BOXES / 2 - 1) * 2>();
-                        else
-                            zbp::bulk_wait_read<T::BOXES - 1>();
-                    }
-                    __syncwarp();
-                }
-                if (save) {
+                auto put = [&](uint32_t to) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-                    stage_row64(box0, lane, w);
-                    staging_release<false>(&tmH, box0, lane, col0, row0, pol_out);
-                }
+                    for (int k = 0; k < 2; ++k)
+                        zbp::st_shared_v4(part(to, 2 * p + k), pack_bf16x2(x[8 * k], x[8 * k + 1]),
+                                          pack_bf16x2(x[8 * k + 2], x[8 * k + 3]), pack_bf16x2(x[8 * k + 4], x[8 * k + 5]),
+                                          pack_bf16x2(x[8 * k + 6], x[8 * k + 7]));
+                };
                 if (FORM == GELU) {
+                    if (save) put(box0);
                     if (args.tanh_form)
-                        gelu_values<true, 32>(x);
+                        gelu_values<true, 16>(x);
                     else
-                        gelu_values<false, 32>(x);
+                        gelu_values<false, 16>(x);
                 }
-                if (res) {
-                    if (T::F32) {
+                if constexpr (T::F32) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const float4 r = zbp::ld_shared_v4(box + static_cast<uint32_t>(lane * 128 + ((k ^ (lane & 7)) << 4)));
+                    for (int k = 0; k < 4; ++k) {
+                        if (res) {
+                            const float4 r = zbp::ld_shared_v4(part(box, k));
                             x[4 * k] += r.x;
                             x[4 * k + 1] += r.y;
                             x[4 * k + 2] += r.z;
                             x[4 * k + 3] += r.w;
                         }
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            add_bf16(x + 8 * k, zbp::ld_shared_v4(at64(box, k)));
-                        }
+                        zbp::st_shared_v4(part(box, k), __float_as_uint(x[4 * k]), __float_as_uint(x[4 * k + 1]),
+                                          __float_as_uint(x[4 * k + 2]), __float_as_uint(x[4 * k + 3]));
                     }
+                } else {
+                    if (res)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) add_bf16(x + 8 * k, zbp::ld_shared_v4(part(box, 2 * p + k)));
+                    put(box);
+                }
+            };
+            auto chunk = [&](int c, float (&sums)[16]) {
+                const int col0 = n0 + c * T::COLS;
+                const uint32_t box0 = boxes_of(slot), box = box0 + (per - 1) * T_BOX;
+                if (inputs) {
+                    if (owed) ask_on();
+                    if (!wait_bar<false>(rbar0 + slot * 8u, turn, abort_flag, args.err, ERR_WAIT_EPI, WAIT_LIMIT_NS, true)) {
+                        ok = false;
+                        return;
+                    }
+                } else {
+                    if (lane == 0) {
+                        if (per == 2)
+                            zbp::bulk_wait_read<TILE_BOXES / 2 - 1>();
+                        else
+                            zbp::bulk_wait_read<TILE_BOXES - 1>();
+                    }
+                    __syncwarp();
                 }
                 if constexpr (T::F32) {
-                    uint32_t o[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(x[i]);
-                    stage_row(box, lane, o);
+                    piece(0, col0, box0, box, sums);
                 } else {
+#pragma unroll 1
+                    for (int p = 0; p < 2; ++p) {
+                        uint32_t v[16];
+                        zbp::tmem_ld_32x32b_x16(taddr + buf * ACC_COLS + c * 32 + p * 16, v);
+                        zbp::tmem_ld_wait();
+                        float x[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-                    stage_row64(box, lane, w);
+                        for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(v[i]);
+                        piece(p, col0 + p * 16, box0, box, x);
+                    }
                 }
-                staging_release<false>(&tmO, box, lane, col0, row0, pol_out);
+                zbp::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (save) zbp::tma_store_2d_hint(&tmH, box0, col0, row0, pol_out);
+                    zbp::tma_store_2d_hint(&tmO, box, col0, row0, pol_out);
+                    zbp::bulk_commit();
+                }
+                owed = inputs;
                 ++used;
                 if (++slot == ring) {
                     slot = 0;
@@ -493,18 +505,13 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
             } else {
 #pragma unroll 1
                 for (int c = 0; c < chunks && ok; ++c) {
-                    uint32_t v[32];
-                    zbp::tmem_ld_32x32b_x32(taddr + buf * ACC_COLS + c * 32, v);
-                    zbp::tmem_ld_wait();
-                    float x[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(v[i]);
-                    chunk(c, x);
+                    chunk(c, acc[0]);
                 }
                 zbp::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) zbp::mbar_arrive_remote(zbp::mapa_shared(zbp::smem_u32(&ctl->tempty[buf]), 0));
             }
+            if (owed) ask_on();
         }
         // inputs asked for and not used (after an abort)
         for (; inputs && used < asked; ++used) {
@@ -617,7 +624,7 @@ __global__ void __launch_bounds__(R_THREADS, 1)
     zb_linear_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                           const LinearArgs args) {
     constexpr uint32_t STAGE = rows_stage(ROWS);
-    constexpr int SEG = 8, PARTS = FORM == STORE32 ? 512 / ROWS : 1;  // accumulators, at most
+    constexpr int PARTS = FORM == STORE32 ? 512 / ROWS : 1;  // accumulators, at most
     constexpr uint32_t TMEM = PARTS * ROWS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -805,10 +812,10 @@ zb_status launch_tiles(const CUtensorMap& x, const CUtensorMap& w, const CUtenso
     static std::atomic<int> cache[64];
     auto kern = zb_linear_tiles_kernel<FORM, W_MN>;
     int ctas = 0;
-    const zb_status s = full_grid(kern, cache, tile_smem<FORM>(), TileCfg<FORM>::THREADS, 2, &ctas);
+    const zb_status s = full_grid(kern, cache, TILE_SMEM, NUM_THREADS, 2, &ctas);
     if (s != ZB_OK) return s;
-    const long long tiles = (static_cast<long long>(a.M) + 255) / 256 * ((a.N + BN - 1) / BN);
-    LaunchCfg cfg(static_cast<int>(std::min<long long>(2 * tiles, ctas)), TileCfg<FORM>::THREADS, tile_smem<FORM>(), 2, stream);
+    const long long tiles = (static_cast<long long>(a.M) + 255) / 256 * ((a.N + a.tile_n - 1) / a.tile_n);
+    LaunchCfg cfg(static_cast<int>(std::min<long long>(2 * tiles, ctas)), NUM_THREADS, TILE_SMEM, 2, stream);
     const cudaError_t e = cudaLaunchKernelEx(&cfg.cfg, kern, x, w, o, h, r, a);
     if (e != cudaSuccess)
         return zb::fail(ZB_ERR_CUDA, std::string("zb_linear_product launch: ") + cudaGetErrorString(e));
@@ -881,6 +888,25 @@ bool stride(int64_t* ld, int64_t width) {
     return *ld >= width && *ld <= (1LL << 30);
 }
 
+// Columns of a tile, where W lies along K (transposed; otherwise its copies come
+// in columns of 64, and fewer save nothing): those for which the rounds of tiles
+// that a CTA pair takes cost least, a tile costing its columns and a fixed part.
+// 256 and 224 columns, GeLU' with residual, K 1024 (and 1536): 4096 x 4096 39.0
+// and 36.1 us, 2048 x 4096 23.5 and 22.0, 4096 x 6144 66.0 and 63.2.
+int choose_tile_n(int64_t M, int64_t N) {
+    const int64_t pairs = std::max(sm_count() / 2, 1), tm = (M + 255) / 256;
+    int best = BN;
+    int64_t least = INT64_MAX;
+    for (int tn = BN; tn >= 192; tn -= 32) {
+        const int64_t cost = (tm * ((N + tn - 1) / tn) + pairs - 1) / pairs * (tn + 32);
+        if (cost < least) {
+            least = cost;
+            best = tn;
+        }
+    }
+    return best;
+}
+
 // The rows kernel where 128 x 128 tiles fit on the SMs at once.
 bool use_rows(int64_t M, int64_t N) { return (M + 127) / 128 * ((N + 127) / 128) <= sm_count(); }
 
@@ -890,10 +916,12 @@ zb_status product(const zb_linear& g, int64_t ldx, int64_t ldw, const void* X, c
     std::string why;
     CUtensorMap x, w, o, h, r;
     const bool rows = use_rows(g.M, g.N);
+    a.tile_n = W_MN ? BN : choose_tile_n(g.M, g.N);
+    const uint32_t w_rows = rows ? 128 : static_cast<uint32_t>(a.tile_n / 2);
     const uint32_t x_rows = !rows ? 128 : g.M <= 32 ? 32 : g.M <= 64 ? 64 : 128;
     bool ok = make_map(&x, X, false, g.K, g.M, ldx, BK, x_rows, &why) &&
               (W_MN ? make_map(&w, W, false, g.N, g.K, ldw, 64, BK, &why)
-                    : make_map(&w, W, false, g.K, g.N, ldw, BK, 128, &why));
+                    : make_map(&w, W, false, g.K, g.N, ldw, BK, w_rows, &why));
     if (!ok) return zb::fail(ZB_ERR_CUDA, why);
     if (rows) {
         if (x_rows == 32) return launch_rows<FORM, W_MN, 32>(x, w, a, stream);
@@ -901,12 +929,13 @@ zb_status product(const zb_linear& g, int64_t ldx, int64_t ldw, const void* X, c
         return launch_rows<FORM, W_MN, 128>(x, w, a, stream);
     }
     constexpr bool f32 = FORM == STORE32;
-    constexpr CUtensorMapSwizzle sw = f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
-    ok = make_map(&o, FORM == GELU ? a.out1 : a.out0, f32, g.N, g.M, a.ldo, 32, 32, &why, sw);
+    constexpr CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_64B;
+    constexpr uint32_t cols = TileCfg<FORM>::COLS;
+    ok = make_map(&o, FORM == GELU ? a.out1 : a.out0, f32, g.N, g.M, a.ldo, cols, 32, &why, sw);
     h = r = o;
-    if (ok && FORM == GELU && a.save) ok = make_map(&h, a.out0, false, g.N, g.M, a.ldo, 32, 32, &why, sw);
-    if (ok && FORM == GRAD) ok = make_map(&h, a.H, false, g.N, g.M, a.ldh, 32, 32, &why, sw);
-    if (ok && a.R) ok = make_map(&r, a.R, f32, g.N, g.M, a.ldr, 32, 32, &why, sw);
+    if (ok && FORM == GELU && a.save) ok = make_map(&h, a.out0, false, g.N, g.M, a.ldo, cols, 32, &why, sw);
+    if (ok && FORM == GRAD) ok = make_map(&h, a.H, false, g.N, g.M, a.ldh, cols, 32, &why, sw);
+    if (ok && a.R) ok = make_map(&r, a.R, f32, g.N, g.M, a.ldr, cols, 32, &why, sw);
     if (!ok) return zb::fail(ZB_ERR_CUDA, why);
     zb::GemmBf16 gm;
     gm.Mg = g.M;
