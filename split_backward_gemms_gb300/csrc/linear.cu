@@ -144,7 +144,7 @@ struct TileCfg {
 constexpr int SEG = 8;            // fp32 outputs: blocks of 64 along K an accumulator takes
 constexpr int TILE_STAGES = 5;    // of the ring: 16 KiB of X and of W
 constexpr int TILE_WARPS = 8;     // of the epilogue
-constexpr int WARP_COLS = 128;    // columns of a warp
+constexpr int WARP_COLS = 128;    // columns of a warp, at most
 constexpr uint32_t TILE_BOXES = 4;  // staging boxes a warp
 constexpr uint32_t T_BOX = 32 * 64;
 constexpr uint32_t T_STAGE = Cfg<2>::STAGE_BYTES;
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const uint32_t rank = zbp::cluster_ctarank();
     const bool leader = rank == 0;
     const int cluster = blockIdx.x / 2, clusters = gridDim.x / 2;
-    const int tile_n = W_MN ? BN : args.tile_n;
+    const int tile_n = args.tile_n;
     const int tiles_m = (args.M + 255) / 256, tiles_n = (args.N + tile_n - 1) / tile_n, num_tiles = tiles_m * tiles_n;
     const uint32_t w_bytes = static_cast<uint32_t>(tile_n / 2) * BK * 2u;  // of a stage in one CTA
     const int num_kb = (args.K + BK - 1) / BK;
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     zbp::tma_load_2d_pair_hint(sa, &tmX, full, k0, m0, pol_x);
                     if (W_MN) {
                         zbp::tma_load_2d_pair_hint(sb, &tmW, full, n0, k0, pol_w);
-                        zbp::tma_load_2d_pair_hint(sb + MN_ATOM_BYTES, &tmW, full, n0 + 64, k0, pol_w);
+                        if (tile_n == BN) zbp::tma_load_2d_pair_hint(sb + MN_ATOM_BYTES, &tmW, full, n0 + 64, k0, pol_w);
                     } else {
                         zbp::tma_load_2d_pair_hint(sb, &tmW, full, k0, n0, pol_w);
                     }
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     } else {
         // ---------------------------------------------------- epilogue
         constexpr int CH = WARP_COLS / T::COLS;  // chunks of a warp's columns
-        const int ew = warp - 2, q = warp & 3, c_lo = (ew >> 2) * WARP_COLS;
+        const int ew = warp - 2, q = warp & 3, half = (tile_n / 2 + 31) / 32 * 32, c_lo = (ew >> 2) * half;
         const uint32_t stg0 = zbp::smem_u32(staging) + static_cast<uint32_t>(ew) * TILE_BOXES * T_BOX;
         const uint32_t rbar0 = zbp::smem_u32(&ctl->rbar[ew][0]);
         const uint64_t pol_out = zbp::l2_policy(args.hint_out), pol_once = zbp::l2_policy(1);
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             tile_coords(tile, tiles_m, tiles_n, Cfg<2>::GROUP_M, mb, nb);
             row0 = mb * 256 + static_cast<int>(rank) * BM + q * 32;
             n0 = nb * tile_n + c_lo;
-            const int cols = min(args.N - n0, tile_n - c_lo);
+            const int cols = min(args.N - n0, min(half, tile_n - c_lo));
             return row0 < args.M ? min(CH, max(0, (cols + T::COLS - 1) / T::COLS)) : 0;
         };
         // the inputs of the next chunk (over the tiles) that has not been asked for
@@ -888,17 +888,18 @@ bool stride(int64_t* ld, int64_t width) {
     return *ld >= width && *ld <= (1LL << 30);
 }
 
-// Columns of a tile, where W lies along K (transposed; otherwise its copies come
-// in columns of 64, and fewer save nothing): those for which the rounds of tiles
-// that a CTA pair takes cost least, a tile costing its columns and a fixed part.
+// Columns of a tile: those for which the rounds of tiles that a CTA pair takes
+// cost least; what a tile costs goes with the operands' bytes, 256 rows and its
+// columns.  W's copies come in columns of 64 for each CTA of the pair unless it
+// lies along K (transposed), so there the columns are 256 or 128.
 // 256 and 224 columns, GeLU' with residual, K 1024 (and 1536): 4096 x 4096 39.0
 // and 36.1 us, 2048 x 4096 23.5 and 22.0, 4096 x 6144 66.0 and 63.2.
-int choose_tile_n(int64_t M, int64_t N) {
+int choose_tile_n(int64_t M, int64_t N, bool along_k) {
     const int64_t pairs = std::max(sm_count() / 2, 1), tm = (M + 255) / 256;
     int best = BN;
     int64_t least = INT64_MAX;
-    for (int tn = BN; tn >= 192; tn -= 32) {
-        const int64_t cost = (tm * ((N + tn - 1) / tn) + pairs - 1) / pairs * (tn + 32);
+    for (int tn = BN; tn >= 128; tn -= along_k ? 32 : 128) {
+        const int64_t cost = (tm * ((N + tn - 1) / tn) + pairs - 1) / pairs * (256 + tn);
         if (cost < least) {
             least = cost;
             best = tn;
@@ -916,7 +917,7 @@ zb_status product(const zb_linear& g, int64_t ldx, int64_t ldw, const void* X, c
     std::string why;
     CUtensorMap x, w, o, h, r;
     const bool rows = use_rows(g.M, g.N);
-    a.tile_n = W_MN ? BN : choose_tile_n(g.M, g.N);
+    a.tile_n = choose_tile_n(g.M, g.N, !W_MN);
     const uint32_t w_rows = rows ? 128 : static_cast<uint32_t>(a.tile_n / 2);
     const uint32_t x_rows = !rows ? 128 : g.M <= 32 ? 32 : g.M <= 64 ? 64 : 128;
     bool ok = make_map(&x, X, false, g.K, g.M, ldx, BK, x_rows, &why) &&
