@@ -41,7 +41,9 @@ struct LinearArgs {
 //   GeLU'(x) = 1/2 + sign(x) (1/2 - g),  g = q - a phi(a)
 // The .ftz forms of ex2 and rcp are single instructions (the others also scale
 // subnormal numbers, which neither e's place in these sums nor a denominator of at
-// least 1 needs): 4096 x 4096, K 1024 with GeLU executes GELU_INSTR.
+// least 1 needs): 4096 x 4096, K 1024 with GeLU' and
+// residual executes 16.5 million warp instructions with the forms of gemm_core.cuh,
+// 10.7 million with these (45.6 and 41.5 us).
 __device__ __forceinline__ float ex2_ftz(float v) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
@@ -908,18 +910,34 @@ int choose_tile_n(int64_t M, int64_t N, bool along_k) {
     return best;
 }
 
-// The rows kernel where 128 x 128 tiles fit on the SMs at once.
-bool use_rows(int64_t M, int64_t N) { return (M + 127) / 128 * ((N + 127) / 128) <= sm_count(); }
+// The rows kernel's tile: as few rows as hold M, 128 at most.
+int rows_of(int64_t M) { return M <= 32 ? 32 : M <= 64 ? 64 : 128; }
+
+// The rows kernel for up to 32 rows, for up to 64 unless its tiles outnumber the
+// SMs, and for more where it can split K as often as pays.  us of the tiles and
+// the rows kernel with residual:
+//   16 x 1024    K 4096  20    5.3      16 x 16384   K 1024  12.7   8.2
+//   64 x 4096    K 1024   6.5  5.6      64 x 32768   K 1024  17.6  25.1
+//   256 x 1024   K 1024   6.6  5.9      512 x 1024   K  512   5.5   6.4
+//   512 x 1024   K 1024   6.7  7.0      512 x 1024   K 4096  14.1   9.8
+//   512 x 2048   K 1024   6.8  8.5      512 x 2048   K 4096  16.4  15.9
+//   1024 x 2048  K 1024   7.6 10.1      1024 x 2048  K 4096  19.5  25.2
+bool use_rows(int64_t M, int64_t N, int64_t K) {
+    const int64_t tiles = (M + rows_of(M) - 1) / rows_of(M) * ((N + 127) / 128), sms = sm_count();
+    if (M <= 32) return true;
+    if (M <= 64) return tiles <= sms;
+    return tiles <= sms / 8 || (tiles <= sms / 4 && K >= 2048) || (tiles <= sms / 2 && K >= 4096);
+}
 
 template <int FORM, int W_MN>
 zb_status product(const zb_linear& g, int64_t ldx, int64_t ldw, const void* X, const void* W, LinearArgs a,
                   void* stream) {
     std::string why;
     CUtensorMap x, w, o, h, r;
-    const bool rows = use_rows(g.M, g.N);
+    const bool rows = use_rows(g.M, g.N, g.K);
     a.tile_n = choose_tile_n(g.M, g.N, !W_MN);
     const uint32_t w_rows = rows ? 128 : static_cast<uint32_t>(a.tile_n / 2);
-    const uint32_t x_rows = !rows ? 128 : g.M <= 32 ? 32 : g.M <= 64 ? 64 : 128;
+    const uint32_t x_rows = rows ? static_cast<uint32_t>(rows_of(g.M)) : 128;
     bool ok = make_map(&x, X, false, g.K, g.M, ldx, BK, x_rows, &why) &&
               (W_MN ? make_map(&w, W, false, g.N, g.K, ldw, 64, BK, &why)
                     : make_map(&w, W, false, g.K, g.N, ldw, BK, w_rows, &why));
