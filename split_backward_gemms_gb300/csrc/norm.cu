@@ -17,27 +17,63 @@ namespace {
 
 constexpr int MAX_WIDTH = 32768;
 
-// 8 consecutive values.
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-    const uint4 q = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+// 8 consecutive values as they lie in memory, so that what a lane has in flight or
+// keeps for later takes few registers.
+template <typename T>
+struct Raw8 {
+    static constexpr int WORDS = static_cast<int>(sizeof(T)) * 2;
+    uint32_t w[WORDS];
+    __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        for (int i = 0; i < WORDS / 4; ++i) {
+            const uint4 q = reinterpret_cast<const uint4*>(p)[i];
+            w[4 * i] = q.x;
+            w[4 * i + 1] = q.y;
+            w[4 * i + 2] = q.z;
+            w[4 * i + 3] = q.w;
+        }
     }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ float operator[](int j) const {
+        if (WORDS == 8) return __uint_as_float(w[WORDS == 8 ? j : 0]);
+        return __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+    }
+};
+using Raw16 = Raw8<__nv_bfloat16>;
+
+// Two fp32 values in one instruction.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pk2(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
 }
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    v[0] = a.x;
-    v[1] = a.y;
-    v[2] = a.z;
-    v[3] = a.w;
-    v[4] = b.x;
-    v[5] = b.y;
-    v[6] = b.z;
-    v[7] = b.w;
+__device__ __forceinline__ void up2(f32x2 v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
 }
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+template <typename R>
+__device__ __forceinline__ f32x2 pair(const R& v, int j) {
+    return pk2(v[2 * j], v[2 * j + 1]);
+}
+
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&v);
@@ -94,24 +130,19 @@ __global__ void __launch_bounds__(Team<G>::THREADS)
     const int team = threadIdx.x / (32 * G), at = threadIdx.x % (32 * G);
     const long long row = static_cast<long long>(blockIdx.x) * Team<G>::ROWS + team;
     if (row >= rows) return;
-    const T* x = X + row * width;
     const int nv = width / 8;
-    float v[V][8];
-    float sum[1] = {0.0f};
+    Raw8<T> x[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int k = at + i * 32 * G;
-        if (k < nv) {
-            load8(x + 8 * k, v[i]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
-        }
+        x[i].zero();
+        if (k < nv) x[i].load(X + row * width + 8 * k);
     }
+    float sum[1] = {0.0f};
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum[0] += v[i][j];
+        for (int j = 0; j < 8; ++j) sum[0] += x[i][j];
     team_sum<G, 1>(sum, part[0], team);
     const float mean = sum[0] / static_cast<float>(width);
     float sq[1] = {0.0f};
@@ -120,8 +151,8 @@ __global__ void __launch_bounds__(Team<G>::THREADS)
         if (at + i * 32 * G < nv)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                v[i][j] -= mean;
-                sq[0] = fmaf(v[i][j], v[i][j], sq[0]);
+                const float d = x[i][j] - mean;
+                sq[0] = fmaf(d, d, sq[0]);
             }
     team_sum<G, 1>(sq, part[1], team);
     const float rstd = 1.0f / sqrtf(sq[0] / static_cast<float>(width) + eps);
@@ -133,15 +164,19 @@ __global__ void __launch_bounds__(Team<G>::THREADS)
     for (int i = 0; i < V; ++i) {
         const int k = at + i * 32 * G;
         if (k >= nv) break;
-        float g[8], b[8] = {};
-        load8(gamma + 8 * k, g);
-        if (beta) load8(beta + 8 * k, b);
+        Raw16 g, b;
+        g.load(gamma + 8 * k);
+        b.zero();
+        if (beta) b.load(beta + 8 * k);
+        float y[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = fmaf(v[i][j] * rstd, g[j], b[j]);
-        store8(Y + row * width + 8 * k, v[i]);
+        for (int j = 0; j < 8; ++j) y[j] = fmaf((x[i][j] - mean) * rstd, g[j], b[j]);
+        store8(Y + row * width + 8 * k, y);
     }
 }
 
+// Everything a lane reads is asked for before the first sum, gamma and the
+// residual's gradient too, so that a row waits for memory once.
 template <typename T, int V, int G>
 __global__ void __launch_bounds__(Team<G>::THREADS)
     zb_layernorm_backward_input_kernel(const __nv_bfloat16* __restrict__ dY, const T* __restrict__ X,
@@ -153,111 +188,131 @@ __global__ void __launch_bounds__(Team<G>::THREADS)
     const long long row = static_cast<long long>(blockIdx.x) * Team<G>::ROWS + team;
     if (row >= rows) return;
     const int nv = width / 8;
-    const float mean = mean_in[row], rstd = rstd_in[row];
-    float xh[V][8], u[V][8];
-    float sum[2] = {0.0f, 0.0f};
+    Raw8<T> x[V], r[V];
+    Raw16 dy[V], g[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int k = at + i * 32 * G;
+        r[i].zero();
         if (k < nv) {
-            load8(X + row * width + 8 * k, xh[i]);
-            load8(dY + row * width + 8 * k, u[i]);
-            float g[8];
-            load8(gamma + 8 * k, g);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                xh[i][j] = (xh[i][j] - mean) * rstd;
-                u[i][j] *= g[j];
-                sum[0] += u[i][j];
-                sum[1] = fmaf(u[i][j], xh[i][j], sum[1]);
-            }
+            x[i].load(X + row * width + 8 * k);
+            dy[i].load(dY + row * width + 8 * k);
+            if (dR) r[i].load(dR + row * width + 8 * k);
+            g[i].load(gamma + 8 * k);
         }
     }
+    const float mean = mean_in[row], rstd = rstd_in[row];
+    float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (at + i * 32 * G < nv)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float u = dy[i][j] * g[i][j];
+                sum[0] += u;
+                sum[1] = fmaf(u, (x[i][j] - mean) * rstd, sum[1]);
+            }
     team_sum<G, 2>(sum, part, team);
     const float mu = sum[0] / static_cast<float>(width), along = sum[1] / static_cast<float>(width);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int k = at + i * 32 * G;
         if (k >= nv) break;
-        float r[8] = {};
-        if (dR) load8(dR + row * width + 8 * k, r);
+        float d[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) r[j] = fmaf(rstd, u[i][j] - mu - xh[i][j] * along, r[j]);
-        store8(dX + row * width + 8 * k, r);
-        if (dX16) store8(dX16 + row * width + 8 * k, r);
+        for (int j = 0; j < 8; ++j)
+            d[j] = fmaf(rstd, dy[i][j] * g[i][j] - mu - (x[i][j] - mean) * rstd * along, r[i][j]);
+        store8(dX + row * width + 8 * k, d);
+        if (dX16) store8(dX16 + row * width + 8 * k, d);
     }
 }
 
-// W: a cluster of 8 blocks takes 64 columns (a 128-byte line of a row in bf16),
-// each block an eighth of the rows, 32 of them at a time (8 lanes a row); the
-// blocks' sums meet in the first one's, in order.
+// W: a cluster of 8 blocks takes `vecs` (a power of two) vectors of 8 columns, its
+// blocks in turn as many rows at a time as they have threads for.  The rows go from
+// the last to the first: where W follows B, the last ones are still in L2 (8191 x
+// 2048 bf16 after B: B and W 37.0 us from the first row on, 36.3 from the last).
+// Lanes of a warp that hold the same columns meet by shuffles, warps in shared
+// memory, and blocks in each other's: block r adds the eighth part r of the columns.
+// All sums in a fixed order.
 constexpr int W_SPLIT = 8;
-constexpr int W_COLS = 64;
-constexpr int W_THREADS = 256;
+constexpr int W_THREADS = 512;
+constexpr int W_WARPS = W_THREADS / 32;
+constexpr int W_COLS = 1024;  // of a cluster, at most
 
 template <typename T>
 __global__ void __cluster_dims__(W_SPLIT, 1, 1) __launch_bounds__(W_THREADS)
     zb_layernorm_backward_weight_kernel(const __nv_bfloat16* __restrict__ dY, const T* __restrict__ X,
                                         const float* __restrict__ mean_in, const float* __restrict__ rstd_in,
                                         float* __restrict__ dgamma, float* __restrict__ dbeta, long long rows,
-                                        int width, int accumulate) {
-    __shared__ float part[W_THREADS / 32][2][W_COLS];
+                                        int width, int vecs, int accumulate) {
+    __shared__ float part[W_WARPS][2][256];  // a warp's columns: 8 for each of its first min(32, vecs) lanes
     __shared__ float block_sum[2][W_COLS];
     const uint32_t rank = zbp::cluster_ctarank();
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int c0 = (blockIdx.x / W_SPLIT) * W_COLS, col = c0 + (lane & 7) * 8;
-    const long long lo = rows * rank / W_SPLIT, hi = rows * (rank + 1) / W_SPLIT;
-    float dg[8] = {}, db[8] = {};
+    const int t = threadIdx.x, lane = t & 31, w = t >> 5;
+    const int c0 = (blockIdx.x / W_SPLIT) * vecs * 8, col = c0 + (t & (vecs - 1)) * 8;
+    const int slots = W_THREADS / vecs;  // rows of a block at a time
+    f32x2 dg2[4] = {0, 0, 0, 0}, db2[4] = {0, 0, 0, 0};
     if (col < width) {
 #pragma unroll 4
-        for (long long r = lo + (threadIdx.x >> 3); r < hi; r += W_THREADS / 8) {
-            float x[8], dy[8];
-            load8(X + r * width + col, x);
-            load8(dY + r * width + col, dy);
+        for (long long r = rows - 1 - (static_cast<long long>(rank) * slots + t / vecs); r >= 0; r -= W_SPLIT * slots) {
+            Raw8<T> x;
+            Raw16 dy;
+            x.load(X + r * width + col);
+            dy.load(dY + r * width + col);
             const float mean = mean_in[r], rstd = rstd_in[r];
+            const f32x2 minus = pk2(-mean, -mean), scale = pk2(rstd, rstd);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                dg[j] = fmaf(dy[j], (x[j] - mean) * rstd, dg[j]);
-                db[j] += dy[j];
+            for (int j = 0; j < 4; ++j) {
+                const f32x2 d = pair(dy, j);
+                dg2[j] = fma2(d, mul2(add2(pair(x, j), minus), scale), dg2[j]);
+                db2[j] = add2(db2[j], d);
             }
         }
     }
+    float dg[8], db[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        dg[j] += __shfl_xor_sync(0xffffffffu, dg[j], 8);
-        db[j] += __shfl_xor_sync(0xffffffffu, db[j], 8);
-        dg[j] += __shfl_xor_sync(0xffffffffu, dg[j], 16);
-        db[j] += __shfl_xor_sync(0xffffffffu, db[j], 16);
-        if (lane < 8) {
+    for (int j = 0; j < 4; ++j) {
+        up2(dg2[j], dg[2 * j], dg[2 * j + 1]);
+        up2(db2[j], db[2 * j], db[2 * j + 1]);
+    }
+    for (int o = vecs; o < 32; o <<= 1)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            dg[j] += __shfl_xor_sync(0xffffffffu, dg[j], o);
+            db[j] += __shfl_xor_sync(0xffffffffu, db[j], o);
+        }
+    if (lane < vecs) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
             part[w][0][lane * 8 + j] = dg[j];
             part[w][1][lane * 8 + j] = db[j];
         }
     }
     __syncthreads();
-    const int t = threadIdx.x;
-    if (t < 2 * W_COLS) {
-        float s = part[0][t / W_COLS][t % W_COLS];
-#pragma unroll
-        for (int k = 1; k < W_THREADS / 32; ++k) s += part[k][t / W_COLS][t % W_COLS];
-        block_sum[t / W_COLS][t % W_COLS] = s;
+    // warps w, w + groups, ... hold the same columns
+    const int groups = vecs > 32 ? vecs / 32 : 1, cols = vecs * 8;
+    for (int i = t; i < 2 * cols; i += W_THREADS) {
+        const int kind = i / cols, c = i - kind * cols;
+        float s = 0.0f;
+        for (int k = c / 256; k < W_WARPS; k += groups) s += part[k][kind][c % 256];
+        block_sum[kind][c] = s;
     }
     zbp::cluster_sync();
-    if (rank == 0 && t < 2 * W_COLS) {
-        const int c = c0 + t % W_COLS;
-        float* out = t < W_COLS ? dgamma : dbeta;
-        if (c < width && out) {
-            const uint32_t here = zbp::smem_u32(&block_sum[t / W_COLS][t % W_COLS]);
-            float s = 0.0f;
+    for (int i = static_cast<int>(rank) * cols / 4 + t; i < static_cast<int>(rank + 1) * cols / 4; i += W_THREADS) {
+        const int kind = i / cols, c = i - kind * cols;
+        float* out = kind ? dbeta : dgamma;
+        if (c0 + c >= width || !out) continue;
+        const uint32_t here = zbp::smem_u32(&block_sum[kind][c]);
+        float s = 0.0f;
 #pragma unroll
-            for (int b = 0; b < W_SPLIT; ++b) {
-                float v;
-                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(zbp::mapa_shared(here, b)) : "memory");
-                s += v;
-            }
-            out[c] = accumulate ? out[c] + s : s;
+        for (int b = 0; b < W_SPLIT; ++b) {
+            float v;
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(zbp::mapa_shared(here, b)) : "memory");
+            s += v;
         }
+        out[c0 + c] = accumulate ? out[c0 + c] + s : s;
     }
-    zbp::cluster_sync();  // no block leaves while the first may still read it
+    zbp::cluster_sync();  // no block leaves while another may still read its sums
 }
 
 // ---------------------------------------------------------------- host side
@@ -289,19 +344,50 @@ zb_status done() {
 
 // Calls f(V, G) with the vectors a lane and the warps a row of `width` values.
 template <typename F>
-void by_width(int64_t width, F&& f) {
+void forward_by_width(int64_t width, F&& f) {
     const int nv = static_cast<int>(width / 8);
     using std::integral_constant;
 #define ZB_CASE(v, g) f(integral_constant<int, v>(), integral_constant<int, g>())
     if (nv <= 32) ZB_CASE(1, 1);
     else if (nv <= 64) ZB_CASE(2, 1);
     else if (nv <= 128) ZB_CASE(4, 1);
+    else if (nv <= 192) ZB_CASE(3, 2);
     else if (nv <= 256) ZB_CASE(4, 2);
+    else if (nv <= 384) ZB_CASE(3, 4);
     else if (nv <= 512) ZB_CASE(4, 4);
+    else if (nv <= 768) ZB_CASE(3, 8);
     else if (nv <= 1024) ZB_CASE(4, 8);
+    else if (nv <= 1536) ZB_CASE(3, 16);
+    else if (nv <= 2048) ZB_CASE(4, 16);
+    else ZB_CASE(8, 16);
+}
+
+template <typename F>
+void backward_by_width(int64_t width, F&& f) {
+    const int nv = static_cast<int>(width / 8);
+    using std::integral_constant;
+    if (nv <= 32) ZB_CASE(1, 1);
+    else if (nv <= 64) ZB_CASE(2, 1);
+    else if (nv <= 96) ZB_CASE(3, 1);
+    else if (nv <= 128) ZB_CASE(2, 2);
+    else if (nv <= 192) ZB_CASE(3, 2);
+    else if (nv <= 256) ZB_CASE(2, 4);
+    else if (nv <= 384) ZB_CASE(3, 4);
+    else if (nv <= 512) ZB_CASE(2, 8);
+    else if (nv <= 768) ZB_CASE(3, 8);
+    else if (nv <= 1024) ZB_CASE(2, 16);
+    else if (nv <= 1536) ZB_CASE(3, 16);
     else if (nv <= 2048) ZB_CASE(4, 16);
     else ZB_CASE(8, 16);
 #undef ZB_CASE
+}
+
+// Vectors of 8 columns a cluster of W takes: the fewest, at least 4 (64 bytes a
+// row), that leave no more than 32 clusters, which are resident at once.
+int w_vecs(int64_t width) {
+    int v = 4;
+    while (width / 8 > 32LL * v) v *= 2;
+    return v;
 }
 
 unsigned blocks_of(int64_t rows, int per) { return static_cast<unsigned>((rows + per - 1) / per); }
@@ -319,7 +405,7 @@ extern "C" zb_status zb_layernorm_forward(const zb_layernorm* n, const void* X, 
         return zb::fail(ZB_ERR_ALIGN, "zb_layernorm_forward: pointers must be 16-byte aligned (mean, rstd: 4)");
     auto go = [&](auto zero) {
         using T = decltype(zero);
-        by_width(n->width, [&](auto v, auto g) {
+        forward_by_width(n->width, [&](auto v, auto g) {
             constexpr int V = v(), G = g();
             zb_layernorm_forward_kernel<T, V, G>
                 <<<blocks_of(n->rows, Team<G>::ROWS), Team<G>::THREADS, 0, static_cast<cudaStream_t>(stream)>>>(
@@ -347,7 +433,7 @@ extern "C" zb_status zb_layernorm_backward_input(const zb_layernorm* n, const vo
         return zb::fail(ZB_ERR_ALIGN, "zb_layernorm_backward_input: pointers must be 16-byte aligned (mean, rstd: 4)");
     auto go = [&](auto zero) {
         using T = decltype(zero);
-        by_width(n->width, [&](auto v, auto g) {
+        backward_by_width(n->width, [&](auto v, auto g) {
             constexpr int V = v(), G = g();
             zb_layernorm_backward_input_kernel<T, V, G>
                 <<<blocks_of(n->rows, Team<G>::ROWS), Team<G>::THREADS, 0, static_cast<cudaStream_t>(stream)>>>(
@@ -373,12 +459,13 @@ extern "C" zb_status zb_layernorm_backward_weight(const zb_layernorm* n, const v
     if (off16(dY) || off16(X) || off4(mean) || off4(rstd) || off4(dgamma) || off4(dbeta))
         return zb::fail(ZB_ERR_ALIGN,
                         "zb_layernorm_backward_weight: dY and X must be 16-byte aligned (fp32 vectors: 4)");
-    const unsigned blocks = blocks_of(n->width, W_COLS) * W_SPLIT;
+    const int vecs = w_vecs(n->width);
+    const unsigned blocks = blocks_of(n->width, vecs * 8) * W_SPLIT;
     auto go = [&](auto zero) {
         using T = decltype(zero);
         zb_layernorm_backward_weight_kernel<T><<<blocks, W_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(
             static_cast<const __nv_bfloat16*>(dY), static_cast<const T*>(X), mean, rstd, dgamma, dbeta, n->rows,
-            static_cast<int>(n->width), accumulate != 0);
+            static_cast<int>(n->width), vecs, accumulate != 0);
     };
     if (n->dtype == ZB_DT_BF16)
         go(__nv_bfloat16());
