@@ -77,13 +77,14 @@ constexpr int SORT_BLOCKS = 8;
 constexpr int SORT_THREADS = 1024;
 constexpr int SORT_WARPS = SORT_THREADS / 32;
 constexpr int SORT_BITS = 10;  // of a digit, at most
+constexpr int SORT_HELD = 8;   // tokens a lane holds in registers from counting to placing
 constexpr size_t sort_smem(int bits) { return (static_cast<size_t>(SORT_WARPS + 1) << bits) * 4; }
 
 struct SortArgs {
     const int* ids;
     int tokens, bits, passes;  // bits of a digit
     uint32_t vocab;
-    uint32_t *keys[2], *vals[2];
+    uint2* pairs[2];  // (key, token), placed by one pass and read by the next
     int *order, *sorted_id;
 };
 
@@ -101,23 +102,41 @@ __global__ void __cluster_dims__(SORT_BLOCKS, 1, 1) __launch_bounds__(SORT_THREA
     const int lo = static_cast<int>(n * part / (SORT_BLOCKS * SORT_WARPS));
     const int hi = static_cast<int>(n * (part + 1) / (SORT_BLOCKS * SORT_WARPS));
     uint32_t* mine = hist + warp * digits;
+    zbp::allow_dependent_launch();
+    constexpr int STEP = 32 * SORT_HELD;
     for (int pass = 0; pass < a.passes; ++pass) {
-        const uint32_t* src_key = a.keys[(pass + 1) & 1];
-        const uint32_t* src_val = a.vals[(pass + 1) & 1];
+        const uint2* src = a.pairs[(pass + 1) & 1];
         const int shift = pass * a.bits;
-        auto key_at = [&](int i) { return pass == 0 ? key_of(a.ids[i], a.vocab) : __ldcg(src_key + i); };
+        uint2 held[SORT_HELD];
+        auto fetch = [&](int i0) {
+#pragma unroll
+            for (int k = 0; k < SORT_HELD; ++k) {
+                const int i = i0 + k * 32 + lane;
+                if (i < hi)
+                    held[k] = pass == 0 ? make_uint2(key_of(a.ids[i], a.vocab), static_cast<uint32_t>(i)) : __ldcg(src + i);
+            }
+        };
         auto digit_of = [&](uint32_t k) { return (k >> shift) & static_cast<uint32_t>(digits - 1); };
+        fetch(lo);
         for (int d = lane; d < digits; d += 32) mine[d] = 0;
         __syncwarp();
-        for (int i = lo + lane; i < hi; i += 32) atomicAdd(&mine[digit_of(key_at(i))], 1u);
+        for (int i0 = lo; i0 < hi; i0 += STEP) {
+            if (i0 > lo) fetch(i0);
+#pragma unroll
+            for (int k = 0; k < SORT_HELD; ++k)
+                if (i0 + k * 32 + lane < hi) atomicAdd(&mine[digit_of(held[k].x)], 1u);
+        }
         __syncthreads();
         // each warp's count becomes the number of such tokens in the warps before it
         uint32_t here = 0;
         if (t < digits) {
+            uint32_t c[SORT_WARPS];
+#pragma unroll
+            for (int w = 0; w < SORT_WARPS; ++w) c[w] = hist[w * digits + t];
+#pragma unroll
             for (int w = 0; w < SORT_WARPS; ++w) {
-                const uint32_t c = hist[w * digits + t];
                 hist[w * digits + t] = here;
-                here += c;
+                here += c[w];
             }
             total[t] = here;
         }
@@ -126,12 +145,14 @@ __global__ void __cluster_dims__(SORT_BLOCKS, 1, 1) __launch_bounds__(SORT_THREA
         uint32_t before = 0, all = 0;
         if (t < digits) {
             const uint32_t at = zbp::smem_u32(&total[t]);
+            uint32_t c[SORT_BLOCKS];
+#pragma unroll
+            for (int b = 0; b < SORT_BLOCKS; ++b)
+                asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(c[b]) : "r"(zbp::mapa_shared(at, b)) : "memory");
 #pragma unroll
             for (int b = 0; b < SORT_BLOCKS; ++b) {
-                uint32_t c;
-                asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(c) : "r"(zbp::mapa_shared(at, b)) : "memory");
-                if (b < static_cast<int>(rank)) before += c;
-                all += c;
+                if (b < static_cast<int>(rank)) before += c[b];
+                all += c[b];
             }
         }
         uint32_t sum = all;  // over the digits up to this one
@@ -142,30 +163,32 @@ __global__ void __cluster_dims__(SORT_BLOCKS, 1, 1) __launch_bounds__(SORT_THREA
         }
         if (lane == 31) warp_total[warp] = sum;
         zbp::cluster_sync();  // also: every block has read the totals
-        for (int w = 0; w < warp; ++w) sum += warp_total[w];
-        if (t < digits) total[t] = sum - all + before;
+        uint32_t left = lane < warp ? warp_total[lane] : 0u;
+        left = __reduce_add_sync(0xffffffffu, left);
+        if (t < digits) total[t] = sum + left - all + before;
         __syncthreads();
         const bool last = pass + 1 == a.passes;
-        for (int i0 = lo; i0 < hi; i0 += 32) {
-            const int i = i0 + lane;
-            const bool on = i < hi;
-            const uint32_t key = on ? key_at(i) : 0u;
-            const uint32_t d = on ? digit_of(key) : ~0u;
-            const uint32_t peers = __match_any_sync(0xffffffffu, d);
-            const int before_me = __popc(peers & ((1u << lane) - 1u));
-            uint32_t place = 0;
-            if (on) place = total[d] + mine[d] + static_cast<uint32_t>(before_me);
-            __syncwarp();
-            if (on && before_me == 0) mine[d] += static_cast<uint32_t>(__popc(peers));
-            __syncwarp();
-            if (on) {
-                const uint32_t val = pass == 0 ? static_cast<uint32_t>(i) : __ldcg(src_val + i);
-                if (last) {
-                    a.order[place] = static_cast<int>(val);
-                    a.sorted_id[place] = id_of(key, a.vocab);
-                } else {
-                    a.keys[pass & 1][place] = key;
-                    a.vals[pass & 1][place] = val;
+        for (int i0 = lo; i0 < hi; i0 += STEP) {
+            if (hi - lo > STEP) fetch(i0);
+#pragma unroll
+            for (int k = 0; k < SORT_HELD; ++k) {
+                if (i0 + k * 32 >= hi) break;
+                const bool on = i0 + k * 32 + lane < hi;
+                const uint32_t d = on ? digit_of(held[k].x) : ~0u;
+                const uint32_t peers = __match_any_sync(0xffffffffu, d);
+                const int before_me = __popc(peers & ((1u << lane) - 1u));
+                uint32_t place = 0;
+                if (on) place = total[d] + mine[d] + static_cast<uint32_t>(before_me);
+                __syncwarp();
+                if (on && before_me == 0) mine[d] += static_cast<uint32_t>(__popc(peers));
+                __syncwarp();
+                if (on) {
+                    if (last) {
+                        a.order[place] = static_cast<int>(held[k].y);
+                        a.sorted_id[place] = id_of(held[k].x, a.vocab);
+                    } else {
+                        a.pairs[pass & 1][place] = held[k];
+                    }
                 }
             }
         }
@@ -174,8 +197,9 @@ __global__ void __cluster_dims__(SORT_BLOCKS, 1, 1) __launch_bounds__(SORT_THREA
 }
 
 // Few tokens: a token's place is the number of tokens that go before it.  One
-// block, every key in shared memory.
-constexpr int RANK_TOKENS = 1024;
+// block, every key in shared memory.  us of this and of the radix sort: 16 tokens
+// RANK_A, 512 tokens RANK_B; 1000 tokens 34.0 and 9.3.
+constexpr int RANK_TOKENS = 512;
 
 __global__ void __launch_bounds__(RANK_TOKENS)
     zb_embedding_rank_kernel(const int* __restrict__ ids, int tokens, uint32_t vocab, int* __restrict__ order,
@@ -205,10 +229,10 @@ __global__ void __launch_bounds__(RANK_TOKENS)
 // piece goes to the workspace (a row for the run that came in from the left, one
 // for the run that goes on to the right), and a second kernel adds such a run's
 // parts in order.  Without accumulation blocks of their own write zeros to the
-// rows of the ids that do not occur.
+// rows of the ids that do not occur, which warps find by searching the sorted ids.
 constexpr int PIECE = 32;
 constexpr int GRAD_THREADS = 256;
-constexpr int ZERO_ROWS = GRAD_THREADS / 32;
+constexpr int ZERO_ROWS = 8;  // of a warp
 
 struct GradArgs {
     const int* order;
@@ -217,117 +241,224 @@ struct GradArgs {
     float* dE;
     float4* part;  // [pieces][2][w4]
     int tokens, pieces, w4, col_blocks;
+    long long piece_blocks, zero_blocks;
     uint32_t vocab;
     int accumulate;
     float scale;
 };
 
-__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-    const uint2 q = *reinterpret_cast<const uint2*>(p);
-    return make_float4(__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xffff0000u), __uint_as_float(q.y << 16),
-                       __uint_as_float(q.y & 0xffff0000u));
-}
+// 4 consecutive values as they lie in memory.
+template <typename T>
+struct Four;
+template <>
+struct Four<float> {
+    float4 q;
+    __device__ __forceinline__ void load(const float* p) { q = *reinterpret_cast<const float4*>(p); }
+    __device__ __forceinline__ float4 get() const { return q; }
+};
+template <>
+struct Four<__nv_bfloat16> {
+    uint2 q;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { q = *reinterpret_cast<const uint2*>(p); }
+    __device__ __forceinline__ float4 get() const {
+        return make_float4(__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xffff0000u), __uint_as_float(q.y << 16),
+                           __uint_as_float(q.y & 0xffff0000u));
+    }
+};
 __device__ __forceinline__ void add4(float4& a, const float4& b) {
     a.x += b.x;
     a.y += b.y;
     a.z += b.z;
     a.w += b.w;
 }
-__device__ __forceinline__ void finish(const GradArgs& a, int id, int c, const float4& s) {
-    float4* out = reinterpret_cast<float4*>(a.dE) + static_cast<long long>(id) * a.w4 + c;
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (a.accumulate) v = *out;
-    v.x = fmaf(a.scale, s.x, v.x);
-    v.y = fmaf(a.scale, s.y, v.y);
-    v.z = fmaf(a.scale, s.z, v.z);
-    v.w = fmaf(a.scale, s.w, v.w);
-    *out = v;
+__device__ __forceinline__ float4* row_of(const GradArgs& a, int id, int c) {
+    return reinterpret_cast<float4*>(a.dE) + static_cast<long long>(id) * a.w4 + c;
+}
+__device__ __forceinline__ float4 scaled(const GradArgs& a, const float4& s, const float4& old) {
+    return make_float4(fmaf(a.scale, s.x, old.x), fmaf(a.scale, s.y, old.y), fmaf(a.scale, s.z, old.z),
+                       fmaf(a.scale, s.w, old.w));
 }
 
-// The warp's search for `id` among the sorted ids (as unsigned: -1 is the last).
-__device__ __forceinline__ bool occurs(const int* sorted_id, int n, uint32_t id) {
+// The warp's searches for the first sorted id (as unsigned: -1 is the last) at
+// least `a`, and at least `b`, 32 probes a step.
+__device__ __forceinline__ void lower_bounds(const int* sorted_id, int n, uint32_t a, uint32_t b, int& at_a, int& at_b) {
     const int lane = threadIdx.x & 31;
-    int lo = 0, len = n;  // the first entry >= id lies in [lo, lo + len]
-    while (len > 0) {
-        const int step = (len + 31) / 32;
-        const int at = lo + (lane + 1) * step - 1;
-        const int end = lo + len;
-        const uint32_t v = at < end ? static_cast<uint32_t>(sorted_id[at]) : ~0u;
-        if (__any_sync(0xffffffffu, at < end && v == id)) return true;
-        const int less = __popc(__ballot_sync(0xffffffffu, at < end && v < id));
-        lo += less * step;
-        len = min(step - 1, end - lo);
+    int lo[2] = {0, 0}, len[2] = {n, n};  // the place lies in [lo, lo + len]
+    const uint32_t want[2] = {a, b};
+    while (len[0] > 0 || len[1] > 0) {
+        uint32_t v[2];
+        int step[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            step[k] = (len[k] + 31) / 32;
+            const int at = lo[k] + (lane + 1) * step[k] - 1;
+            v[k] = len[k] > 0 && at < lo[k] + len[k] ? static_cast<uint32_t>(sorted_id[at]) : ~0u;
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (len[k] <= 0) continue;
+            const int end = lo[k] + len[k];
+            lo[k] = min(end, lo[k] + __popc(__ballot_sync(0xffffffffu, v[k] < want[k])) * step[k]);
+            len[k] = min(step[k] - 1, end - lo[k]);
+        }
     }
-    return false;
+    at_a = lo[0];
+    at_b = lo[1];
 }
 
-template <typename T>
-__global__ void __launch_bounds__(GRAD_THREADS) zb_embedding_backward_kernel(const GradArgs a, int zero_blocks) {
-    if (static_cast<int>(blockIdx.x) < zero_blocks) {
-        const long long row = static_cast<long long>(blockIdx.x) * ZERO_ROWS + (threadIdx.x >> 5);
-        if (row >= a.vocab) return;
-        if (occurs(a.sorted_id, a.tokens, static_cast<uint32_t>(row))) return;
-        float4* out = reinterpret_cast<float4*>(a.dE) + row * a.w4;
-        for (int c = threadIdx.x & 31; c < a.w4; c += 32) out[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+// Zeros for those of a warp's ZERO_ROWS rows whose ids do not occur.
+__device__ void zero_rows(const GradArgs& a, long long chunk) {
+    const int lane = threadIdx.x & 31;
+    const long long row0 = chunk * ZERO_ROWS;
+    if (row0 >= a.vocab) return;
+    const uint32_t first = static_cast<uint32_t>(row0), rows = min(static_cast<uint32_t>(ZERO_ROWS), a.vocab - first);
+    int lo, hi;
+    lower_bounds(a.sorted_id, a.tokens, first, first + rows, lo, hi);
+    uint32_t occurs = 0;  // a bit a row
+    if (hi - lo <= 64) {
+        for (int i = lo; i < hi; i += 32) {
+            uint32_t bit = 0;
+            if (i + lane < hi) {
+                const uint32_t r = static_cast<uint32_t>(a.sorted_id[i + lane]) - first;
+                if (r < rows) bit = 1u << r;
+            }
+            occurs |= __reduce_or_sync(0xffffffffu, bit);
+        }
+    } else {
+        // some ids are frequent: each row's own first place
+        int at = lo;
+        for (uint32_t r = 0; r < rows; ++r) {
+            int next, unused;
+            lower_bounds(a.sorted_id, a.tokens, first + r + 1, 0, next, unused);
+            if (next > at) occurs |= 1u << r;
+            at = next;
+        }
+    }
+    const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (uint32_t r = 0; r < rows; ++r) {
+        if ((occurs >> r) & 1u) continue;
+        float4* out = reinterpret_cast<float4*>(a.dE) + (row0 + r) * a.w4;
+        for (int c = lane; c < a.w4; c += 32) out[c] = zero;
+    }
+}
+
+// ADD: the sums are added to what dE holds (`accumulate`).
+template <typename T, bool ADD>
+__global__ void __launch_bounds__(GRAD_THREADS) zb_embedding_backward_kernel(const GradArgs a) {
+    zbp::grid_dependency_wait();
+    zbp::allow_dependent_launch();
+    // blocks that write zeros are spread evenly among the others, whose reads they overlap
+    const long long all = a.piece_blocks + a.zero_blocks, zeros = blockIdx.x * a.zero_blocks / all;
+    if ((blockIdx.x + 1) * a.zero_blocks / all > zeros) {
+        zero_rows(a, zeros * (GRAD_THREADS / 32) + (threadIdx.x >> 5));
         return;
     }
     __shared__ int id_s[PIECE + 2], tok_s[PIECE];
-    const int b = static_cast<int>(blockIdx.x) - zero_blocks;
-    const int piece = b / a.col_blocks;
-    const int c = (b - piece * a.col_blocks) * GRAD_THREADS + threadIdx.x;
+    const int block = static_cast<int>(blockIdx.x - zeros), piece = block / a.col_blocks;
+    const int c = (block - piece * a.col_blocks) * GRAD_THREADS + threadIdx.x;
     const int first = piece * PIECE, n = min(PIECE, a.tokens - first);
     if (threadIdx.x < PIECE + 2) {
         const int i = first - 1 + static_cast<int>(threadIdx.x);
         id_s[threadIdx.x] = i >= 0 && i < a.tokens ? a.sorted_id[i] : -1;
         if (threadIdx.x < PIECE) {
-            const int tok = threadIdx.x < n ? a.order[first + threadIdx.x] : 0;
+            const int tok = static_cast<int>(threadIdx.x) < n ? a.order[first + threadIdx.x] : 0;
             tok_s[threadIdx.x] = tok >= 0 && tok < a.tokens ? tok : 0;
         }
     }
     __syncthreads();
     if (c >= a.w4) return;
     const T* dY = static_cast<const T*>(a.dY) + 4 * c;
-    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const float4 none = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float4 sum = none;
+    // the run at hand came in from the left
     bool from_left = id_s[0] == id_s[1];
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) {
-        const int id = id_s[i + 1];
-        add4(sum, load4(dY + static_cast<long long>(tok_s[i]) * (4 * a.w4)));
-        const bool more = id_s[i + 2] == id;  // the run goes on
-        if (more && i + 1 < n) continue;
-        if (static_cast<uint32_t>(id) < a.vocab) {
-            if (from_left)
-                a.part[(2LL * piece) * a.w4 + c] = sum;
-            else if (more)
-                a.part[(2LL * piece + 1) * a.w4 + c] = sum;
-            else
-                finish(a, id, c, sum);
+    // U rows at a time: all of them, and what dE holds for the runs that end among
+    // them, are asked for before the first is added
+    constexpr int U = 8;
+    for (int i0 = 0; i0 < n; i0 += U) {
+        Four<T> v[U];
+        float4 old[ADD ? U : 1];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i0 + u < n) v[u].load(dY + static_cast<long long>(tok_s[i0 + u]) * (4 * a.w4));
+        if (ADD) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int id = i0 + u < n ? id_s[i0 + u + 1] : -1;
+                old[ADD ? u : 0] = none;
+                if (static_cast<uint32_t>(id) < a.vocab && id_s[i0 + u + 2] != id) old[ADD ? u : 0] = *row_of(a, id, c);
+            }
         }
-        sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        from_left = false;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u;
+            if (i >= n) break;
+            const int id = id_s[i + 1];
+            add4(sum, v[u].get());
+            const bool more = id_s[i + 2] == id;  // the run goes on
+            if (more && i + 1 < n) continue;
+            if (static_cast<uint32_t>(id) < a.vocab) {
+                if (from_left)
+                    a.part[(2LL * piece) * a.w4 + c] = sum;
+                else if (more)
+                    a.part[(2LL * piece + 1) * a.w4 + c] = sum;
+                else
+                    *row_of(a, id, c) = scaled(a, sum, ADD ? old[ADD ? u : 0] : none);
+            }
+            sum = none;
+            from_left = false;
+        }
     }
 }
 
-// Adds the parts of the run that starts in piece p and goes on after it.
-constexpr int JOIN_THREADS = 64;
+// Adds the parts of the run that starts in piece p and goes on after it.  Each
+// quarter of the block's threads takes a quarter of the parts, 8 at a time; the
+// quarters' sums are added in order.
+constexpr int JOIN_COLS = 64, JOIN_QUARTERS = 4;
 
-__global__ void __launch_bounds__(JOIN_THREADS) zb_embedding_join_kernel(const GradArgs a, int col_blocks) {
+__global__ void __launch_bounds__(JOIN_COLS * JOIN_QUARTERS) zb_embedding_join_kernel(const GradArgs a, int col_blocks) {
+    zbp::grid_dependency_wait();
     const int piece = blockIdx.x / col_blocks;
-    const int c = (blockIdx.x - piece * col_blocks) * JOIN_THREADS + threadIdx.x;
     const int first = piece * PIECE, end = first + PIECE;  // not the last piece
     const int id = a.sorted_id[end - 1];
     if (static_cast<uint32_t>(id) >= a.vocab || a.sorted_id[end] != id) return;
     // a run that came in from the left and fills the piece is joined by an earlier block
     if (first > 0 && a.sorted_id[first] == id && a.sorted_id[first - 1] == id) return;
-    if (c >= a.w4) return;
-    float4 sum = a.part[(2LL * piece + 1) * a.w4 + c];
-    for (int p = piece + 1; p < a.pieces; ++p) {
-        add4(sum, a.part[2LL * p * a.w4 + c]);
-        const int next = (p + 1) * PIECE;
-        if (next >= a.tokens || a.sorted_id[next] != id || a.sorted_id[next - 1] != id) break;
+    // pieces that the run fills and leaves, then the one that it ends in
+    int last = piece + 1;
+    for (const int lane = threadIdx.x & 31;; last += 32) {
+        const int p = last + lane, next = (p + 1) * PIECE;
+        const bool on = p + 1 < a.pieces && a.sorted_id[next - 1] == id && a.sorted_id[next] == id;
+        const uint32_t stop = ~__ballot_sync(0xffffffffu, on);
+        if (stop) {
+            last += __ffs(static_cast<int>(stop)) - 1;
+            break;
+        }
     }
-    finish(a, id, c, sum);
+    const int c = (blockIdx.x - piece * col_blocks) * JOIN_COLS + threadIdx.x % JOIN_COLS;
+    const int quarter = threadIdx.x / JOIN_COLS, parts = last - piece;
+    const int lo = piece + 1 + static_cast<int>(static_cast<long long>(parts) * quarter / JOIN_QUARTERS);
+    const int hi = piece + 1 + static_cast<int>(static_cast<long long>(parts) * (quarter + 1) / JOIN_QUARTERS);
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (c < a.w4) {
+        if (quarter == 0) sum = a.part[(2LL * piece + 1) * a.w4 + c];
+        for (int p0 = lo; p0 < hi; p0 += 8) {
+            float4 v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (p0 + u < hi) v[u] = a.part[2LL * (p0 + u) * a.w4 + c];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (p0 + u < hi) add4(sum, v[u]);
+        }
+    }
+    __shared__ float4 quarters[JOIN_QUARTERS - 1][JOIN_COLS];
+    if (quarter > 0) quarters[quarter - 1][threadIdx.x % JOIN_COLS] = sum;
+    __syncthreads();
+    if (quarter > 0 || c >= a.w4) return;
+#pragma unroll
+    for (int q = 0; q + 1 < JOIN_QUARTERS; ++q) add4(sum, quarters[q][threadIdx.x]);
+    *row_of(a, id, c) = scaled(a, sum, a.accumulate ? *row_of(a, id, c) : make_float4(0.0f, 0.0f, 0.0f, 0.0f));
 }
 
 // ---------------------------------------------------------------- host side
@@ -350,6 +481,22 @@ zb_status launched(const char* who) {
     if (e != cudaSuccess) return zb::fail(ZB_ERR_CUDA, std::string(who) + " launch: " + cudaGetErrorString(e));
     zb::clear_error();
     return ZB_OK;
+}
+
+// Launches a kernel that waits for the one before it in the stream by itself
+// (grid_dependency_wait), so that its blocks may be set up before that one ends.
+template <typename K, typename... Args>
+cudaError_t launch_after(K kern, long long blocks, int threads, void* stream, const Args&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 zb_status done() {
@@ -428,11 +575,7 @@ extern "C" zb_status zb_embedding_sort(const zb_embedding* e, const int32_t* ids
     a.passes = (bits + SORT_BITS - 1) / SORT_BITS;
     a.bits = (bits + a.passes - 1) / a.passes;
     a.vocab = vocab;
-    uint32_t* ws = static_cast<uint32_t*>(workspace);
-    for (int i = 0; i < 2; ++i) {
-        a.keys[i] = ws + static_cast<size_t>(2 * i) * n;
-        a.vals[i] = ws + static_cast<size_t>(2 * i + 1) * n;
-    }
+    for (int i = 0; i < 2; ++i) a.pairs[i] = static_cast<uint2*>(workspace) + static_cast<size_t>(i) * n;
     a.order = order;
     a.sorted_id = sorted_id;
     const cudaError_t err = cudaFuncSetAttribute(zb_embedding_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -467,20 +610,25 @@ extern "C" zb_status zb_embedding_backward(const zb_embedding* e, const int32_t*
     a.vocab = static_cast<uint32_t>(e->vocab);
     a.accumulate = accumulate != 0;
     a.scale = e->scale;
-    const long long zero = accumulate ? 0 : (e->vocab + ZERO_ROWS - 1) / ZERO_ROWS;
-    const long long blocks = zero + static_cast<long long>(a.pieces) * a.col_blocks;
-    const int join_cols = (a.w4 + JOIN_THREADS - 1) / JOIN_THREADS;
+    constexpr int per = ZERO_ROWS * (GRAD_THREADS / 32);
+    a.zero_blocks = accumulate ? 0 : (e->vocab + per - 1) / per;
+    a.piece_blocks = static_cast<long long>(a.pieces) * a.col_blocks;
+    const long long blocks = a.piece_blocks + a.zero_blocks;
+    const int join_cols = (a.w4 + JOIN_COLS - 1) / JOIN_COLS;
     const long long joins = static_cast<long long>(std::max(a.pieces - 1, 0)) * join_cols;
     if (blocks > 0x7fffffffLL || joins > 0x7fffffffLL)
         return zb::fail(ZB_ERR_SHAPE, "zb_embedding_backward: too many elements");
     if (blocks == 0) return done();
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    auto go = [&](auto kern) { return launch_after(kern, blocks, GRAD_THREADS, stream, a); };
+    cudaError_t err;
     if (e->dtype == ZB_DT_BF16)
-        zb_embedding_backward_kernel<__nv_bfloat16>
-            <<<static_cast<unsigned>(blocks), GRAD_THREADS, 0, st>>>(a, static_cast<int>(zero));
+        err = accumulate ? go(zb_embedding_backward_kernel<__nv_bfloat16, true>)
+                         : go(zb_embedding_backward_kernel<__nv_bfloat16, false>);
     else
-        zb_embedding_backward_kernel<float>
-            <<<static_cast<unsigned>(blocks), GRAD_THREADS, 0, st>>>(a, static_cast<int>(zero));
-    if (joins > 0) zb_embedding_join_kernel<<<static_cast<unsigned>(joins), JOIN_THREADS, 0, st>>>(a, join_cols);
+        err = accumulate ? go(zb_embedding_backward_kernel<float, true>) : go(zb_embedding_backward_kernel<float, false>);
+    if (err == cudaSuccess && joins > 0)
+        err = launch_after(zb_embedding_join_kernel, joins, JOIN_COLS * JOIN_QUARTERS, stream, a, join_cols);
+    if (err != cudaSuccess)
+        return zb::fail(ZB_ERR_CUDA, std::string("zb_embedding_backward launch: ") + cudaGetErrorString(err));
     return launched("zb_embedding_backward");
 }
