@@ -67,8 +67,7 @@ __device__ __forceinline__ uint32_t key_of(int id, uint32_t vocab) {
 }
 __device__ __forceinline__ int id_of(uint32_t key, uint32_t vocab) { return key < vocab ? static_cast<int>(key) : -1; }
 
-// A stable radix sort by one cluster of 8 blocks, digits from the lowest up.  A
-// block owns an eighth of the tokens and a warp a contiguous part of them, so
+// A stable radix sort by one cluster of 8 blocks, digits from the lowest up.  A block owns an eighth of the tokens and a warp a contiguous part of them, so
 // that a digit's tokens are placed in the order (block, warp, token): each warp
 // counts its digits, the counts are summed over warps and blocks (through
 // distributed shared memory) into the first place of each warp's tokens of each
@@ -130,13 +129,16 @@ __global__ void __cluster_dims__(SORT_BLOCKS, 1, 1) __launch_bounds__(SORT_THREA
         // each warp's count becomes the number of such tokens in the warps before it
         uint32_t here = 0;
         if (t < digits) {
-            uint32_t c[SORT_WARPS];
+#pragma unroll 1
+            for (int w0 = 0; w0 < SORT_WARPS; w0 += 8) {
+                uint32_t c[8];
 #pragma unroll
-            for (int w = 0; w < SORT_WARPS; ++w) c[w] = hist[w * digits + t];
+                for (int w = 0; w < 8; ++w) c[w] = hist[(w0 + w) * digits + t];
 #pragma unroll
-            for (int w = 0; w < SORT_WARPS; ++w) {
-                hist[w * digits + t] = here;
-                here += c[w];
+                for (int w = 0; w < 8; ++w) {
+                    hist[(w0 + w) * digits + t] = here;
+                    here += c[w];
+                }
             }
             total[t] = here;
         }
@@ -197,29 +199,35 @@ __global__ void __cluster_dims__(SORT_BLOCKS, 1, 1) __launch_bounds__(SORT_THREA
 }
 
 // Few tokens: a token's place is the number of tokens that go before it.  One
-// block, every key in shared memory.  us of this and of the radix sort: 16 tokens
-// RANK_A, 512 tokens RANK_B; 1000 tokens 34.0 and 9.3.
-constexpr int RANK_TOKENS = 512;
+// block, every key in shared memory.  us of this and of the radix sort: 128 tokens
+// 2.5 and 8.4, 256 tokens 4.1 and 8.4 (of 32000 ids).
+constexpr int RANK_TOKENS = 256;
+constexpr int RANK_THREADS = 1024;
 
-__global__ void __launch_bounds__(RANK_TOKENS)
-    zb_embedding_rank_kernel(const int* __restrict__ ids, int tokens, uint32_t vocab, int* __restrict__ order,
+__global__ void __launch_bounds__(RANK_THREADS)
+    zb_embedding_rank_kernel(const int* __restrict__ ids, int tokens, int lanes, uint32_t vocab, int* __restrict__ order,
                              int* __restrict__ sorted_id) {
+    // `lanes` (a power of two, neighbours in a warp) share the keys of a token
     __shared__ __align__(16) uint32_t keys[RANK_TOKENS];
-    const int t = threadIdx.x;
+    const int t = threadIdx.x / lanes, s = threadIdx.x & (lanes - 1);
     const int n4 = (tokens + 3) / 4;
-    const uint32_t key = t < tokens ? key_of(ids[t], vocab) : ~0u;  // past the end: behind every key
-    if (t < 4 * n4) keys[t] = key;
+    if (threadIdx.x < 4 * n4)
+        keys[threadIdx.x] = static_cast<int>(threadIdx.x) < tokens ? key_of(ids[threadIdx.x], vocab) : ~0u;  // behind every key
     __syncthreads();
-    if (t >= tokens) return;
+    const uint32_t key = keys[min(t, tokens - 1)];
     int place = 0;
-    for (int j = 0; j < n4; ++j) {
+#pragma unroll 4
+    for (int j = s; j < n4; j += lanes) {
         const uint4 k = reinterpret_cast<const uint4*>(keys)[j];
         const uint32_t v[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) place += v[i] < key || (v[i] == key && 4 * j + i < t);
+        for (int i = 0; i < 4; ++i) place += v[i] < key + (4 * j + i < t ? 1u : 0u);
     }
-    order[place] = t;
-    sorted_id[place] = id_of(key, vocab);
+    for (int o = 1; o < lanes; o <<= 1) place += __shfl_xor_sync(0xffffffffu, place, o);
+    if (s == 0 && t < tokens) {
+        order[place] = t;
+        sorted_id[place] = id_of(key, vocab);
+    }
 }
 
 // ---------------------------------------------------------------- gradient
@@ -411,37 +419,25 @@ __global__ void __launch_bounds__(GRAD_THREADS) zb_embedding_backward_kernel(con
     }
 }
 
-// Adds the parts of the run that starts in piece p and goes on after it.  Each
-// quarter of the block's threads takes a quarter of the parts, 8 at a time; the
-// quarters' sums are added in order.
-constexpr int JOIN_COLS = 64, JOIN_QUARTERS = 4;
+// Adds the parts of the runs that start in a piece and go on after it.  A block has
+// JOIN_PIECES pieces, of which each group of JOIN_COLS threads (4 columns each) joins
+// the run of one, if it has up to JOIN_SHORT parts to add; longer ones are joined by
+// the whole block, a quarter of the parts each, the quarters' sums in order.  (A
+// block for each piece, most of which have nothing to do: 17 us for 16384 tokens of
+// 32000 ids, width 2048, where this takes 8.5.)
+constexpr int JOIN_COLS = 64, JOIN_PIECES = 4, JOIN_SHORT = 8;
 
-__global__ void __launch_bounds__(JOIN_COLS * JOIN_QUARTERS) zb_embedding_join_kernel(const GradArgs a, int col_blocks) {
+__global__ void __launch_bounds__(JOIN_COLS * JOIN_PIECES) zb_embedding_join_kernel(const GradArgs a, int col_blocks) {
+    __shared__ int last_s[JOIN_PIECES];  // a run's last piece; 0: no run to join
+    __shared__ float4 quarters[JOIN_PIECES][JOIN_COLS];
     zbp::grid_dependency_wait();
-    const int piece = blockIdx.x / col_blocks;
-    const int first = piece * PIECE, end = first + PIECE;  // not the last piece
-    const int id = a.sorted_id[end - 1];
-    if (static_cast<uint32_t>(id) >= a.vocab || a.sorted_id[end] != id) return;
-    // a run that came in from the left and fills the piece is joined by an earlier block
-    if (first > 0 && a.sorted_id[first] == id && a.sorted_id[first - 1] == id) return;
-    // pieces that the run fills and leaves, then the one that it ends in
-    int last = piece + 1;
-    for (const int lane = threadIdx.x & 31;; last += 32) {
-        const int p = last + lane, next = (p + 1) * PIECE;
-        const bool on = p + 1 < a.pieces && a.sorted_id[next - 1] == id && a.sorted_id[next] == id;
-        const uint32_t stop = ~__ballot_sync(0xffffffffu, on);
-        if (stop) {
-            last += __ffs(static_cast<int>(stop)) - 1;
-            break;
-        }
-    }
-    const int c = (blockIdx.x - piece * col_blocks) * JOIN_COLS + threadIdx.x % JOIN_COLS;
-    const int quarter = threadIdx.x / JOIN_COLS, parts = last - piece;
-    const int lo = piece + 1 + static_cast<int>(static_cast<long long>(parts) * quarter / JOIN_QUARTERS);
-    const int hi = piece + 1 + static_cast<int>(static_cast<long long>(parts) * (quarter + 1) / JOIN_QUARTERS);
-    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (c < a.w4) {
-        if (quarter == 0) sum = a.part[(2LL * piece + 1) * a.w4 + c];
+    const int group = threadIdx.x / JOIN_COLS, lane = threadIdx.x & 31;
+    const int piece0 = static_cast<int>(blockIdx.x / col_blocks) * JOIN_PIECES;
+    const int col = threadIdx.x % JOIN_COLS, c = static_cast<int>(blockIdx.x % col_blocks) * JOIN_COLS + col;
+    const bool on = c < a.w4;
+    const float4 none = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    // parts of pieces [lo, hi), 8 at a time
+    auto add_parts = [&](float4& sum, int lo, int hi) {
         for (int p0 = lo; p0 < hi; p0 += 8) {
             float4 v[8];
 #pragma unroll
@@ -451,14 +447,56 @@ __global__ void __launch_bounds__(JOIN_COLS * JOIN_QUARTERS) zb_embedding_join_k
             for (int u = 0; u < 8; ++u)
                 if (p0 + u < hi) add4(sum, v[u]);
         }
+    };
+    auto put = [&](int id, const float4& sum) {
+        float4* out = row_of(a, id, c);
+        *out = scaled(a, sum, a.accumulate ? *out : none);
+    };
+    const int piece = piece0 + group;
+    int last = 0, id = -1;
+    if (piece + 1 < a.pieces) {
+        const int first = piece * PIECE, end = first + PIECE;
+        id = a.sorted_id[end - 1];
+        const int next = a.sorted_id[end], here = a.sorted_id[first], prev = first > 0 ? a.sorted_id[first - 1] : -1;
+        // (a run that came in from the left and fills the piece is joined at its start)
+        if (static_cast<uint32_t>(id) < a.vocab && next == id && !(here == id && prev == id)) {
+            // pieces that the run fills and leaves, then the one that it ends in
+            for (last = piece + 1;; last += 32) {
+                const int p = last + lane, n = (p + 1) * PIECE;
+                const bool through = p + 1 < a.pieces && a.sorted_id[n - 1] == id && a.sorted_id[n] == id;
+                const uint32_t stop = ~__ballot_sync(0xffffffffu, through);
+                if (stop) {
+                    last += __ffs(static_cast<int>(stop)) - 1;
+                    break;
+                }
+            }
+            if (on && last - piece <= JOIN_SHORT) {
+                float4 sum = a.part[(2LL * piece + 1) * a.w4 + c];
+                add_parts(sum, piece + 1, last + 1);
+                put(id, sum);
+            }
+        }
     }
-    __shared__ float4 quarters[JOIN_QUARTERS - 1][JOIN_COLS];
-    if (quarter > 0) quarters[quarter - 1][threadIdx.x % JOIN_COLS] = sum;
+    if (col == 0) last_s[group] = last;
     __syncthreads();
-    if (quarter > 0 || c >= a.w4) return;
+    for (int k = 0; k < JOIN_PIECES; ++k) {
+        const int p = piece0 + k, parts = last_s[k] - p;
+        if (last_s[k] == 0 || parts <= JOIN_SHORT) continue;
+        float4 sum = none;
+        if (on) {
+            if (group == 0) sum = a.part[(2LL * p + 1) * a.w4 + c];
+            add_parts(sum, p + 1 + static_cast<int>(static_cast<long long>(parts) * group / JOIN_PIECES),
+                      p + 1 + static_cast<int>(static_cast<long long>(parts) * (group + 1) / JOIN_PIECES));
+        }
+        quarters[group][col] = sum;
+        __syncthreads();
+        if (group == 0 && on) {
 #pragma unroll
-    for (int q = 0; q + 1 < JOIN_QUARTERS; ++q) add4(sum, quarters[q][threadIdx.x]);
-    *row_of(a, id, c) = scaled(a, sum, a.accumulate ? *row_of(a, id, c) : make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+            for (int q = 1; q < JOIN_PIECES; ++q) add4(sum, quarters[q][col]);
+            put(a.sorted_id[(p + 1) * PIECE - 1], sum);
+        }
+        __syncthreads();
+    }
 }
 
 // ---------------------------------------------------------------- host side
@@ -564,7 +602,9 @@ extern "C" zb_status zb_embedding_sort(const zb_embedding* e, const int32_t* ids
     const int n = static_cast<int>(e->tokens);
     const uint32_t vocab = static_cast<uint32_t>(e->vocab);
     if (n <= RANK_TOKENS) {
-        zb_embedding_rank_kernel<<<1, (n + 31) / 32 * 32, 0, st>>>(ids, n, vocab, order, sorted_id);
+        int lanes = 1;
+        while (lanes < 32 && 2 * lanes * n <= RANK_THREADS) lanes *= 2;
+        zb_embedding_rank_kernel<<<1, (n * lanes + 31) / 32 * 32, 0, st>>>(ids, n, lanes, vocab, order, sorted_id);
         return launched("zb_embedding_sort");
     }
     int bits = 1;
@@ -615,7 +655,7 @@ extern "C" zb_status zb_embedding_backward(const zb_embedding* e, const int32_t*
     a.piece_blocks = static_cast<long long>(a.pieces) * a.col_blocks;
     const long long blocks = a.piece_blocks + a.zero_blocks;
     const int join_cols = (a.w4 + JOIN_COLS - 1) / JOIN_COLS;
-    const long long joins = static_cast<long long>(std::max(a.pieces - 1, 0)) * join_cols;
+    const long long joins = (static_cast<long long>(std::max(a.pieces - 1, 0)) + JOIN_PIECES - 1) / JOIN_PIECES * join_cols;
     if (blocks > 0x7fffffffLL || joins > 0x7fffffffLL)
         return zb::fail(ZB_ERR_SHAPE, "zb_embedding_backward: too many elements");
     if (blocks == 0) return done();
@@ -627,7 +667,7 @@ extern "C" zb_status zb_embedding_backward(const zb_embedding* e, const int32_t*
     else
         err = accumulate ? go(zb_embedding_backward_kernel<float, true>) : go(zb_embedding_backward_kernel<float, false>);
     if (err == cudaSuccess && joins > 0)
-        err = launch_after(zb_embedding_join_kernel, joins, JOIN_COLS * JOIN_QUARTERS, stream, a, join_cols);
+        err = launch_after(zb_embedding_join_kernel, joins, JOIN_COLS * JOIN_PIECES, stream, a, join_cols);
     if (err != cudaSuccess)
         return zb::fail(ZB_ERR_CUDA, std::string("zb_embedding_backward launch: ") + cudaGetErrorString(err));
     return launched("zb_embedding_backward");
