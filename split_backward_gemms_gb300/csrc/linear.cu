@@ -77,14 +77,21 @@ __device__ __forceinline__ void tail_pair(float x0, float x1, f32x2& A, f32x2& E
     Q = mul2(T, P);
 }
 
+// The tanh form, with its limits at the infinities (there the formula is 0 times an
+// infinity; a NaN stays one).
+__device__ __forceinline__ float gelu_tanh(float x) { return x < -32.0f ? 0.0f : gelu_t<true>(x); }
+__device__ __forceinline__ float gelu_tanh_grad(float x) {
+    return fabsf(x) > 32.0f ? (x > 0.0f ? 1.0f : 0.0f) : gelu_grad_t<true>(x);
+}
+
 // GeLU of N values in place (an even number of them), in fp32.
 template <bool TANH, int N>
 __device__ __forceinline__ void gelu_values(float (&x)[N]) {
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
         if (TANH) {
-            x[i] = gelu_t<true>(x[i]);
-            x[i + 1] = gelu_t<true>(x[i + 1]);
+            x[i] = gelu_tanh(x[i]);
+            x[i + 1] = gelu_tanh(x[i + 1]);
         } else {
             f32x2 A, E, Q;
             tail_pair(x[i], x[i + 1], A, E, Q);
@@ -101,8 +108,8 @@ __device__ __forceinline__ void gelu_grad_values(float (&x)[N], const uint32_t (
     for (int i = 0; i < N; i += 2) {
         const float h0 = __uint_as_float(h[i / 2] << 16), h1 = __uint_as_float(h[i / 2] & 0xffff0000u);
         if (TANH) {
-            x[i] *= gelu_grad_t<true>(h0);
-            x[i + 1] *= gelu_grad_t<true>(h1);
+            x[i] *= gelu_tanh_grad(h0);
+            x[i + 1] *= gelu_tanh_grad(h1);
         } else {
             f32x2 A, E, Q;
             tail_pair(h0, h1, A, E, Q);

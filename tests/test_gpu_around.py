@@ -155,6 +155,21 @@ def test_linear_fp32(zb, M, N, K, transposed):
     assert np.linalg.norm(f64(c.out) - ref) <= 1e-6 * np.linalg.norm(ref)
 
 
+# tiles of 256, 224, 192, 160 and 128 columns where W lies along K; more column
+# tiles than SMs; problems on either side of the rule between the two kernels
+TILINGS = [(2100, 2056, 136), (2304, 1640, 200), (4096, 2400, 72), (3300, 1608, 72), (1500, 4008, 72), (700, 1000, 72),
+           (20, 20488, 136), (40, 19448, 72), (40, 20488, 72), (65, 4104, 2048), (65, 4872, 2040), (130, 4104, 4096)]
+
+
+@pytest.mark.parametrize("M,N,K", TILINGS)
+@pytest.mark.parametrize("transposed", [False, True])
+def test_linear_tilings(zb, M, N, K, transposed):
+    gap = 8 * (N % 3)
+    Linear(zb, M, N, K, "grad", transposed=transposed, gap=gap).run().check()
+    Linear(zb, M, N, K, "gelu", transposed=transposed, gap=gap, save=transposed).run().check()
+    Linear(zb, M, N, K, transposed=transposed, dtype=F32, gap=gap).run().check()
+
+
 @pytest.mark.parametrize("M,N,K,dtype", [(5, 64, 512, BF16), (300, 1032, 520, BF16), (2048, 2048, 256, BF16),
                                          (40, 1024, 2048, F32), (2048, 1032, 256, F32)])
 def test_linear_in_place(zb, M, N, K, dtype):
@@ -179,6 +194,33 @@ def test_linear_infinities_stay_in_their_places(zb, M, N, K, dtype):
     hit[2, :], hit[5, 7], hit[:, 11], hit[:, 20] = True, True, True, True
     assert torch.equal(bits(c.out)[~hit], bits(plain)[~hit])
     assert not torch.isfinite(c.out[hit]).any()
+
+
+@pytest.mark.parametrize("M,N,K", [(9, 72, 136), (2100, 2048, 128)])
+@pytest.mark.parametrize("tanh", [False, True])
+def test_linear_gelu_of_infinities(zb, M, N, K, tanh):
+    """GeLU and GeLU' take their limits there, and nothing beside them changes."""
+    c = Linear(zb, M, N, K, "gelu", tanh=tanh).run()
+    sync(zb)
+    plain = c.out.clone()
+    c.bias[4], c.bias[5], c.bias[6] = INF, -INF, NAN
+    c.run()
+    sync(zb)
+    rest = [n for n in range(N) if n not in (4, 5, 6)]
+    assert torch.equal(bits(c.out)[:, rest], bits(plain)[:, rest])
+    assert (c.out[:, 4] == INF).all() and torch.equal(c.out[:, 5], c.R[:, 5]) and torch.isnan(c.out[:, 6]).all()
+    c = Linear(zb, M, N, K, "grad", tanh=tanh, transposed=True, residual=False).run()
+    sync(zb)
+    plain = c.out.clone()
+    c.H[3, 4], c.H[3, 5], c.H[3, 6] = INF, -INF, NAN
+    c.run()
+    sync(zb)
+    d = f64(c.X[3]) @ f64(c.W[4])
+    near(c.out[3, 4], d, (K + 2) * 2.0 ** -23 * (np.abs(f64(c.X[3])) @ np.abs(f64(c.W[4]))) + 2.0 ** -8 * abs(d))
+    assert c.out[3, 5] == 0 and torch.isnan(c.out[3, 6])
+    same = bits(c.out) == bits(plain)
+    same[3, 4:7] = True
+    assert same.all()
 
 
 @pytest.mark.parametrize("M,N,K,form,dtype", [(16, 1024, 4096, "store", BF16), (512, 1024, 1024, "grad", BF16),
@@ -214,7 +256,8 @@ def _norm_inputs(rows, width, dtype, seed=0, shift=0.5):
 
 
 NORMS = [(1, 8), (2, 16), (5, 64), (3, 256), (33, 264), (7, 512), (100, 520), (16, 1024), (65, 1032), (9, 2048),
-         (130, 2056), (257, 4096), (31, 5000), (8, 8192), (3, 12296), (2, 16384), (5, 16392), (2, 32768), (1025, 768)]
+         (130, 2056), (257, 4096), (31, 5000), (8, 8192), (3, 12296), (2, 16384), (5, 16392), (2, 32768), (1025, 768),
+         (40, 1400), (5, 10000), (700, 8), (1030, 4104)]
 CHAIN = 64 + 5 + 16
 
 
