@@ -1,11 +1,10 @@
 // linear.cu — a linear map with its epilogue: D = X W (or X W^T) with bias,
 // GeLU or GeLU', and a residual (zb_linear_product).
 //
-// Two kernels, by the number of output tiles (see use_rows):
-//   zb_linear_tiles_kernel  persistent CTA pairs over 256 x 256 tiles, for
-//                           problems that fill the GPU with them;
-//   zb_linear_rows_kernel   one 128-column tile of few rows a cluster, whose
-//                           CTAs split K, for the others.
+// Two kernels (use_rows says which):
+//   zb_linear_tiles_kernel  persistent CTA pairs over tiles of 256 rows;
+//   zb_linear_rows_kernel   one tile of 32, 64 or 128 rows x 128 columns a
+//                           cluster, whose CTAs split K, for few rows or few tiles.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -134,13 +133,22 @@ __device__ __forceinline__ void add_bf16(float* x, const float4& r) {
 
 // ---------------------------------------------------------------- large problems
 // The roles of the dense kernel (gemm_tc.cu) on CTA pairs: warp 0 copies, warp
-// 1 of the even CTA issues 256 x 256 MMAs into one of two accumulators, warps
-// 2-9 drain (a TMEM lane is a row, a warp has 32 rows x 128 columns in chunks of
-// 32).  The residual comes by TMA into the staging box that the chunk's results
-// then leave from: a thread adds its row's values and writes the sums back to
-// where they lay.  So its bytes cost no registers and no waiting loads, and an
-// output that is the residual itself needs no care (each of its elements is read
-// and written by one warp, in this order).  H is loaded a chunk ahead.
+// 1 of the even CTA issues MMAs of 256 rows x up to 256 columns into one of two
+// accumulators, warps 2-9 drain (a TMEM lane is a row; a warp has 32 rows and half
+// of the columns, in chunks of 32).  H and the residual come by TMA, the residual
+// into the staging box that the chunk's results then leave from: a thread adds its
+// row's values and writes the sums back to where they lay.  So their bytes cost no
+// registers and no waiting loads, and an output that is the residual itself needs
+// no care (each of its elements is read and written by one warp, in this order).
+// The boxes are a ring over the chunks of all of a CTA's tiles, asked for again as
+// soon as the stores have read them.
+//
+// 5 stages and 4 boxes a warp or 4 and 6, us of 4096 x 4096 (8192 x 4096) with
+// residual: GeLU' K 64 31.9, 30.0; K 1024 38.8, 42.4; K 4096 (180, 189).  16
+// epilogue warps with 2 boxes each: 33.2, 39.0 (179); fp32 K 1024 43.1 for 40.9.  H
+// and R asked for in L2 a tile ahead: no faster at K 64, 41.3 for 39.5 at K 1024.
+// With K 4096 the store without residual runs at 1.81-1.97 PF/s, with it at 1.67-1.74;
+// at K 1024 the epilogue's bytes take as long as the MMAs.
 //
 // fp32 outputs (STORE32): the tensor core cuts off low bits as it adds, so the
 // accumulators take SEG blocks of K each and the epilogue adds them in registers,
@@ -151,7 +159,7 @@ struct TileCfg {
     static constexpr int COLS = F32 ? 16 : 32;  // of a box: 32 rows of 64 bytes
 };
 constexpr int SEG = 8;            // fp32 outputs: blocks of 64 along K an accumulator takes
-constexpr int TILE_STAGES = 5;    // of the ring: 16 KiB of X and of W
+constexpr int TILE_STAGES = 5;    // of the ring: 16 KiB of X, up to 16 of W
 constexpr int TILE_WARPS = 8;     // of the epilogue
 constexpr int WARP_COLS = 128;    // columns of a warp, at most
 constexpr uint32_t TILE_BOXES = 4;  // staging boxes a warp
@@ -160,7 +168,7 @@ constexpr uint32_t T_STAGE = Cfg<2>::STAGE_BYTES;
 
 struct TileCtl {
     uint64_t full[TILE_STAGES], empty[TILE_STAGES], tfull[2], tempty[2], drain;
-    uint64_t rbar[TILE_WARPS][TILE_BOXES];  // a residual box has landed
+    uint64_t rbar[TILE_WARPS][TILE_BOXES];  // a chunk's H and residual have landed
     uint32_t tmem_base;
     int abort_flag;
 };
