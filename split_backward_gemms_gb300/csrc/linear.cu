@@ -327,13 +327,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const uint32_t rbar0 = zbp::smem_u32(&ctl->rbar[ew][0]);
         const uint64_t pol_out = zbp::l2_policy(args.hint_out), pol_once = zbp::l2_policy(1);
         const bool res = args.R != nullptr, save = FORM == GELU && args.save;
-        // boxes of a chunk: H's (read by GRAD, written by GELU where it is kept),
-        // then the residual's, which the results leave from; without a residual
-        // GRAD's leave from H's
-        const uint32_t per = (save || (FORM == GRAD && res)) ? 2 : 1;
-        const bool inputs = res || FORM == GRAD;
-        const uint32_t in_bytes = (FORM == GRAD ? T_BOX : 0u) + (res ? T_BOX : 0u);
-        const uint32_t ring = per == 2 ? TILE_BOXES / 2 : TILE_BOXES;  // chunks whose boxes there are
+        // The boxes are a ring of chunks: one box a chunk, for the residual, which the
+        // results leave from; or two where GELU keeps H, whose box comes first.  Without
+        // a residual GRAD's results leave from H's box.  With one, H has the last box to
+        // itself: it is free as soon as H is in registers, so one is enough, and three
+        // are left to the residual, which hold it until the results are stored.
+        const bool h_box = FORM == GRAD && res, inputs = res || FORM == GRAD;
+        const uint32_t per = save ? 2 : 1, ring = save ? TILE_BOXES / 2 : h_box ? TILE_BOXES - 1 : TILE_BOXES;
+        const uint32_t hat = stg0 + (TILE_BOXES - 1) * T_BOX, hbar = rbar0 + (TILE_BOXES - 1) * 8u;
         auto boxes_of = [&](uint32_t slot) { return stg0 + slot * per * T_BOX; };
         auto place = [&](int tile, int& row0, int& n0) {  // a tile's first row and column of this warp; its live chunks
             int mb, nb;
@@ -343,28 +344,42 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const int cols = min(args.N - n0, min(half, tile_n - c_lo));
             return row0 < args.M ? min(CH, max(0, (cols + T::COLS - 1) / T::COLS)) : 0;
         };
-        // the inputs of the next chunk (over the tiles) that has not been asked for
-        int a_tile = cluster - clusters, a_c = 0, a_chunks = 0, a_row0 = 0, a_n0 = 0;
-        uint32_t asked = 0, used = 0;            // chunks asked for, chunks stored
-        uint32_t a_slot = 0, slot = 0, turn = 0;  // their places in the ring; parity of the ring's turn
+        // a walk over the chunks of all tiles, ahead of the one that stores them
+        struct Cursor {
+            int tile, c, chunks, row0, n0;
+        };
+        auto next = [&](Cursor& a) {
+            while (a.c >= a.chunks) {
+                if (a.tile >= num_tiles) return false;
+                a.tile += clusters;
+                if (a.tile >= num_tiles) return false;
+                a.c = 0;
+                a.chunks = place(a.tile, a.row0, a.n0);
+            }
+            return true;
+        };
+        Cursor ahead = {cluster - clusters, 0, 0, 0, 0}, h_ahead = ahead;
+        uint32_t asked = 0, used = 0, h_asked = 0;  // chunks asked for, chunks stored
+        uint32_t a_slot = 0, slot = 0, turn = 0;     // their places in the ring; parity of the ring's turn
         auto ask = [&]() {
-            while (a_c >= a_chunks) {
-                if (a_tile >= num_tiles) return;
-                a_tile += clusters;
-                if (a_tile >= num_tiles) return;
-                a_c = 0;
-                a_chunks = place(a_tile, a_row0, a_n0);
-            }
+            if (!next(ahead)) return;
             if (lane == 0) {
-                const uint32_t bar = rbar0 + a_slot * 8u, at = boxes_of(a_slot);
-                const int x = a_n0 + a_c * T::COLS;
-                zbp::mbar_arrive_expect_tx(bar, in_bytes);
-                if (FORM == GRAD) zbp::tma_load_2d_hint(at, &tmH, bar, x, a_row0, pol_once);
-                if (res) zbp::tma_load_2d_hint(at + (per - 1) * T_BOX, &tmR, bar, x, a_row0, pol_once);
+                const uint32_t bar = rbar0 + a_slot * 8u, at = boxes_of(a_slot) + (per - 1) * T_BOX;
+                zbp::mbar_arrive_expect_tx(bar, T_BOX);
+                zbp::tma_load_2d_hint(at, res ? &tmR : &tmH, bar, ahead.n0 + ahead.c * T::COLS, ahead.row0, pol_once);
             }
-            ++a_c;
+            ++ahead.c;
             ++asked;
             a_slot = a_slot + 1 == ring ? 0 : a_slot + 1;
+        };
+        auto ask_h = [&]() {
+            if (!next(h_ahead)) return;
+            if (lane == 0) {
+                zbp::mbar_arrive_expect_tx(hbar, T_BOX);
+                zbp::tma_load_2d_hint(hat, &tmH, hbar, h_ahead.n0 + h_ahead.c * T::COLS, h_ahead.row0, pol_once);
+            }
+            ++h_ahead.c;
+            ++h_asked;
         };
         bool owed = false;  // the last chunk's boxes have not been asked for again
         // once the stores so far have read their boxes
@@ -374,6 +389,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             ask();
             owed = false;
         };
+        if (h_box) ask_h();
         if (inputs)
             for (uint32_t k = 0; k < ring; ++k) ask();
         // this lane's 16-byte part k of its row in a box
@@ -414,17 +430,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
             if (!ok) break;
             // 16 columns from col, the p-th of their boxes
-            auto piece = [&](int p, int col, uint32_t box0, uint32_t box, float (&x)[16]) {
+            auto piece = [&](int p, int col, uint32_t box0, uint32_t box, const uint32_t (&w)[8], float (&x)[16]) {
                 if (FORM == GRAD) {
-                    uint32_t w[8];
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float4 h = zbp::ld_shared_v4(part(box0, 2 * p + k));
-                        w[4 * k] = __float_as_uint(h.x);
-                        w[4 * k + 1] = __float_as_uint(h.y);
-                        w[4 * k + 2] = __float_as_uint(h.z);
-                        w[4 * k + 3] = __float_as_uint(h.w);
-                    }
                     if (args.tanh_form)
                         gelu_grad_values<true, 16>(x, w);
                     else
@@ -472,6 +479,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             auto chunk = [&](int c, float (&sums)[16]) {
                 const int col0 = n0 + c * T::COLS;
                 const uint32_t box0 = boxes_of(slot), box = box0 + (per - 1) * T_BOX;
+                uint32_t v[T::F32 ? 1 : 32];  // bf16: the chunk's sums, on their way while the inputs are waited for
+                if constexpr (!T::F32) zbp::tmem_ld_32x32b_x32(taddr + buf * ACC_COLS + c * 32, v);
                 if (inputs) {
                     if (owed) ask_on();
                     if (!wait_bar<false>(rbar0 + slot * 8u, turn, abort_flag, args.err, ERR_WAIT_EPI, WAIT_LIMIT_NS, true)) {
@@ -487,19 +496,35 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     }
                     __syncwarp();
                 }
-                if constexpr (T::F32) {
-                    piece(0, col0, box0, box, sums);
-                } else {
-#pragma unroll 1
-                    for (int p = 0; p < 2; ++p) {
-                        uint32_t v[16];
-                        zbp::tmem_ld_32x32b_x16(taddr + buf * ACC_COLS + c * 32 + p * 16, v);
-                        zbp::tmem_ld_wait();
-                        float x[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(v[i]);
-                        piece(p, col0 + p * 16, box0, box, x);
+                uint32_t w[2][8];  // H
+                if (FORM == GRAD) {
+                    if (h_box && !wait_bar<false>(hbar, used & 1u, abort_flag, args.err, ERR_WAIT_EPI, WAIT_LIMIT_NS, true)) {
+                        ok = false;
+                        return;
                     }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float4 h = zbp::ld_shared_v4(part(h_box ? hat : box0, k));
+                        w[k / 2][k % 2 * 4] = __float_as_uint(h.x);
+                        w[k / 2][k % 2 * 4 + 1] = __float_as_uint(h.y);
+                        w[k / 2][k % 2 * 4 + 2] = __float_as_uint(h.z);
+                        w[k / 2][k % 2 * 4 + 3] = __float_as_uint(h.w);
+                    }
+                    if (h_box) {
+                        zbp::fence_proxy_async_smem();  // every lane has read the box
+                        __syncwarp();
+                        ask_h();
+                    }
+                }
+                if constexpr (T::F32) {
+                    piece(0, col0, box0, box, w[0], sums);
+                } else {
+                    zbp::tmem_ld_wait();
+                    float x[2][16];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) x[i / 16][i % 16] = __uint_as_float(v[i]);
+                    piece(0, col0, box0, box, w[0], x[0]);
+                    piece(1, col0 + 16, box0, box, w[1], x[1]);
                 }
                 zbp::fence_proxy_async_smem();
                 __syncwarp();
@@ -530,7 +555,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
             if (owed) ask_on();
         }
+        zbp::tmem_ld_wait();  // (a chunk's sums may be on their way after an abort)
         // inputs asked for and not used (after an abort)
+        if (h_box && h_asked > used)
+            wait_bar<false>(hbar, (h_asked - 1) & 1u, abort_flag, args.err, ERR_WAIT_EPI, DRAIN_LIMIT_NS, false);
         for (; inputs && used < asked; ++used) {
             wait_bar<false>(rbar0 + slot * 8u, turn, abort_flag, args.err, ERR_WAIT_EPI, DRAIN_LIMIT_NS, false);
             if (++slot == ring) {
