@@ -157,7 +157,13 @@ template <int FORM>
 struct TileCfg {
     static constexpr bool F32 = FORM == STORE32;
     static constexpr int COLS = F32 ? 16 : 32;  // of a box: 32 rows of 64 bytes
+    // F32's 128 sums a thread need the registers that warps 0-3 (2 and 3 idle) give up
+    static constexpr int THREADS = F32 ? 384 : NUM_THREADS;
+    static constexpr int FIRST = F32 ? 4 : 2;  // first epilogue warp
 };
+// (fp32 kernels are compiled to 168 registers a thread, what 384 threads leave)
+constexpr int REGS_LOW = 56, REGS_HIGH = 224;
+static_assert(128 * REGS_LOW + 256 * REGS_HIGH <= 384 * 168, "register split");
 constexpr int SEG = 8;            // fp32 outputs: blocks of 64 along K an accumulator takes
 constexpr int TILE_STAGES = 5;    // of the ring: 16 KiB of X, up to 16 of W
 constexpr int TILE_WARPS = 8;     // of the epilogue
@@ -176,7 +182,7 @@ constexpr size_t TILE_SMEM = 1024 + TILE_STAGES * T_STAGE + TILE_WARPS * TILE_BO
 static_assert(TILE_SMEM <= 232448, "shared memory");
 
 template <int FORM, int W_MN>
-__global__ void __launch_bounds__(NUM_THREADS, 1)
+__global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
     zb_linear_tiles_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                            const __grid_constant__ CUtensorMap tmO, const __grid_constant__ CUtensorMap tmH,
                            const __grid_constant__ CUtensorMap tmR, const LinearArgs args) {
@@ -229,6 +235,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     zbp::grid_dependency_wait();
     zbp::allow_dependent_launch();
 
+    if (T::F32 && warp < T::FIRST) zbp::regs_dec<REGS_LOW>();
     if (warp == 0) {
         // ---------------------------------------------------- TMA producer
         const uint32_t full0 = zbp::smem_u32(&ctl->full[0]), empty0 = zbp::smem_u32(&ctl->empty[0]);
@@ -319,10 +326,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             __syncwarp();
             wait_bar<false>(zbp::smem_u32(&ctl->drain), 0, abort_flag, args.err, ERR_WAIT_MMA, DRAIN_LIMIT_NS, false);
         }
-    } else {
+    } else if (warp >= T::FIRST) {
         // ---------------------------------------------------- epilogue
+        if (T::F32) zbp::regs_inc<REGS_HIGH>();
         constexpr int CH = WARP_COLS / T::COLS;  // chunks of a warp's columns
-        const int ew = warp - 2, q = warp & 3, half = (tile_n / 2 + 31) / 32 * 32, c_lo = (ew >> 2) * half;
+        const int ew = warp - T::FIRST, q = warp & 3, half = (tile_n / 2 + 31) / 32 * 32, c_lo = (ew >> 2) * half;
         const uint32_t stg0 = zbp::smem_u32(staging) + static_cast<uint32_t>(ew) * TILE_BOXES * T_BOX;
         const uint32_t rbar0 = zbp::smem_u32(&ctl->rbar[ew][0]);
         const uint64_t pol_out = zbp::l2_policy(args.hint_out), pol_once = zbp::l2_policy(1);
@@ -415,13 +423,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 zbp::tc_fence_after();
                 if constexpr (T::F32) {
 #pragma unroll
-                    for (int c = 0; c < CH; ++c) {
-                        uint32_t v[16];
-                        zbp::tmem_ld_32x32b_x16(taddr + buf * ACC_COLS + c * 16, v);
+                    for (int c = 0; c < CH; c += 2) {
+                        uint32_t v[32];
+                        zbp::tmem_ld_32x32b_x32(taddr + buf * ACC_COLS + c * 16, v);
                         zbp::tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            acc[c][i] = kb0 == 0 ? __uint_as_float(v[i]) : acc[c][i] + __uint_as_float(v[i]);
+                        for (int i = 0; i < 32; ++i) {
+                            float& sum = acc[c + i / 16][i % 16];
+                            sum = kb0 == 0 ? __uint_as_float(v[i]) : sum + __uint_as_float(v[i]);
+                        }
                     }
                     zbp::tc_fence_before();
                     __syncwarp();
@@ -857,10 +867,10 @@ zb_status launch_tiles(const CUtensorMap& x, const CUtensorMap& w, const CUtenso
     static std::atomic<int> cache[64];
     auto kern = zb_linear_tiles_kernel<FORM, W_MN>;
     int ctas = 0;
-    const zb_status s = full_grid(kern, cache, TILE_SMEM, NUM_THREADS, 2, &ctas);
+    const zb_status s = full_grid(kern, cache, TILE_SMEM, TileCfg<FORM>::THREADS, 2, &ctas);
     if (s != ZB_OK) return s;
     const long long tiles = (static_cast<long long>(a.M) + 255) / 256 * ((a.N + a.tile_n - 1) / a.tile_n);
-    LaunchCfg cfg(static_cast<int>(std::min<long long>(2 * tiles, ctas)), NUM_THREADS, TILE_SMEM, 2, stream);
+    LaunchCfg cfg(static_cast<int>(std::min<long long>(2 * tiles, ctas)), TileCfg<FORM>::THREADS, TILE_SMEM, 2, stream);
     const cudaError_t e = cudaLaunchKernelEx(&cfg.cfg, kern, x, w, o, h, r, a);
     if (e != cudaSuccess)
         return zb::fail(ZB_ERR_CUDA, std::string("zb_linear_product launch: ") + cudaGetErrorString(e));
