@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
         // a residual GRAD's results leave from H's box.  With one, H has the last box to
         // itself: it is free as soon as H is in registers, so one is enough, and three
         // are left to the residual, which hold it until the results are stored.
-        const bool h_box = FORM == GRAD && res, inputs = res || FORM == GRAD;
+        const bool h_box = FORM == GRAD && res, inputs = !T::F32 && (res || FORM == GRAD);
         const uint32_t per = save ? 2 : 1, ring = save ? TILE_BOXES / 2 : h_box ? TILE_BOXES - 1 : TILE_BOXES;
         const uint32_t hat = stg0 + (TILE_BOXES - 1) * T_BOX, hbar = rbar0 + (TILE_BOXES - 1) * 8u;
         auto boxes_of = [&](uint32_t slot) { return stg0 + slot * per * T_BOX; };
@@ -402,6 +402,24 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
             for (uint32_t k = 0; k < ring; ++k) ask();
         // this lane's 16-byte part k of its row in a box
         auto part = [&](uint32_t box, int k) { return box + static_cast<uint32_t>(lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)); };
+        // fp32: the residual is what the sums start from, since it can be waited for while
+        // a tile's first MMAs run, but not between its last ones and the next tile's, whose
+        // two accumulators hold 16 blocks of K only.  Chunk c comes into box c mod 4.
+        uint32_t on_way = 0, phases = 0;  // a bit a box: asked for and not read; phase of its barrier
+        auto ask32 = [&](int c, int row0, int n0) {
+            const uint32_t b = static_cast<uint32_t>(c) % TILE_BOXES;
+            if (lane == 0) {
+                zbp::mbar_arrive_expect_tx(rbar0 + b * 8u, T_BOX);
+                zbp::tma_load_2d_hint(stg0 + b * T_BOX, &tmR, rbar0 + b * 8u, n0 + c * T::COLS, row0, pol_once);
+            }
+            on_way |= 1u << b;
+        };
+        auto ask32_tile = [&](int tile) {  // the first boxes of a tile
+            int row0, n0;
+            const int chunks = min(static_cast<int>(TILE_BOXES), tile < num_tiles ? place(tile, row0, n0) : 0);
+            for (int c = 0; c < chunks; ++c) ask32(c, row0, n0);
+        };
+        if (T::F32 && res) ask32_tile(cluster);
         uint32_t local = 0;
         bool ok = true;
         for (int tile = cluster; tile < num_tiles && ok; tile += clusters) {
@@ -410,6 +428,35 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(c_lo);
             float acc[T::F32 ? CH : 1][16];
             uint32_t buf = 0;
+            if constexpr (T::F32) {
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) acc[c][i] = 0.0f;
+                    if (!res || c >= chunks || !ok) continue;
+                    constexpr uint32_t B = TILE_BOXES;
+                    const uint32_t b = static_cast<uint32_t>(c) % B, box = stg0 + b * T_BOX;
+                    if (!wait_bar<false>(rbar0 + b * 8u, (phases >> b) & 1u, abort_flag, args.err, ERR_WAIT_EPI,
+                                        WAIT_LIMIT_NS, true)) {
+                        ok = false;
+                        continue;
+                    }
+                    phases ^= 1u << b;
+                    on_way &= ~(1u << b);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float4 r = zbp::ld_shared_v4(part(box, k));
+                        acc[c][4 * k] = r.x;
+                        acc[c][4 * k + 1] = r.y;
+                        acc[c][4 * k + 2] = r.z;
+                        acc[c][4 * k + 3] = r.w;
+                    }
+                    zbp::fence_proxy_async_smem();  // every lane has read the box
+                    __syncwarp();
+                    if (c + static_cast<int>(B) < chunks) ask32(c + static_cast<int>(B), row0, n0);
+                }
+                if (!ok) break;
+            }
             // fp32 outputs add the accumulators' parts; the others have one, read piece by piece below
             for (int kb0 = 0; kb0 < num_kb; kb0 += T::F32 ? SEG : num_kb) {
                 buf = local & 1u;
@@ -429,8 +476,7 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
                         zbp::tmem_ld_wait();
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
-                            float& sum = acc[c + i / 16][i % 16];
-                            sum = kb0 == 0 ? __uint_as_float(v[i]) : sum + __uint_as_float(v[i]);
+                            acc[c + i / 16][i % 16] += __uint_as_float(v[i]);
                         }
                     }
                     zbp::tc_fence_before();
@@ -469,13 +515,6 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
                 if constexpr (T::F32) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        if (res) {
-                            const float4 r = zbp::ld_shared_v4(part(box, k));
-                            x[4 * k] += r.x;
-                            x[4 * k + 1] += r.y;
-                            x[4 * k + 2] += r.z;
-                            x[4 * k + 3] += r.w;
-                        }
                         zbp::st_shared_v4(part(box, k), __float_as_uint(x[4 * k]), __float_as_uint(x[4 * k + 1]),
                                           __float_as_uint(x[4 * k + 2]), __float_as_uint(x[4 * k + 3]));
                     }
@@ -564,9 +603,17 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
                 if (lane == 0) zbp::mbar_arrive_remote(zbp::mapa_shared(zbp::smem_u32(&ctl->tempty[buf]), 0));
             }
             if (owed) ask_on();
+            if (T::F32 && res) {
+                if (lane == 0) zbp::bulk_wait_read<0>();
+                __syncwarp();
+                ask32_tile(tile + clusters);
+            }
         }
         zbp::tmem_ld_wait();  // (a chunk's sums may be on their way after an abort)
         // inputs asked for and not used (after an abort)
+        for (uint32_t b = 0; T::F32 && b < TILE_BOXES; ++b)
+            if ((on_way >> b) & 1u)
+                wait_bar<false>(rbar0 + b * 8u, (phases >> b) & 1u, abort_flag, args.err, ERR_WAIT_EPI, DRAIN_LIMIT_NS, false);
         if (h_box && h_asked > used)
             wait_bar<false>(hbar, (h_asked - 1) & 1u, abort_flag, args.err, ERR_WAIT_EPI, DRAIN_LIMIT_NS, false);
         for (; inputs && used < asked; ++used) {
