@@ -77,7 +77,7 @@ constexpr int SORT_THREADS = 1024;
 constexpr int SORT_WARPS = SORT_THREADS / 32;
 constexpr int SORT_BITS = 10;  // of a digit, at most
 constexpr int SORT_HELD = 8;   // tokens a lane holds in registers from counting to placing
-constexpr size_t sort_smem(int bits) { return (static_cast<size_t>(SORT_WARPS + 1) << bits) * 4; }
+constexpr size_t sort_smem(int bits) { return (static_cast<size_t>(SORT_WARPS + 2) << bits) * 4; }
 
 struct SortArgs {
     const int* ids;
@@ -94,6 +94,7 @@ __global__ void __cluster_dims__(SORT_BLOCKS, 1, 1) __launch_bounds__(SORT_THREA
     const int digits = 1 << a.bits;
     uint32_t* hist = sort_shared;                        // [warp][digit]
     uint32_t* total = sort_shared + SORT_WARPS * digits;  // [digit]: the block's
+    uint32_t* base = total + digits;                      // [digit]: place of the block's first such token
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = threadIdx.x;
     const uint32_t rank = zbp::cluster_ctarank();
     const long long n = a.tokens;
@@ -164,10 +165,10 @@ __global__ void __cluster_dims__(SORT_BLOCKS, 1, 1) __launch_bounds__(SORT_THREA
             if (lane >= o) sum += u;
         }
         if (lane == 31) warp_total[warp] = sum;
-        zbp::cluster_sync();  // also: every block has read the totals
+        __syncthreads();
         uint32_t left = lane < warp ? warp_total[lane] : 0u;
         left = __reduce_add_sync(0xffffffffu, left);
-        if (t < digits) total[t] = sum + left - all + before;
+        if (t < digits) base[t] = sum + left - all + before;
         __syncthreads();
         const bool last = pass + 1 == a.passes;
         for (int i0 = lo; i0 < hi; i0 += STEP) {
@@ -180,7 +181,7 @@ __global__ void __cluster_dims__(SORT_BLOCKS, 1, 1) __launch_bounds__(SORT_THREA
                 const uint32_t peers = __match_any_sync(0xffffffffu, d);
                 const int before_me = __popc(peers & ((1u << lane) - 1u));
                 uint32_t place = 0;
-                if (on) place = total[d] + mine[d] + static_cast<uint32_t>(before_me);
+                if (on) place = base[d] + mine[d] + static_cast<uint32_t>(before_me);
                 __syncwarp();
                 if (on && before_me == 0) mine[d] += static_cast<uint32_t>(__popc(peers));
                 __syncwarp();
@@ -194,7 +195,7 @@ __global__ void __cluster_dims__(SORT_BLOCKS, 1, 1) __launch_bounds__(SORT_THREA
                 }
             }
         }
-        zbp::cluster_sync();  // the next pass reads what the others placed; no one's shared memory is read any more
+        zbp::cluster_sync();  // the next pass reads what the others placed; no one's totals are read any more
     }
 }
 
