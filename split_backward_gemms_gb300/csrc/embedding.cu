@@ -67,15 +67,20 @@ __device__ __forceinline__ uint32_t key_of(int id, uint32_t vocab) {
 }
 __device__ __forceinline__ int id_of(uint32_t key, uint32_t vocab) { return key < vocab ? static_cast<int>(key) : -1; }
 
-// A stable radix sort by one cluster of 8 blocks, digits from the lowest up.  A block owns an eighth of the tokens and a warp a contiguous part of them, so
-// that a digit's tokens are placed in the order (block, warp, token): each warp
+// A stable radix sort by one cluster of 8 or 16 blocks, digits from the lowest up.
+// A block owns its part of the tokens and a warp a contiguous part of that, so that a
+// digit's tokens are placed in the order (block, warp, token): each warp
 // counts its digits, the counts are summed over warps and blocks (through
 // distributed shared memory) into the first place of each warp's tokens of each
 // digit, and the warp places its tokens by them.
-constexpr int SORT_BLOCKS = 8;
+// Latency bounds it up to some 10000 tokens (a pass is 3 to 4 us: one read of the
+// tokens, three barriers, one placing), then the placing: us of 8 and 16 blocks, 32000
+// ids: 1025 tokens 8.5 and 9.5, 8192 10.7 and 10.8, 16384 13.8 and 11.8, 262144 104
+// and 57.  One block alone: 10.0 at 1025, 27.7 at 8192.
 constexpr int SORT_THREADS = 1024;
 constexpr int SORT_WARPS = SORT_THREADS / 32;
 constexpr int SORT_BITS = 10;  // of a digit, at most
+constexpr int SORT_LONG = 8192;  // tokens from which on 16 blocks sort
 constexpr int SORT_HELD = 8;   // tokens a lane holds in registers from counting to placing
 constexpr size_t sort_smem(int bits) { return (static_cast<size_t>(SORT_WARPS + 2) << bits) * 4; }
 
@@ -87,7 +92,8 @@ struct SortArgs {
     int *order, *sorted_id;
 };
 
-__global__ void __cluster_dims__(SORT_BLOCKS, 1, 1) __launch_bounds__(SORT_THREADS)
+template <int BLOCKS>
+__global__ void __cluster_dims__(BLOCKS, 1, 1) __launch_bounds__(SORT_THREADS)
     zb_embedding_sort_kernel(const SortArgs a) {
     extern __shared__ uint32_t sort_shared[];
     __shared__ uint32_t warp_total[SORT_WARPS];
@@ -99,8 +105,8 @@ __global__ void __cluster_dims__(SORT_BLOCKS, 1, 1) __launch_bounds__(SORT_THREA
     const uint32_t rank = zbp::cluster_ctarank();
     const long long n = a.tokens;
     const int part = static_cast<int>(rank) * SORT_WARPS + warp;
-    const int lo = static_cast<int>(n * part / (SORT_BLOCKS * SORT_WARPS));
-    const int hi = static_cast<int>(n * (part + 1) / (SORT_BLOCKS * SORT_WARPS));
+    const int lo = static_cast<int>(n * part / (BLOCKS * SORT_WARPS));
+    const int hi = static_cast<int>(n * (part + 1) / (BLOCKS * SORT_WARPS));
     uint32_t* mine = hist + warp * digits;
     zbp::allow_dependent_launch();
     constexpr int STEP = 32 * SORT_HELD;
@@ -148,12 +154,12 @@ __global__ void __cluster_dims__(SORT_BLOCKS, 1, 1) __launch_bounds__(SORT_THREA
         uint32_t before = 0, all = 0;
         if (t < digits) {
             const uint32_t at = zbp::smem_u32(&total[t]);
-            uint32_t c[SORT_BLOCKS];
+            uint32_t c[BLOCKS];
 #pragma unroll
-            for (int b = 0; b < SORT_BLOCKS; ++b)
+            for (int b = 0; b < BLOCKS; ++b)
                 asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(c[b]) : "r"(zbp::mapa_shared(at, b)) : "memory");
 #pragma unroll
-            for (int b = 0; b < SORT_BLOCKS; ++b) {
+            for (int b = 0; b < BLOCKS; ++b) {
                 if (b < static_cast<int>(rank)) before += c[b];
                 all += c[b];
             }
@@ -619,12 +625,17 @@ extern "C" zb_status zb_embedding_sort(const zb_embedding* e, const int32_t* ids
     for (int i = 0; i < 2; ++i) a.pairs[i] = static_cast<uint2*>(workspace) + static_cast<size_t>(i) * n;
     a.order = order;
     a.sorted_id = sorted_id;
-    const cudaError_t err = cudaFuncSetAttribute(zb_embedding_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 static_cast<int>(sort_smem(SORT_BITS)));
-    if (err != cudaSuccess)
-        return zb::fail(ZB_ERR_CUDA, std::string("zb_embedding_sort: cudaFuncSetAttribute: ") + cudaGetErrorString(err));
-    zb_embedding_sort_kernel<<<SORT_BLOCKS, SORT_THREADS, sort_smem(a.bits), st>>>(a);
-    return launched("zb_embedding_sort");
+    auto go = [&](auto kern, int blocks) {
+        cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(sort_smem(SORT_BITS)));
+        if (err == cudaSuccess && blocks > 8)
+            err = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (err != cudaSuccess)
+            return zb::fail(ZB_ERR_CUDA, std::string("zb_embedding_sort: cudaFuncSetAttribute: ") + cudaGetErrorString(err));
+        kern<<<blocks, SORT_THREADS, sort_smem(a.bits), st>>>(a);
+        return launched("zb_embedding_sort");
+    };
+    return n > SORT_LONG ? go(zb_embedding_sort_kernel<16>, 16) : go(zb_embedding_sort_kernel<8>, 8);
 }
 
 extern "C" zb_status zb_embedding_backward(const zb_embedding* e, const int32_t* order, const int32_t* sorted_id,
