@@ -18,7 +18,9 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 
 // ---------------------------------------------------------------- lookup
-// A warp copies up to 32 x LOOK_U pieces of 8 values of one token's row.
+// A warp copies up to 32 x LOOK_U pieces of 8 values of one token's row.  HBM bounds
+// it (8192 tokens of 50000 ids, width 4096: 17 us, 7.7 TB/s with the repeated ids' rows
+// from L2).
 constexpr int LOOK_U = 4;
 
 template <typename T>
@@ -74,7 +76,7 @@ __device__ __forceinline__ int id_of(uint32_t key, uint32_t vocab) { return key 
 // distributed shared memory) into the first place of each warp's tokens of each
 // digit, and the warp places its tokens by them.
 // Latency bounds it up to some 10000 tokens (a pass is 3 to 4 us: one read of the
-// tokens, three barriers, one placing), then the placing: us of 8 and 16 blocks, 32000
+// tokens, two cluster barriers, one placing), then the placing: us of 8 and 16 blocks, 32000
 // ids: 1025 tokens 8.5 and 9.5, 8192 10.7 and 10.8, 16384 13.8 and 11.8, 262144 104
 // and 57.  One block alone: 10.0 at 1025, 27.7 at 8192.
 constexpr int SORT_THREADS = 1024;
@@ -245,6 +247,11 @@ __global__ void __launch_bounds__(RANK_THREADS)
 // for the run that goes on to the right), and a second kernel adds such a run's
 // parts in order.  Without accumulation blocks of their own write zeros to the
 // rows of the ids that do not occur, which warps find by searching the sorted ids.
+//
+// 16384 tokens of 32000 ids, width 2048, bf16: 60 us of sums and zeros (329 MB, 5.4
+// TB/s; zeros alone run at 6.1) and 8 of joining; accumulating 28 and 8.  One row at a
+// time instead of 8: 66 accumulating in all.  Zeros in blocks before the others: 76
+// overwriting for 66 in all.
 constexpr int PIECE = 32;
 constexpr int GRAD_THREADS = 256;
 constexpr int ZERO_ROWS = 8;  // of a warp
