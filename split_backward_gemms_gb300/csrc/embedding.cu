@@ -7,8 +7,8 @@
 #include <algorithm>
 #include <string>
 
+#include "launch.cuh"
 #include "ptx.cuh"
-#include "zb_internal.h"
 
 namespace {
 
@@ -29,6 +29,8 @@ __global__ void __launch_bounds__(256)
                                 long long tokens, long long vocab, int w8, int segs, float scale) {
     const long long item = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
     const long long t = item / segs;
+    zbp::grid_dependency_wait();
+    zbp::allow_dependent_launch();
     if (t >= tokens) return;
     const int at = static_cast<int>(item - t * segs) * 32 * LOOK_U + (threadIdx.x & 31);
     const int id = ids[t];
@@ -110,6 +112,7 @@ __global__ void __cluster_dims__(BLOCKS, 1, 1) __launch_bounds__(SORT_THREADS)
     const int lo = static_cast<int>(n * part / (BLOCKS * SORT_WARPS));
     const int hi = static_cast<int>(n * (part + 1) / (BLOCKS * SORT_WARPS));
     uint32_t* mine = hist + warp * digits;
+    zbp::grid_dependency_wait();
     zbp::allow_dependent_launch();
     constexpr int STEP = 32 * SORT_HELD;
     for (int pass = 0; pass < a.passes; ++pass) {
@@ -220,6 +223,8 @@ __global__ void __launch_bounds__(RANK_THREADS)
     __shared__ __align__(16) uint32_t keys[RANK_TOKENS];
     const int t = threadIdx.x / lanes, s = threadIdx.x & (lanes - 1);
     const int n4 = (tokens + 3) / 4;
+    zbp::grid_dependency_wait();
+    zbp::allow_dependent_launch();
     if (threadIdx.x < 4 * n4)
         keys[threadIdx.x] = static_cast<int>(threadIdx.x) < tokens ? key_of(ids[threadIdx.x], vocab) : ~0u;  // behind every key
     __syncthreads();
@@ -514,9 +519,6 @@ __global__ void __launch_bounds__(JOIN_COLS * JOIN_PIECES) zb_embedding_join_ker
 }
 
 // ---------------------------------------------------------------- host side
-bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
-bool off4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
-
 zb_status check_embedding(const char* who, const zb_embedding* e) {
     const std::string w = who;
     if (!e) return zb::fail(ZB_ERR_INVALID_ARG, w + ": descriptor is NULL");
@@ -525,34 +527,6 @@ zb_status check_embedding(const char* who, const zb_embedding* e) {
     if (e->width < 1 || e->width > (1LL << 20)) return zb::fail(ZB_ERR_SHAPE, w + ": width must be in [1, 2^20]");
     if (e->width % 8) return zb::fail(ZB_ERR_ALIGN, w + ": width must be a multiple of 8");
     if (e->dtype != ZB_DT_BF16 && e->dtype != ZB_DT_F32) return zb::fail(ZB_ERR_DTYPE, w + ": unknown dtype");
-    return ZB_OK;
-}
-
-zb_status launched(const char* who) {
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return zb::fail(ZB_ERR_CUDA, std::string(who) + " launch: " + cudaGetErrorString(e));
-    zb::clear_error();
-    return ZB_OK;
-}
-
-// Launches a kernel that waits for the one before it in the stream by itself
-// (grid_dependency_wait), so that its blocks may be set up before that one ends.
-template <typename K, typename... Args>
-cudaError_t launch_after(K kern, long long blocks, int threads, void* stream, const Args&... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
-zb_status done() {
-    zb::clear_error();
     return ZB_OK;
 }
 
@@ -583,14 +557,14 @@ extern "C" zb_status zb_embedding_forward(const zb_embedding* e, const int32_t* 
     const int segs = (w8 + 32 * LOOK_U - 1) / (32 * LOOK_U);
     const long long blocks = (e->tokens * segs + 7) / 8;
     if (blocks > 0x7fffffffLL) return zb::fail(ZB_ERR_SHAPE, "zb_embedding_forward: too many elements");
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (e->dtype == ZB_DT_BF16)
-        zb_embedding_forward_kernel<<<static_cast<unsigned>(blocks), 256, 0, st>>>(
-            ids, static_cast<const uint4*>(E), static_cast<__nv_bfloat16*>(Y), e->tokens, e->vocab, w8, segs, e->scale);
-    else
-        zb_embedding_forward_kernel<<<static_cast<unsigned>(blocks), 256, 0, st>>>(
-            ids, static_cast<const uint4*>(E), static_cast<float*>(Y), e->tokens, e->vocab, w8, segs, e->scale);
-    return launched("zb_embedding_forward");
+    auto go = [&](auto kern, auto* y) {
+        return launch_after(kern, blocks, 256, 0, stream, ids, static_cast<const uint4*>(E), y,
+                            static_cast<long long>(e->tokens), static_cast<long long>(e->vocab), w8, segs, e->scale);
+    };
+    return launched("zb_embedding_forward",
+                    e->dtype == ZB_DT_BF16
+                        ? go(zb_embedding_forward_kernel<__nv_bfloat16>, static_cast<__nv_bfloat16*>(Y))
+                        : go(zb_embedding_forward_kernel<float>, static_cast<float*>(Y)));
 }
 
 extern "C" size_t zb_embedding_workspace_bytes(const zb_embedding* e) {
@@ -612,14 +586,13 @@ extern "C" zb_status zb_embedding_sort(const zb_embedding* e, const int32_t* ids
         return zb::fail(ZB_ERR_ALIGN, "zb_embedding_sort: pointers must be 4-byte aligned");
     s = check_workspace("zb_embedding_sort", e, workspace, ws_bytes);
     if (s != ZB_OK) return s;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int n = static_cast<int>(e->tokens);
     const uint32_t vocab = static_cast<uint32_t>(e->vocab);
     if (n <= RANK_TOKENS) {
         int lanes = 1;
         while (lanes < 32 && 2 * lanes * n <= RANK_THREADS) lanes *= 2;
-        zb_embedding_rank_kernel<<<1, (n * lanes + 31) / 32 * 32, 0, st>>>(ids, n, lanes, vocab, order, sorted_id);
-        return launched("zb_embedding_sort");
+        return launched("zb_embedding_sort", launch_after(zb_embedding_rank_kernel, 1, (n * lanes + 31) / 32 * 32, 0, stream,
+                                                          ids, n, lanes, vocab, order, sorted_id));
     }
     int bits = 1;
     while (vocab >> bits) ++bits;
@@ -639,8 +612,7 @@ extern "C" zb_status zb_embedding_sort(const zb_embedding* e, const int32_t* ids
             err = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (err != cudaSuccess)
             return zb::fail(ZB_ERR_CUDA, std::string("zb_embedding_sort: cudaFuncSetAttribute: ") + cudaGetErrorString(err));
-        kern<<<blocks, SORT_THREADS, sort_smem(a.bits), st>>>(a);
-        return launched("zb_embedding_sort");
+        return launched("zb_embedding_sort", launch_after(kern, blocks, SORT_THREADS, sort_smem(a.bits), stream, a));
     };
     return n > SORT_LONG ? go(zb_embedding_sort_kernel<16>, 16) : go(zb_embedding_sort_kernel<8>, 8);
 }
@@ -678,7 +650,7 @@ extern "C" zb_status zb_embedding_backward(const zb_embedding* e, const int32_t*
     if (blocks > 0x7fffffffLL || joins > 0x7fffffffLL)
         return zb::fail(ZB_ERR_SHAPE, "zb_embedding_backward: too many elements");
     if (blocks == 0) return done();
-    auto go = [&](auto kern) { return launch_after(kern, blocks, GRAD_THREADS, stream, a); };
+    auto go = [&](auto kern) { return launch_after(kern, blocks, GRAD_THREADS, 0, stream, a); };
     cudaError_t err;
     if (e->dtype == ZB_DT_BF16)
         err = accumulate ? go(zb_embedding_backward_kernel<__nv_bfloat16, true>)
@@ -686,8 +658,6 @@ extern "C" zb_status zb_embedding_backward(const zb_embedding* e, const int32_t*
     else
         err = accumulate ? go(zb_embedding_backward_kernel<float, true>) : go(zb_embedding_backward_kernel<float, false>);
     if (err == cudaSuccess && joins > 0)
-        err = launch_after(zb_embedding_join_kernel, joins, JOIN_COLS * JOIN_PIECES, stream, a, join_cols);
-    if (err != cudaSuccess)
-        return zb::fail(ZB_ERR_CUDA, std::string("zb_embedding_backward launch: ") + cudaGetErrorString(err));
-    return launched("zb_embedding_backward");
+        err = launch_after(zb_embedding_join_kernel, joins, JOIN_COLS * JOIN_PIECES, 0, stream, a, join_cols);
+    return launched("zb_embedding_backward", err);
 }

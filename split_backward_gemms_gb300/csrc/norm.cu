@@ -10,8 +10,8 @@
 #include <cmath>
 #include <string>
 
+#include "launch.cuh"
 #include "ptx.cuh"
-#include "zb_internal.h"
 
 namespace {
 
@@ -134,6 +134,8 @@ __global__ void __launch_bounds__(Team<G>::THREADS)
     __shared__ float part[2][Team<G>::ROWS][G][1];
     const int team = threadIdx.x / (32 * G), at = threadIdx.x % (32 * G);
     const long long row = static_cast<long long>(blockIdx.x) * Team<G>::ROWS + team;
+    zbp::grid_dependency_wait();
+    zbp::allow_dependent_launch();
     if (row >= rows) return;
     const int nv = width / 8;
     Raw8<T> x[V];
@@ -193,6 +195,8 @@ __global__ void __launch_bounds__(Team<G>::THREADS)
     __shared__ float part[Team<G>::ROWS][G][2];
     const int team = threadIdx.x / (32 * G), at = threadIdx.x % (32 * G);
     const long long row = static_cast<long long>(blockIdx.x) * Team<G>::ROWS + team;
+    zbp::grid_dependency_wait();
+    zbp::allow_dependent_launch();
     if (row >= rows) return;
     const int nv = width / 8;
     Raw8<T> x[V], r[V];
@@ -260,6 +264,8 @@ __global__ void __cluster_dims__(W_SPLIT, 1, 1) __launch_bounds__(W_THREADS)
     const int t = threadIdx.x, lane = t & 31, w = t >> 5;
     const int c0 = (blockIdx.x / W_SPLIT) * vecs * 8, col = c0 + (t & (vecs - 1)) * 8;
     const int slots = W_THREADS / vecs;  // rows of a block at a time
+    zbp::grid_dependency_wait();
+    zbp::allow_dependent_launch();
     f32x2 dg2[4] = {0, 0, 0, 0}, db2[4] = {0, 0, 0, 0};
     if (col < width) {
 #pragma unroll 4
@@ -325,9 +331,6 @@ __global__ void __cluster_dims__(W_SPLIT, 1, 1) __launch_bounds__(W_THREADS)
 }
 
 // ---------------------------------------------------------------- host side
-bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
-bool off4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
-
 zb_status check_norm(const char* who, const zb_layernorm* n) {
     const std::string w = who;
     if (!n) return zb::fail(ZB_ERR_INVALID_ARG, w + ": descriptor is NULL");
@@ -336,18 +339,6 @@ zb_status check_norm(const char* who, const zb_layernorm* n) {
     if (n->width % 8) return zb::fail(ZB_ERR_ALIGN, w + ": width must be a multiple of 8");
     if (n->dtype != ZB_DT_BF16 && n->dtype != ZB_DT_F32) return zb::fail(ZB_ERR_DTYPE, w + ": unknown dtype");
     if (!(n->eps > 0.0f) || std::isinf(n->eps)) return zb::fail(ZB_ERR_INVALID_ARG, w + ": eps must be positive");
-    return ZB_OK;
-}
-
-zb_status launched(const char* who) {
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return zb::fail(ZB_ERR_CUDA, std::string(who) + " launch: " + cudaGetErrorString(e));
-    zb::clear_error();
-    return ZB_OK;
-}
-
-zb_status done() {
-    zb::clear_error();
     return ZB_OK;
 }
 
@@ -412,12 +403,13 @@ extern "C" zb_status zb_layernorm_forward(const zb_layernorm* n, const void* X, 
         return zb::fail(ZB_ERR_INVALID_ARG, "zb_layernorm_forward: required pointer is NULL");
     if (off16(X) || off16(gamma) || off16(beta) || off16(Y) || off4(mean) || off4(rstd))
         return zb::fail(ZB_ERR_ALIGN, "zb_layernorm_forward: pointers must be 16-byte aligned (mean, rstd: 4)");
+    cudaError_t err = cudaSuccess;
     auto go = [&](auto zero) {
         using T = decltype(zero);
         forward_by_width(n->width, [&](auto v, auto g) {
             constexpr int V = v(), G = g();
-            zb_layernorm_forward_kernel<T, V, G>
-                <<<blocks_of(n->rows, Team<G>::ROWS), Team<G>::THREADS, 0, static_cast<cudaStream_t>(stream)>>>(
+            err = launch_after(
+                zb_layernorm_forward_kernel<T, V, G>, blocks_of(n->rows, Team<G>::ROWS), Team<G>::THREADS, 0, stream,
                     static_cast<const T*>(X), static_cast<const __nv_bfloat16*>(gamma),
                     static_cast<const __nv_bfloat16*>(beta), static_cast<__nv_bfloat16*>(Y), mean, rstd, n->rows,
                     static_cast<int>(n->width), n->eps);
@@ -427,7 +419,7 @@ extern "C" zb_status zb_layernorm_forward(const zb_layernorm* n, const void* X, 
         go(__nv_bfloat16());
     else
         go(float());
-    return launched("zb_layernorm_forward");
+    return launched("zb_layernorm_forward", err);
 }
 
 extern "C" zb_status zb_layernorm_backward_input(const zb_layernorm* n, const void* dY, const void* X,
@@ -440,13 +432,14 @@ extern "C" zb_status zb_layernorm_backward_input(const zb_layernorm* n, const vo
         return zb::fail(ZB_ERR_INVALID_ARG, "zb_layernorm_backward_input: required pointer is NULL");
     if (off16(dY) || off16(X) || off16(gamma) || off4(mean) || off4(rstd) || off16(dR) || off16(dX) || off16(dX16))
         return zb::fail(ZB_ERR_ALIGN, "zb_layernorm_backward_input: pointers must be 16-byte aligned (mean, rstd: 4)");
+    cudaError_t err = cudaSuccess;
     auto go = [&](auto zero) {
         using T = decltype(zero);
         backward_by_width(n->width, [&](auto v, auto g) {
             constexpr int V = v(), G = g();
-            zb_layernorm_backward_input_kernel<T, V, G>
-                <<<blocks_of(n->rows, Team<G>::ROWS), Team<G>::THREADS, 0, static_cast<cudaStream_t>(stream)>>>(
-                    static_cast<const __nv_bfloat16*>(dY), static_cast<const T*>(X),
+            err = launch_after(
+                zb_layernorm_backward_input_kernel<T, V, G>, blocks_of(n->rows, Team<G>::ROWS), Team<G>::THREADS, 0,
+                stream, static_cast<const __nv_bfloat16*>(dY), static_cast<const T*>(X),
                     static_cast<const __nv_bfloat16*>(gamma), mean, rstd, static_cast<const T*>(dR),
                     static_cast<T*>(dX), static_cast<__nv_bfloat16*>(dX16), n->rows, static_cast<int>(n->width));
         });
@@ -455,7 +448,7 @@ extern "C" zb_status zb_layernorm_backward_input(const zb_layernorm* n, const vo
         go(__nv_bfloat16());
     else
         go(float());
-    return launched("zb_layernorm_backward_input");
+    return launched("zb_layernorm_backward_input", err);
 }
 
 extern "C" zb_status zb_layernorm_backward_weight(const zb_layernorm* n, const void* dY, const void* X,
@@ -470,15 +463,16 @@ extern "C" zb_status zb_layernorm_backward_weight(const zb_layernorm* n, const v
                         "zb_layernorm_backward_weight: dY and X must be 16-byte aligned (fp32 vectors: 4)");
     const int vecs = w_vecs(n->width);
     const unsigned blocks = blocks_of(n->width, vecs * 8) * W_SPLIT;
+    cudaError_t err = cudaSuccess;
     auto go = [&](auto zero) {
         using T = decltype(zero);
-        zb_layernorm_backward_weight_kernel<T><<<blocks, W_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(
-            static_cast<const __nv_bfloat16*>(dY), static_cast<const T*>(X), mean, rstd, dgamma, dbeta, n->rows,
+        err = launch_after(
+            zb_layernorm_backward_weight_kernel<T>, blocks, W_THREADS, 0, stream, static_cast<const __nv_bfloat16*>(dY), static_cast<const T*>(X), mean, rstd, dgamma, dbeta, n->rows,
             static_cast<int>(n->width), vecs, accumulate != 0);
     };
     if (n->dtype == ZB_DT_BF16)
         go(__nv_bfloat16());
     else
         go(float());
-    return launched("zb_layernorm_backward_weight");
+    return launched("zb_layernorm_backward_weight", err);
 }
