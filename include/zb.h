@@ -822,7 +822,11 @@ zb_status zb_embedding_forward(const zb_embedding* e, const int32_t* ids, const 
 
 /* The tokens in ascending order of (id, token), those with an id outside [0,
  * vocab) behind all others: order[i] is the i-th token, sorted_id[i] its id (-1
- * outside).  Workspace: zb_embedding_workspace_bytes, 256-byte aligned. */
+ * outside); neither may overlap ids.  Workspace: zb_embedding_workspace_bytes,
+ * 256-byte aligned, in use until the call's work on the stream has ended (calls or
+ * captured graphs that may run at once need one each; the sort and the gradient of
+ * the same tokens may share one).  ids, order and sorted_id are read from any
+ * 4-byte boundary. */
 size_t zb_embedding_workspace_bytes(const zb_embedding* e);
 zb_status zb_embedding_sort(const zb_embedding* e, const int32_t* ids, int32_t* order, int32_t* sorted_id,
                             void* workspace, size_t ws_bytes, void* stream);
