@@ -745,8 +745,10 @@ __global__ void __launch_bounds__(R_THREADS, 1)
     const int num_kb_all = (args.K + BK - 1) / BK;
     const int kb0 = static_cast<int>(static_cast<long long>(num_kb_all) * rank / split);
     const int num_kb = static_cast<int>(static_cast<long long>(num_kb_all) * (rank + 1) / split) - kb0;
-    // accumulators, and blocks of K in each
-    const int parts = min(PARTS, (num_kb + SEG - 1) / SEG), seg = (num_kb + parts - 1) / parts;
+    // blocks of K an accumulator takes, and the accumulators that so many fill (fewer than
+    // there are where a part of K is long: 129 blocks in 16 accumulators fill 15 of 9)
+    const int most = min(PARTS, (num_kb + SEG - 1) / SEG), seg = (num_kb + most - 1) / most;
+    const int parts = (num_kb + seg - 1) / seg;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) {

@@ -1,0 +1,77 @@
+"""fp32 products of a long K: what each accumulator holds, and in what order the
+sums are added.
+
+The operands stay on the GPU (some are hundreds of MB); the values they are compared
+with are computed there in 64 bits by plain products.  Element-wise bounds as in
+test_gpu_around.py: K products are off by at most K 2^-23 times the sum of the
+absolute products, and the norm of the error is a random walk, below 1e-6 of the
+norm of the result, whatever K, since an accumulator takes 512 products.
+"""
+
+import pytest
+import torch
+
+from tests.gpu_util import have_gpu, sync
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32, F64 = torch.bfloat16, torch.float32, torch.float64
+NAN = float("nan")
+
+
+@pytest.fixture(scope="module")
+def zb():
+    if not have_gpu():
+        pytest.skip("no CUDA device")
+    from split_backward_gemms_gb300 import build as B
+    B.build()
+    from split_backward_gemms_gb300 import zb as _zb
+    return _zb
+
+
+def normal(shape, seed, std=1.0, dtype=BF16):
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    return (torch.randn(shape, generator=gen, device="cuda", dtype=F32) * std).to(dtype)
+
+
+def product(X, W):
+    """X W and |X| |W| in 64 bits, by columns of W so that its copy stays small."""
+    D = torch.empty((X.shape[0], W.shape[1]), dtype=F64, device="cuda")
+    A = torch.empty_like(D)
+    x = X.to(F64)
+    for c in range(0, W.shape[1], 2048):
+        w = W[:, c:c + 2048].to(F64)
+        D[:, c:c + 2048], A[:, c:c + 2048] = x @ w, x.abs() @ w.abs()
+    return D, A
+
+
+def fp32_product(zb, X, W, transposed=False, bias=None, R=None):
+    N = W.shape[0] if transposed else W.shape[1]
+    out = torch.full((X.shape[0], N), NAN, dtype=F32, device="cuda")
+    zb.zb_linear_product(zb.make_linear(X.shape[0], N, X.shape[1], transposed=transposed, dtype=zb.ZB_DT_F32), X, W, bias,
+                         R, None, out, None)
+    return out
+
+
+def check_random(zb, M, N, K, transposed):
+    X, W = normal((M, K), M + K), normal((K, N), N, K ** -0.5)
+    out = fp32_product(zb, X, W.T.contiguous() if transposed else W, transposed)
+    sync(zb)
+    D, A = product(X, W)
+    off = (out.to(F64) - D).abs()
+    assert (off <= (K + 2) * 2.0 ** -23 * A).all()
+    assert torch.linalg.norm(off) <= 1e-6 * torch.linalg.norm(D)
+
+
+# blocks of 64 along K a CTA takes that 16 accumulators of equal length do not divide
+# evenly: 129, 145, 161 (one part of K), 129 (8 parts)
+@pytest.mark.parametrize("M,N,K", [(16, 16384, 8256), (5, 20488, 9280), (32, 16384, 10304), (16, 256, 66048)])
+@pytest.mark.parametrize("transposed", [False, True])
+def test_nothing_is_added_that_no_product_wrote(zb, M, N, K, transposed):
+    """Large sums left in every SM's tensor memory by the call before do not show."""
+    big = torch.full((32, 8192), 100.0, dtype=BF16, device="cuda")
+    wide = torch.full((8192, 19456), 100.0, dtype=BF16, device="cuda")  # a tile of 128 columns for each of 152 SMs
+    left = fp32_product(zb, big, wide)
+    check_random(zb, M, N, K, transposed)
+    assert (left == 8192 * 1e4).all()
