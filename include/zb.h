@@ -770,8 +770,7 @@ typedef struct zb_linear {
  * outputs otherwise overlap nothing that is read.  A bf16 output's sum runs over
  * all of K, or over up to 8 parts of it that are added in a fixed order (few
  * rows or few tiles); for fp32 outputs the partial sums of at most 512 products
- * (more only where few tiles meet a K of more than 16384) are added in fp32,
- * since one long accumulator loses low bits. */
+ * are added in fp32, since one long accumulator loses low bits. */
 zb_status zb_linear_product(const zb_linear* g, const void* X, const void* W, const void* bias,
                             const void* R, const void* H, void* out0, void* out1, void* stream);
 

@@ -653,9 +653,11 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
 // 16 x 1024, K 4096 takes 5.2 us in a graph of such calls, of which streaming the
 // weight is 1.3: the rest is the chain of launch, first loads, MMAs, exchange.
 //
-// fp32 outputs: an accumulator takes SEG blocks of K, as above; here each part has
-// tensor memory of its own (as far as it reaches: 512 columns / ROWS).
+// fp32 outputs: an accumulator takes at most SEG blocks of K, as above.  Tensor memory
+// holds 512 columns / ROWS of them; when all are full, the epilogue adds them to its
+// registers and they are filled again.
 constexpr int R_THREADS = NUM_THREADS;
+constexpr int R_EPI_WARPS = R_THREADS / 32 - 2;
 constexpr int R_STAGES = 10;
 constexpr int R_MIN_KB = 2;  // blocks of K a CTA, at least
 constexpr uint32_t R_SMEM = 120 * 1024;
@@ -663,7 +665,7 @@ constexpr uint32_t R_W_BYTES = 128 * BK * 2;
 constexpr uint32_t rows_stage(int rows) { return R_W_BYTES + static_cast<uint32_t>(rows) * BK * 2; }
 
 struct RowsCtl {
-    uint64_t full[R_STAGES], empty[R_STAGES], tfull, drain;
+    uint64_t full[R_STAGES], empty[R_STAGES], tfull, tempty, drain;
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -729,7 +731,8 @@ __global__ void __launch_bounds__(R_THREADS, 1)
     zb_linear_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                           const LinearArgs args) {
     constexpr uint32_t STAGE = rows_stage(ROWS);
-    constexpr int PARTS = FORM == STORE32 ? 512 / ROWS : 1;  // accumulators, at most
+    constexpr bool F32 = FORM == STORE32;
+    constexpr int PARTS = F32 ? 512 / ROWS : 1;  // accumulators
     constexpr uint32_t TMEM = PARTS * ROWS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -745,10 +748,7 @@ __global__ void __launch_bounds__(R_THREADS, 1)
     const int num_kb_all = (args.K + BK - 1) / BK;
     const int kb0 = static_cast<int>(static_cast<long long>(num_kb_all) * rank / split);
     const int num_kb = static_cast<int>(static_cast<long long>(num_kb_all) * (rank + 1) / split) - kb0;
-    // blocks of K an accumulator takes, and the accumulators that so many fill (fewer than
-    // there are where a part of K is long: 129 blocks in 16 accumulators fill 15 of 9)
-    const int most = min(PARTS, (num_kb + SEG - 1) / SEG), seg = (num_kb + most - 1) / most;
-    const int parts = (num_kb + seg - 1) / seg;
+    const int fills = F32 ? (num_kb + SEG - 1) / SEG : 1, seg = (num_kb + fills - 1) / fills;  // blocks of K a filling
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) {
@@ -756,6 +756,7 @@ __global__ void __launch_bounds__(R_THREADS, 1)
             zbp::mbar_init(zbp::smem_u32(&ctl->empty[s]), 1);
         }
         zbp::mbar_init(zbp::smem_u32(&ctl->tfull), 1);
+        zbp::mbar_init(zbp::smem_u32(&ctl->tempty), R_EPI_WARPS);
         zbp::mbar_init(zbp::smem_u32(&ctl->drain), 1);
         ctl->abort_flag = 0;
         zbp::fence_mbar_init();
@@ -819,27 +820,41 @@ __global__ void __launch_bounds__(R_THREADS, 1)
         constexpr uint32_t W_STEP = W_MN ? 2048 >> 4 : 32 >> 4, hi = zbp::desc_hi(1024);
         const uint32_t a0 = zbp::desc_lo(ring, W_MN ? MN_ATOM_BYTES : 16), b0 = zbp::desc_lo(ring + R_W_BYTES, 16);
         int s = 0;
-        uint32_t sp = 0, d_tmem = tmem_base;
-        int in_part = 0;
-        for (int kb = 0; kb < num_kb; ++kb) {
-            if (!wait_bar<false>(full0 + static_cast<uint32_t>(s) * 8u, sp, abort_flag, args.err, ERR_WAIT_MMA,
-                                WAIT_LIMIT_NS, true))
-                break;
-            zbp::tc_fence_after();
-            if (zbp::elect_one()) {
-                const uint32_t off = static_cast<uint32_t>(s) * (STAGE >> 4);
-                zbp::mma4_f16<W_STEP, 2>(d_tmem, a0 + off, hi, b0 + off, hi, idesc, in_part != 0);
-                zbp::tc_commit(empty0 + static_cast<uint32_t>(s) * 8u);
-                if (kb + 1 == num_kb) zbp::tc_commit(zbp::smem_u32(&ctl->tfull));
+        uint32_t sp = 0, turn = 0;  // turn: phase of the accumulators' next release
+        bool ok = true;
+        for (int lo = 0; lo < num_kb && ok; lo += PARTS * seg) {
+            if (F32 && lo) {
+                if (!wait_bar<false>(zbp::smem_u32(&ctl->tempty), turn, abort_flag, args.err, ERR_WAIT_MMA, WAIT_LIMIT_NS,
+                                    true))
+                    break;
+                zbp::tc_fence_after();
+                turn ^= 1u;
             }
-            __syncwarp();
-            if (++in_part == seg) {
-                in_part = 0;
-                d_tmem += ROWS;
-            }
-            if (++s == stages) {
-                s = 0;
-                sp ^= 1u;
+            const int given = min(num_kb, lo + PARTS * seg);  // the accumulators are then handed to the epilogue
+            uint32_t d_tmem = tmem_base;
+            int in_part = 0;
+            for (int kb = lo; kb < given; ++kb) {
+                if (!wait_bar<false>(full0 + static_cast<uint32_t>(s) * 8u, sp, abort_flag, args.err, ERR_WAIT_MMA,
+                                    WAIT_LIMIT_NS, true)) {
+                    ok = false;
+                    break;
+                }
+                zbp::tc_fence_after();
+                if (zbp::elect_one()) {
+                    const uint32_t off = static_cast<uint32_t>(s) * (STAGE >> 4);
+                    zbp::mma4_f16<W_STEP, 2>(d_tmem, a0 + off, hi, b0 + off, hi, idesc, in_part != 0);
+                    zbp::tc_commit(empty0 + static_cast<uint32_t>(s) * 8u);
+                    if (kb + 1 == given) zbp::tc_commit(zbp::smem_u32(&ctl->tfull));
+                }
+                __syncwarp();
+                if (++in_part == seg) {
+                    in_part = 0;
+                    d_tmem += ROWS;
+                }
+                if (++s == stages) {
+                    s = 0;
+                    sp ^= 1u;
+                }
             }
         }
         // every MMA issued here completes before TMEM is released
@@ -848,26 +863,49 @@ __global__ void __launch_bounds__(R_THREADS, 1)
         wait_bar<false>(zbp::smem_u32(&ctl->drain), 0, abort_flag, args.err, ERR_WAIT_MMA, DRAIN_LIMIT_NS, false);
     } else {
         // ---------------------------------------------------- partial tile to shared memory
+        constexpr int CHUNKS = ROWS > 64 ? 2 : 1;  // of 32 rows a warp: hf and hf + 2
         const int q = warp & 3, hf = (warp - 2) >> 2;
-        if (wait_bar<false>(zbp::smem_u32(&ctl->tfull), 0, abort_flag, args.err, ERR_WAIT_EPI, WAIT_LIMIT_NS, true)) {
-            zbp::tc_fence_after();
-            const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-#pragma unroll 1
-            for (int c = hf; c < ROWS / 32 && c * 32 < live; c += 2) {
-                float x[32];
-#pragma unroll 1
-                for (int p = 0; p < parts; ++p) {
-                    uint32_t v[32];
-                    zbp::tmem_ld_32x32b_x32(taddr + p * ROWS + c * 32, v);
-                    zbp::tmem_ld_wait();
+        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+        auto has = [&](int j) { return hf + 2 * j < ROWS / 32 && (hf + 2 * j) * 32 < live; };
+        float x[CHUNKS][32];
+        if constexpr (F32)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] = p == 0 ? __uint_as_float(v[i]) : x[i] + __uint_as_float(v[i]);
-                }
-                float* to = reinterpret_cast<float*>(smem) + c * 32 * 128 + q * 32 + lane;
+            for (int j = 0; j < CHUNKS; ++j)
 #pragma unroll
-                for (int i = 0; i < 32; ++i) to[i * 128] = x[i];
+                for (int i = 0; i < 32; ++i) x[j][i] = 0.0f;
+        uint32_t turn = 0;
+        bool ok = true;
+        for (int kb = 0; kb < num_kb; kb += PARTS * seg) {
+            if (!wait_bar<false>(zbp::smem_u32(&ctl->tfull), turn, abort_flag, args.err, ERR_WAIT_EPI, WAIT_LIMIT_NS, true)) {
+                ok = false;
+                break;
             }
+            turn ^= 1u;
+            zbp::tc_fence_after();
+            const int parts = F32 ? min(PARTS, (num_kb - kb + seg - 1) / seg) : 1;  // full ones
+#pragma unroll
+            for (int j = 0; j < CHUNKS; ++j)
+                if (has(j))
+#pragma unroll 1
+                    for (int p = 0; p < parts; ++p) {
+                        uint32_t v[32];
+                        zbp::tmem_ld_32x32b_x32(taddr + static_cast<uint32_t>(p * ROWS + (hf + 2 * j) * 32), v);
+                        zbp::tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[j][i] = F32 ? x[j][i] + __uint_as_float(v[i]) : __uint_as_float(v[i]);
+                    }
             zbp::tc_fence_before();
+            __syncwarp();
+            if (F32 && lane == 0) zbp::mbar_arrive(zbp::smem_u32(&ctl->tempty));
+        }
+        if (ok) {  // every MMA has read its stages, which the partial tile takes the place of
+#pragma unroll
+            for (int j = 0; j < CHUNKS; ++j)
+                if (has(j)) {
+                    float* to = reinterpret_cast<float*>(smem) + (hf + 2 * j) * 32 * 128 + q * 32 + lane;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) to[i * 128] = x[j][i];
+                }
         }
         __syncwarp();
     }

@@ -75,3 +75,32 @@ def test_nothing_is_added_that_no_product_wrote(zb, M, N, K, transposed):
     left = fp32_product(zb, big, wide)
     check_random(zb, M, N, K, transposed)
     assert (left == 8192 * 1e4).all()
+
+
+# few rows and few tiles, whose kernel splits K among CTAs or not at all
+LONG = [(16, 16384, 16384), (32, 19456, 8704), (64, 16384, 8192), (64, 16384, 16384), (128, 8192, 8192), (512, 2048, 8192),
+        (512, 2048, 16384), (16, 1024, 65536)]
+
+
+@pytest.mark.parametrize("M,N,K", LONG)
+@pytest.mark.parametrize("transposed", [False, True])
+def test_long_k(zb, M, N, K, transposed):
+    check_random(zb, M, N, K, transposed)
+
+
+@pytest.mark.parametrize("M,N,K", LONG + [(2048, 4096, 8192)])
+@pytest.mark.parametrize("transposed", [False, True])
+def test_an_accumulator_takes_512_products(zb, M, N, K, transposed):
+    """2^31, K - 2 halves, -2^31: beside 2^31 an accumulator loses halves (at most the 511
+    that it takes; where its magnitude is cut to a step of 128 just below 2^31, it may
+    gain up to 127), but every other one is exact, and so are the fp32 sums of what is
+    left, multiples of 128 below 2^31 and of 256 above.  (Every CTA's part of K is a
+    multiple of 512 here.)"""
+    X, W = torch.ones((M, K), dtype=BF16, device="cuda"), torch.full((K, N), 0.5, dtype=BF16, device="cuda")
+    X[:, 0], X[:, -1] = 2.0 ** 16, 2.0 ** 16
+    W[0], W[-1] = 2.0 ** 15, -2.0 ** 15
+    out = fp32_product(zb, X, W.T.contiguous() if transposed else W, transposed)
+    sync(zb)
+    lost = (K - 2) / 2 - out
+    assert lost.min() >= -127 and lost.max() <= 511
+    assert (out == out[0, 0]).all()
