@@ -402,9 +402,11 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
             for (uint32_t k = 0; k < ring; ++k) ask();
         // this lane's 16-byte part k of its row in a box
         auto part = [&](uint32_t box, int k) { return box + static_cast<uint32_t>(lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4)); };
-        // fp32: the residual is what the sums start from, since it can be waited for while
-        // a tile's first MMAs run, but not between its last ones and the next tile's, whose
-        // two accumulators hold 16 blocks of K only.  Chunk c comes into box c mod 4.
+        // fp32: the residual is added just before the tile's last accumulator, while whose
+        // MMAs run; not after it, since the next tile's MMAs have but the other accumulator
+        // until this one is read (4096 x 4096, K 1024 42.5 us for 38.8); nor first, which
+        // would round every later sum at the residual's size and is no faster (41.2 and
+        // 41.0 on another box; 35.3 and 36.4 at K 512).  Chunk c comes into box c mod 4.
         uint32_t on_way = 0, phases = 0;  // a bit a box: asked for and not read; phase of its barrier
         auto ask32 = [&](int c, int row0, int n0) {
             const uint32_t b = static_cast<uint32_t>(c) % TILE_BOXES;
@@ -430,11 +432,15 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
             uint32_t buf = 0;
             if constexpr (T::F32) {
 #pragma unroll
-                for (int c = 0; c < CH; ++c) {
+                for (int c = 0; c < CH; ++c)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) acc[c][i] = 0.0f;
-                    if (!res || c >= chunks || !ok) continue;
-                    constexpr uint32_t B = TILE_BOXES;
+            }
+            auto add_residual = [&]() {
+                constexpr uint32_t B = TILE_BOXES;
+#pragma unroll
+                for (int c = 0; c < (T::F32 ? CH : 0); ++c) {
+                    if (c >= chunks || !ok) continue;
                     const uint32_t b = static_cast<uint32_t>(c) % B, box = stg0 + b * T_BOX;
                     if (!wait_bar<false>(rbar0 + b * 8u, (phases >> b) & 1u, abort_flag, args.err, ERR_WAIT_EPI,
                                         WAIT_LIMIT_NS, true)) {
@@ -446,19 +452,22 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const float4 r = zbp::ld_shared_v4(part(box, k));
-                        acc[c][4 * k] = r.x;
-                        acc[c][4 * k + 1] = r.y;
-                        acc[c][4 * k + 2] = r.z;
-                        acc[c][4 * k + 3] = r.w;
+                        acc[c][4 * k] += r.x;
+                        acc[c][4 * k + 1] += r.y;
+                        acc[c][4 * k + 2] += r.z;
+                        acc[c][4 * k + 3] += r.w;
                     }
                     zbp::fence_proxy_async_smem();  // every lane has read the box
                     __syncwarp();
                     if (c + static_cast<int>(B) < chunks) ask32(c + static_cast<int>(B), row0, n0);
                 }
-                if (!ok) break;
-            }
+            };
             // fp32 outputs add the accumulators' parts; the others have one, read piece by piece below
             for (int kb0 = 0; kb0 < num_kb; kb0 += T::F32 ? SEG : num_kb) {
+                if (T::F32 && res && kb0 + SEG >= num_kb) {
+                    add_residual();
+                    if (!ok) break;
+                }
                 buf = local & 1u;
                 const uint32_t tr = local >> 1;
                 ++local;

@@ -104,3 +104,26 @@ def test_an_accumulator_takes_512_products(zb, M, N, K, transposed):
     lost = (K - 2) / 2 - out
     assert lost.min() >= -127 and lost.max() <= 511
     assert (out == out[0, 0]).all()
+
+
+# the kernel for few rows or tiles (the first two), and the other one
+@pytest.mark.parametrize("M,N,K", [(48, 512, 8192), (300, 512, 8192), (2048, 2048, 8192), (2051, 2056, 8200), (2048, 2048, 512),
+                                   (2048, 2048, 1000)])
+@pytest.mark.parametrize("transposed", [False, True])
+def test_a_large_residual_is_rounded_three_times_at_most(zb, M, N, K, transposed):
+    """Sums of 512 products are 0.3 of a step of the residual, so each would be lost by
+    itself; together they are not.  Three roundings at the size of the result, whatever K."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(M + K)
+
+    def uniform(lo, hi, *shape):
+        return torch.rand(shape, generator=gen, device="cuda") * (hi - lo) + lo
+
+    X = uniform(0.5, 1.5, M, K).to(BF16)
+    W = (uniform(0.5, 1.5, K, N) * (0.3 * 2.0 ** -3 / 512)).to(BF16)
+    R, bias = uniform(2.0 ** 20, 2.0 ** 21, M, N), uniform(-0.05, 0.05, N).to(BF16)
+    out = fp32_product(zb, X, W.T.contiguous() if transposed else W, transposed, bias, R)
+    sync(zb)
+    D, A = product(X, W)
+    ref = D + bias.to(F64) + R.to(F64)
+    assert ((out.to(F64) - ref).abs() <= 3 * 2.0 ** -24 * ref.abs() + (K + 2) * 2.0 ** -23 * A).all()
