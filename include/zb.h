@@ -768,8 +768,8 @@ typedef struct zb_linear {
  * bf16 [M,N] (read by GELU_GRAD alone).  Everything is added in fp32, and rounded
  * to the output's type once; of an fp32 output's additions at most three (the
  * residual, the last partial sum, the bias) are at the residual's size, however
- * long K is.  The output may be R itself (the same address and stride);
- * outputs otherwise overlap nothing that is read.  A bf16 output's sum runs over
+ * long K is.  An output (one of GELU's two) may be R itself, the same address and
+ * stride; outputs otherwise overlap nothing that is read, nor each other.  A bf16 output's sum runs over
  * all of K, or over up to 8 parts of it that are added in a fixed order (few
  * rows or few tiles); for fp32 outputs the partial sums of at most 512 products
  * are added in fp32, since one long accumulator loses low bits. */

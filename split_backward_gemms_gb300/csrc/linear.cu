@@ -694,6 +694,19 @@ __device__ __forceinline__ void finish4(const LinearArgs& a, long long row, int 
         *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p) + at) =
             make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
     };
+    // the residual before anything is stored: an output may take its place
+    float r[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (FORM == STORE32) {
+        if (a.R) {
+            const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(a.R) + row * a.ldr + col);
+            r[0] = f.x;
+            r[1] = f.y;
+            r[2] = f.z;
+            r[3] = f.w;
+        }
+    } else if (a.R) {
+        four(static_cast<const __nv_bfloat16*>(a.R) + row * a.ldr + col, r);
+    }
     if (FORM != GRAD && a.bias) {
         float b[4];
         four(a.bias + col, b);
@@ -715,24 +728,13 @@ __device__ __forceinline__ void finish4(const LinearArgs& a, long long row, int 
         else
             gelu_grad_values<false, 4>(x, h);
     }
-    if (FORM == STORE32) {
-        if (a.R) {
-            const float4 r = *reinterpret_cast<const float4*>(static_cast<const float*>(a.R) + row * a.ldr + col);
-            x[0] += r.x;
-            x[1] += r.y;
-            x[2] += r.z;
-            x[3] += r.w;
-        }
-        *reinterpret_cast<float4*>(static_cast<float*>(a.out0) + row * a.ldo + col) = make_float4(x[0], x[1], x[2], x[3]);
-    } else {
-        if (a.R) {
-            float r[4];
-            four(static_cast<const __nv_bfloat16*>(a.R) + row * a.ldr + col, r);
+    if (a.R)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] += r[i];
-        }
+        for (int i = 0; i < 4; ++i) x[i] += r[i];
+    if (FORM == STORE32)
+        *reinterpret_cast<float4*>(static_cast<float*>(a.out0) + row * a.ldo + col) = make_float4(x[0], x[1], x[2], x[3]);
+    else
         put(FORM == GELU ? a.out1 : a.out0, row * a.ldo + col, x);
-    }
 }
 
 template <int FORM, int W_MN, int ROWS>
