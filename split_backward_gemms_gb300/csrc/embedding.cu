@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <string>
 
 #include "launch.cuh"
@@ -530,6 +531,37 @@ zb_status check_embedding(const char* who, const zb_embedding* e) {
     return ZB_OK;
 }
 
+// Blocks of the sort's cluster: 16 from SORT_LONG tokens on where the device can hold a
+// cluster of 16 (more than the 8 that any device can), which is asked once a device.
+int sort_blocks(int tokens) {
+    static std::atomic<int> long_ok[64];  // 1: yes, -1: no
+    int dev = 0;
+    if (tokens <= SORT_LONG || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 8;
+    int ok = long_ok[dev].load(std::memory_order_relaxed);
+    if (!ok) {
+        auto kern = zb_embedding_sort_kernel<16>;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(16);
+        cfg.blockDim = dim3(SORT_THREADS);
+        cfg.dynamicSmemBytes = sort_smem(SORT_BITS);
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 16;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int clusters = 0;
+        const bool fits = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(sort_smem(SORT_BITS))) == cudaSuccess &&
+                          cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                          cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) == cudaSuccess && clusters > 0;
+        if (!fits) cudaGetLastError();
+        ok = fits ? 1 : -1;
+        long_ok[dev].store(ok, std::memory_order_relaxed);
+    }
+    return ok > 0 ? 16 : 8;
+}
+
 size_t sort_bytes(const zb_embedding& e) { return e.tokens > RANK_TOKENS ? 16 * static_cast<size_t>(e.tokens) : 0; }
 size_t pieces_of(const zb_embedding& e) { return (static_cast<size_t>(e.tokens) + PIECE - 1) / PIECE; }
 
@@ -605,16 +637,17 @@ extern "C" zb_status zb_embedding_sort(const zb_embedding* e, const int32_t* ids
     for (int i = 0; i < 2; ++i) a.pairs[i] = static_cast<uint2*>(workspace) + static_cast<size_t>(i) * n;
     a.order = order;
     a.sorted_id = sorted_id;
-    auto go = [&](auto kern, int blocks) {
-        cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(sort_smem(SORT_BITS)));
-        if (err == cudaSuccess && blocks > 8)
-            err = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    const int blocks = sort_blocks(n);
+    auto go = [&](auto kern) {
+        // (a cluster of 16 has got its attributes from sort_blocks)
+        const cudaError_t err = blocks > 8 ? cudaSuccess
+                                           : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                                  static_cast<int>(sort_smem(SORT_BITS)));
         if (err != cudaSuccess)
             return zb::fail(ZB_ERR_CUDA, std::string("zb_embedding_sort: cudaFuncSetAttribute: ") + cudaGetErrorString(err));
         return launched("zb_embedding_sort", launch_after(kern, blocks, SORT_THREADS, sort_smem(a.bits), stream, a));
     };
-    return n > SORT_LONG ? go(zb_embedding_sort_kernel<16>, 16) : go(zb_embedding_sort_kernel<8>, 8);
+    return blocks > 8 ? go(zb_embedding_sort_kernel<16>) : go(zb_embedding_sort_kernel<8>);
 }
 
 extern "C" zb_status zb_embedding_backward(const zb_embedding* e, const int32_t* order, const int32_t* sorted_id,
