@@ -32,10 +32,11 @@
  *    waiting.  A device-side wait that gives up (bounded spin in the GEMM
  *    pipeline) sets a device error word; it is reported as ZB_ERR_TIMEOUT by
  *    zb_sync_status().  Launch failures are reported as ZB_ERR_CUDA at once.
- *    A GEMM that follows another of this library's GEMMs on the same stream
- *    may start its setup before that one ends (programmatic dependent
- *    launch); it touches no memory until every earlier work item of the
- *    stream has completed, so stream order holds as usual.  One exception:
+ *    A kernel of this library that follows another one on the same stream
+ *    (products, norm, embedding, routing) may start its setup before that
+ *    one ends (programmatic dependent launch); it touches no memory until
+ *    every earlier work item of the stream has completed, so stream order
+ *    holds as usual.  One exception:
  *    zb_backward_weight's dW1 and dW2 GEMMs run at once (one grouped
  *    launch, or the second launched beside the first), since neither reads
  *    or writes what the other writes; when the caller's buffers overlap

@@ -16,7 +16,7 @@ bool off4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 
 // Launches a kernel that waits for the one before it in the stream by itself
 // (grid_dependency_wait before its first access to global memory), so that its blocks
-// may be set up while that one's last blocks run.
+// may be set up while that one's last blocks run (unless ZB_GEMM_PDL=0 says no).
 template <typename K, typename... Args>
 cudaError_t launch_after(K kern, long long blocks, int threads, size_t smem, void* stream, const Args&... args) {
     cudaLaunchConfig_t cfg = {};
@@ -26,7 +26,7 @@ cudaError_t launch_after(K kern, long long blocks, int threads, size_t smem, voi
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
+    attr.val.programmaticStreamSerializationAllowed = zb::dependent_launches();
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, args...);

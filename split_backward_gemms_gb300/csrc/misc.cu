@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cstdlib>
 #include <mutex>
 
 #include "ptx.cuh"
@@ -327,6 +328,14 @@ __global__ void __launch_bounds__(STATS_THREADS)
 }  // namespace
 
 namespace zb {
+
+bool dependent_launches() {
+    static const bool on = [] {
+        const char* v = std::getenv("ZB_GEMM_PDL");
+        return !(v && v[0] == '0');
+    }();
+    return on;
+}
 
 unsigned int* device_error_word() {
     static std::mutex mu;

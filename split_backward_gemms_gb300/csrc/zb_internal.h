@@ -15,6 +15,10 @@ namespace zb {
 zb_status fail(zb_status st, const std::string& msg);  // sets zb_last_error, returns st
 void clear_error();
 
+// Whether kernels may be launched as programmatic dependents of the one before them in
+// the stream (ZB_GEMM_PDL=0 in the environment: never).
+bool dependent_launches();
+
 // Device error word of the current device (bit set by a bounded wait that
 // gave up).  Returns nullptr with a message on CUDA failure.
 unsigned int* device_error_word();

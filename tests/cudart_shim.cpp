@@ -67,6 +67,8 @@ extern "C" cudaError_t cudaFuncSetAttribute(const void* f, cudaFuncAttribute a, 
     return fake() ? cudaSuccess : REAL(cudaFuncSetAttribute)(f, a, v);
 }
 
+extern "C" cudaError_t cudaGetLastError() { return fake() ? cudaSuccess : REAL(cudaGetLastError)(); }
+
 extern "C" cudaError_t cudaGetDevice(int* dev) {
     if (!fake()) return REAL(cudaGetDevice)(dev);
     *dev = 0;

@@ -24,3 +24,27 @@ for tokens in (300, 8192, 8193, 200000):
 @pytest.mark.parametrize("most,blocks", [(16, [8, 8, 16, 16]), (8, [8, 8, 8, 8])])
 def test_sort_takes_clusters_that_can_be_resident(folder, most, blocks):
     assert [n[0] for n in cudart_shim.run(folder, SORT, SHIM_CLUSTERS=str(most))] == blocks
+
+
+CALLS = f"""
+from split_backward_gemms_gb300 import zb
+n = zb.make_layernorm(64, 512)
+zb.zb_layernorm_forward(n, {P}, {P}, {P}, {P}, {P}, {P}, stream=0)
+zb.zb_layernorm_backward_input(n, {P}, {P}, {P}, {P}, {P}, {P}, {P}, None, stream=0)
+zb.zb_layernorm_backward_weight(n, {P}, {P}, {P}, {P}, {P}, {P}, 0, stream=0)
+for tokens in (100, 3000, 9000):
+    e = zb.make_embedding(tokens, 1000, 64)
+    zb.zb_embedding_forward(e, {P}, {P}, {P}, stream=0)
+    zb.zb_embedding_sort(e, {P}, {P}, {P}, {P}, 1 << 40, stream=0)
+    zb.zb_embedding_backward(e, {P}, {P}, {P}, {P}, 0, {P}, 1 << 40, stream=0)
+for M in (16, 2000):
+    zb.zb_linear_product(zb.make_linear(M, 2048, 512), {P}, {P}, {P}, {P}, None, {P}, None, stream=0)
+zb.zb_moe_forward(zb.make_moe(64, 128, 256, 4), {P}, {P}, {P}, {P}, {P}, {P}, {P}, {P}, {P}, stream=0)
+"""
+
+
+@pytest.mark.parametrize("env,programmatic", [({}, 1), ({"ZB_GEMM_PDL": "1"}, 1), ({"ZB_GEMM_PDL": "0"}, 0)])
+def test_programmatic_launches_as_the_environment_says(folder, env, programmatic):
+    launches = cudart_shim.run(folder, CALLS, **env)
+    # norm 3; lookup, order, gradient and join each three times; linear 2; experts' two products
+    assert len(launches) == 3 + 12 + 2 + 2 and {n[3] for n in launches} == {programmatic}

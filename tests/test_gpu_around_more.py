@@ -60,3 +60,53 @@ def test_many_tokens_sorted_without_clusters_of_16(zb, tmp_path):
     for most, blocks in ((16, 16), (8, 8)):
         launches = cudart_shim.run(tmp_path, code, fake=False, SHIM_CLUSTERS=str(most))
         assert [n[:2] for n in launches] == [(blocks, 1024)] * len(SORTED)
+
+
+def _bits_child(out):
+    """Chains of the library's kernels, each reading what the one before it wrote."""
+    from split_backward_gemms_gb300 import zb
+    got = {}
+    for T, h, f, zdt, dt in ((40, 64, 256, zb.ZB_DT_F32, torch.float32), (2100, 512, 2048, zb.ZB_DT_BF16, torch.bfloat16)):
+        gen = torch.Generator(device="cuda")
+        gen.manual_seed(T)
+
+        def normal(*shape, dtype=torch.bfloat16):
+            return torch.randn(shape, generator=gen, device="cuda").to(dtype)
+
+        def empty(*shape, dtype=torch.bfloat16):
+            return torch.empty(shape, dtype=dtype, device="cuda")
+
+        e, n = zb.make_embedding(T, 700, h, zdt, scale=2.0), zb.make_layernorm(T, h, zdt)
+        ids, table, gamma, W1, W2 = i32(_ids(T, 700, "padded")), normal(700, h), normal(h), normal(h, f), normal(f, h)
+        R, R2, N, H, A, dN = empty(T, h, dtype=dt), empty(T, h, dtype=dt), empty(T, h), empty(T, f), empty(T, f), empty(T, h)
+        mean, rstd, dg, dE = (empty(*s, dtype=torch.float32) for s in ((T,), (T,), (h,), (700, h)))
+        order, sid = empty(T, dtype=torch.int32), empty(T, dtype=torch.int32)
+        dR, ws = empty(T, h, dtype=dt), empty(zb.zb_embedding_workspace_bytes(e), dtype=torch.uint8)
+        torch.cuda.synchronize()
+        zb.zb_embedding_forward(e, ids, table, R)
+        zb.zb_layernorm_forward(n, R, gamma, None, N, mean, rstd)
+        zb.zb_linear_product(zb.make_linear(T, f, h, epilogue=zb.ZB_LINEAR_GELU), N, W1, None, None, None, H, A)
+        zb.zb_linear_product(zb.make_linear(T, h, f, dtype=zdt), A, W2, None, R, None, R2, None)
+        zb.zb_linear_product(zb.make_linear(T, h, f, transposed=True), H, W1, None, None, None, dN, None)
+        zb.zb_layernorm_backward_input(n, dN, R2, gamma, mean, rstd, R, dR, None)
+        zb.zb_layernorm_backward_weight(n, dN, R2, mean, rstd, dg, None, 0)
+        zb.zb_embedding_sort(e, ids, order, sid, ws, ws.numel())
+        zb.zb_embedding_backward(e, order, sid, dR, dE, 0, ws, ws.numel())
+        sync(zb)
+        for name, t in dict(R2=R2, H=H, A=A, dR=dR, dg=dg, dE=dE, order=order).items():
+            got[f"{name}_{T}"] = t.cpu().view(torch.int16 if t.dtype == torch.bfloat16 else torch.int32).numpy()
+    np.savez(out, **got)
+
+
+def test_launch_modes_change_no_bits(zb, tmp_path):
+    """Programmatic launches, and the L2 priorities of the products' copies, on and off."""
+    res = []
+    for k, env in enumerate(({}, {"ZB_GEMM_PDL": "0"}, {"ZB_GEMM_L2_HINTS": "0"})):
+        out = str(tmp_path / f"{k}.npz")
+        launches = cudart_shim.run(tmp_path, f"import tests.test_gpu_around_more as t; t._bits_child({out!r})", fake=False,
+                                   **env)
+        assert {n[3] for n in launches} == {0 if "ZB_GEMM_PDL" in env else 1}
+        res.append(np.load(out))
+    for other in res[1:]:
+        for name in res[0].files:
+            assert np.array_equal(res[0][name], other[name]), (name, other)
