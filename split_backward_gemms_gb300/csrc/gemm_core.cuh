@@ -490,13 +490,17 @@ int sm_count() {
 // dY (37.7 MB) across the waves of the F1 and B1 GEMMs (DRAM reads 673 ->
 // 398 MB and 934 -> 815 MB per launch) and a group's 25 MB of A in the W
 // GEMMs.  ZB_GEMM_L2_HINTS=0 in the environment turns the hints off.
-void choose_l2_hints(const zb::GemmBf16& g, int cg, EpiArgs* ea) {
+bool l2_hints() {
     static const bool on = [] {
         const char* v = std::getenv("ZB_GEMM_L2_HINTS");
         return !(v && std::strcmp(v, "0") == 0);
     }();
+    return on;
+}
+
+void choose_l2_hints(const zb::GemmBf16& g, int cg, EpiArgs* ea) {
     ea->hint_a = ea->hint_b = ea->hint_out = 0;
-    if (!on) return;
+    if (!l2_hints()) return;
     constexpr double kKeep = 48e6;
     const long long group_rows = static_cast<long long>(Cfg<1>::GROUP_M) * BM * cg;
     const long long groups = (g.Mg + group_rows - 1) / group_rows;

@@ -26,6 +26,7 @@ struct LinearArgs {
     int M, N, K;
     int save, tanh_form;
     int hint_a, hint_b, hint_out;  // L2 priorities of the copies (choose_l2_hints)
+    int hint_once;                 // of H's and the residual's, which are read once
     int tile_n;                    // tiles kernel: columns of a tile, a multiple of 32
     int tiles_n, split;            // rows kernel: column tiles, CTAs along K
     int stages;                    // rows kernel: of the ring
@@ -333,7 +334,7 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
         const int ew = warp - T::FIRST, q = warp & 3, half = (tile_n / 2 + 31) / 32 * 32, c_lo = (ew >> 2) * half;
         const uint32_t stg0 = zbp::smem_u32(staging) + static_cast<uint32_t>(ew) * TILE_BOXES * T_BOX;
         const uint32_t rbar0 = zbp::smem_u32(&ctl->rbar[ew][0]);
-        const uint64_t pol_out = zbp::l2_policy(args.hint_out), pol_once = zbp::l2_policy(1);
+        const uint64_t pol_out = zbp::l2_policy(args.hint_out), pol_once = zbp::l2_policy(args.hint_once);
         const bool res = args.R != nullptr, save = FORM == GELU && args.save;
         // The boxes are a ring of chunks: one box a chunk, for the residual, which the
         // results leave from; or two where GELU keeps H, whose box comes first.  Without
@@ -1120,6 +1121,7 @@ zb_status product(const zb_linear& g, int64_t ldx, int64_t ldw, const void* X, c
     a.hint_a = ea.hint_a;
     a.hint_b = ea.hint_b;
     a.hint_out = ea.hint_out;
+    a.hint_once = l2_hints() ? 1 : 0;
     return launch_tiles<FORM, W_MN>(x, w, o, h, r, a, stream);
 }
 

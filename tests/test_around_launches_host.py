@@ -1,6 +1,8 @@
 """What the operators around the block ask of the CUDA runtime (no GPU: a stand-in
 takes the calls)."""
 
+import ctypes as C
+
 import pytest
 
 from tests import cudart_shim
@@ -48,3 +50,25 @@ def test_programmatic_launches_as_the_environment_says(folder, env, programmatic
     launches = cudart_shim.run(folder, CALLS, **env)
     # norm 3; lookup, order, gradient and join each three times; linear 2; experts' two products
     assert len(launches) == 3 + 12 + 2 + 2 and {n[3] for n in launches} == {programmatic}
+
+
+class LinearArgs(C.Structure):
+    """The last argument of the kernel for many rows (csrc/linear.cu)."""
+    _fields_ = [("pointers", C.c_void_p * 5), ("ld", C.c_int64 * 3), ("MNK", C.c_int32 * 3), ("save", C.c_int32),
+                ("tanh", C.c_int32), ("hint_a", C.c_int32), ("hint_b", C.c_int32), ("hint_out", C.c_int32),
+                ("hint_once", C.c_int32), ("tile_n", C.c_int32)]
+
+
+LINEAR = f"""
+from split_backward_gemms_gb300 import zb
+g = zb.make_linear(8192, 4096, 4096, transposed=True, epilogue=zb.ZB_LINEAR_GELU_GRAD)
+zb.zb_linear_product(g, {P}, {P}, None, {P}, {P}, {P}, None, stream=0)
+"""
+
+
+@pytest.mark.parametrize("env,once", [({}, 1), ({"ZB_GEMM_L2_HINTS": "0"}, 0)])
+def test_l2_priorities_of_linear_maps_as_the_environment_says(folder, env, once):
+    (launch,) = cudart_shim.run(folder, LINEAR, SHIM_ARG="5", SHIM_BYTES=str(C.sizeof(LinearArgs)), **env)
+    a = LinearArgs.from_buffer_copy(launch[4])
+    assert list(a.MNK) == [8192, 4096, 4096] and a.tile_n == 256 and a.hint_once == once
+    assert (a.hint_a, a.hint_b, a.hint_out) != (0, 0, 0) if once else (a.hint_a, a.hint_b, a.hint_out) == (0, 0, 0)
