@@ -7,8 +7,8 @@ import torch
 
 from oracle import around as oa
 from tests import cudart_shim
-from tests.gpu_util import f64, have_gpu, sync
-from tests.test_gpu_around import Linear, _ids, i32
+from tests.gpu_util import empty_f32, f64, have_gpu, sync
+from tests.test_gpu_around import BF16, E, F32, Linear, _ids, _norm_inputs, dev, i32, near
 
 pytestmark = pytest.mark.gpu
 
@@ -110,3 +110,32 @@ def test_launch_modes_change_no_bits(zb, tmp_path):
     for other in res[1:]:
         for name in res[0].files:
             assert np.array_equal(res[0][name], other[name]), (name, other)
+
+
+# rows that a thread of the norm's W adds one after the other: 9 to 47
+@pytest.mark.parametrize("rows,width", [(1000, 16392), (500, 32768), (3000, 8200), (2300, 12296), (4700, 4104), (9000, 264),
+                                        (4097, 2056)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_norm_weight_of_many_rows(zb, rows, width, dtype):
+    """A column's roundings: one for each row a thread adds, then the shuffles, warps and
+    blocks that hold the column; dgamma's terms have two of their own."""
+    rng, X, _, _ = _norm_inputs(rows, width, dtype, seed=2)
+    dY = dev(rng.normal(size=(rows, width)))
+    n = zb.make_layernorm(rows, width, zb.ZB_DT_BF16 if dtype == BF16 else zb.ZB_DT_F32)
+    m, r = oa.norm_stats(f64(X), n.eps)
+    mean, rstd = dev(m, F32), dev(r, F32)
+    old = dev(rng.normal(size=(2, width)), F32)
+    sums, more = empty_f32(2, width), old.clone()
+    zb.zb_layernorm_backward_weight(n, dY, X, mean, rstd, sums[0], sums[1], 0)
+    zb.zb_layernorm_backward_weight(n, dY, X, mean, rstd, more[0], more[1], 1)
+    sync(zb)
+    x, dy, m, r = f64(X), f64(dY), f64(mean), f64(rstd)
+    vecs = 4  # of 8 columns, that a cluster of 8 blocks of 512 threads takes
+    while width > 256 * vecs:
+        vecs *= 2
+    chain = -(-rows * vecs // 4096) + max(0, 5 - int(np.log2(vecs))) + 16 // max(1, vecs // 32) + 8
+    dg, db = oa.norm_backward_weight(dy, x, m, r)
+    size = (np.abs(dy) * np.abs((x - m[:, None]) * r[:, None])).sum(axis=0)
+    near(sums[0], dg, (chain + 2) * E * size)
+    near(sums[1], db, chain * E * np.abs(dy).sum(axis=0))
+    assert torch.equal(more, old + sums)
