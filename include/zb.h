@@ -779,7 +779,8 @@ zb_status zb_linear_product(const zb_linear* g, const void* X, const void* W, co
 
 /* Layer norm of rows of `width` values (a multiple of 8, at most 32768):
  *   mean = sum x / width,  rstd = (sum (x - mean)^2 / width + eps)^-1/2,
- *   y = gamma (x - mean) rstd + beta. */
+ *   y = gamma (x - mean) rstd + beta.
+ * Sums are fp32: values of 1e17 and more can overflow the sum of squares. */
 typedef struct zb_layernorm {
     int64_t rows;
     int64_t width;

@@ -6,7 +6,8 @@ Importing this module loads the library and fails loudly if it is missing;
 there is no CPU fallback.
 
 Pointers may be given as torch tensors (their ``data_ptr()``), plain ints or
-None.  ``stream`` may be a ``torch.cuda.Stream``, an int handle or None (the
+None.  Only the address is taken: rows are dense, or lie at the strides that the
+descriptor names, whatever a tensor's own strides are.  ``stream`` may be a ``torch.cuda.Stream``, an int handle or None (the
 current torch stream when torch's CUDA is initialised, else the legacy
 default stream).  A non-OK status raises ``ZBError`` carrying the status and
 ``zb_last_error()``.
