@@ -406,8 +406,8 @@ __global__ void __launch_bounds__(TileCfg<FORM>::THREADS, 1)
         // fp32: the residual is added just before the tile's last accumulator, while whose
         // MMAs run; not after it, since the next tile's MMAs have but the other accumulator
         // until this one is read (4096 x 4096, K 1024 42.5 us for 38.8); nor first, which
-        // would round every later sum at the residual's size and is no faster (41.2 and
-        // 41.0 on another box; 35.3 and 36.4 at K 512).  Chunk c comes into box c mod 4.
+        // would round every later sum at the residual's size (and saves 35.3 us for 36.4 at
+        // K 512, nothing at K 1024).  Chunk c comes into box c mod 4.
         uint32_t on_way = 0, phases = 0;  // a bit a box: asked for and not read; phase of its barrier
         auto ask32 = [&](int c, int row0, int n0) {
             const uint32_t b = static_cast<uint32_t>(c) % TILE_BOXES;
